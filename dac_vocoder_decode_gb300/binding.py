@@ -35,6 +35,13 @@ VOC_SNAKE_BETA = 1
 VOC_FLAG_CHECK_FINITE = 1
 VOC_FLAG_SYNC = 2
 VOC_FLAG_PROFILE = 4
+VOC_LM_BF16 = 0
+VOC_LM_F16 = 1
+VOC_LM_F32 = 2
+VOC_LM_RMS = 0
+VOC_LM_NONE = 1
+VOC_LM_GATED = 2
+VOC_LM_BLOCK = 64
 
 STATUS_NAMES = {0: "VOC_OK", -1: "VOC_INVALID_ARG", -2: "VOC_UNSUPPORTED", -3: "VOC_CUDA_ERROR",
                 -4: "VOC_OOM", -5: "VOC_WORKSPACE_TOO_SMALL", -6: "VOC_NONFINITE",
@@ -60,6 +67,8 @@ EXPORTED = [
     "vocoder_encoder_launches", "vocoder_encoder_profile_count", "vocoder_encoder_profile_entry",
     "vocoder_encoder_profile_impl_bytes",
     "vocoder_encoder_last_error", "vocoder_encoder_destroy",
+    "vocoder_lm_rows_fp8", "vocoder_lm_linear_fp8", "vocoder_lm_kv_append",
+    "vocoder_lm_attention_ws_bytes", "vocoder_lm_attention",
 ]
 
 
@@ -217,6 +226,19 @@ def load_library():
     lib.vocoder_encoder_last_error.argtypes = [P]
     lib.vocoder_encoder_destroy.restype = None
     lib.vocoder_encoder_destroy.argtypes = [P]
+    L, FL, U, Z = ctypes.c_longlong, ctypes.c_float, ctypes.c_uint, ctypes.c_size_t
+    lib.vocoder_lm_rows_fp8.restype = I
+    lib.vocoder_lm_rows_fp8.argtypes = [P, L, P, L, P, I, I, L, I, FL, P, L, P, L, P, P, U]
+    lib.vocoder_lm_linear_fp8.restype = I
+    lib.vocoder_lm_linear_fp8.argtypes = [P, L, P, P, L, P, P, I, I, I, P, L, I, P, U]
+    lib.vocoder_lm_kv_append.restype = I
+    lib.vocoder_lm_kv_append.argtypes = [P, P, P, P, I, I, I, P, L, L, P, L, L, I, P, L, I, P, P,
+                                         I, I, I, P, U]
+    lib.vocoder_lm_attention_ws_bytes.restype = Z
+    lib.vocoder_lm_attention_ws_bytes.argtypes = [I] * 7
+    lib.vocoder_lm_attention.restype = I
+    lib.vocoder_lm_attention.argtypes = [P, L, L, I, I, P, P, P, P, I, I, I, P, L, I, P, P, I, I,
+                                         I, I, FL, I, I, P, L, L, P, Z, P, U]
     _lib = lib
     return lib
 
@@ -731,3 +753,270 @@ class Encoder:
                                  device=audio.device)
         vocoder_encode(self.handle, audio.contiguous(), latent, ws, stream, flags)
         return latent
+
+
+# ------------------------------------------------------------------ 8-bit operators
+_LM_TYPES = None
+
+
+def _lm_types():
+    """torch dtype -> VOC_LM_* (torch is imported with the first call only)."""
+    global _LM_TYPES
+    if _LM_TYPES is None:
+        import torch
+        _LM_TYPES = {torch.bfloat16: VOC_LM_BF16, torch.float16: VOC_LM_F16,
+                     torch.float32: VOC_LM_F32}
+    return _LM_TYPES
+
+
+def _bad(msg: str):
+    return VocoderError(VOC_INVALID_ARG, msg)
+
+
+def _lm_on_device(device, *tensors):
+    """All operands live on the current CUDA device."""
+    import torch
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise _bad(f"tensors must be on the current CUDA device, got {device}")
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise _bad("tensors must be on one CUDA device")
+
+
+def _lm_stream(device, stream, *made):
+    """Raw stream; tensors `made` here are kept until the work on a stream of the caller's ends."""
+    import torch
+    current = torch.cuda.current_stream(device)
+    if stream is None:
+        return current.cuda_stream
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.cuda_stream != current.cuda_stream:
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rows_ok(t, name, rows, width):
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width or \
+            (t.stride(1) != 1 and width > 1):
+        raise _bad(f"{name} must be [{rows}, {width}] with contiguous rows, got "
+                   f"{tuple(t.shape)} with strides {tuple(t.stride())}")
+
+
+def _ld(t):
+    """Row stride; that of a single row may be anything and does not count."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+
+
+def rows_fp8(x, mode: int = VOC_LM_RMS, weight=None, residual=None, eps: float = 1e-6,
+             sum_out=None, out=None, scale=None, stream=None, flags: int = 0):
+    """Rows of x [rows, d] (VOC_LM_GATED: [rows, 2d]) to e4m3 with a scale per row (see
+    vocoder_lm_rows_fp8 in include/vocoder.h).  Returns (out, scale, sum): out float8_e4m3fn
+    [rows, d] (a new one has its row stride padded to 16, as linear_fp8 takes it), scale fp32
+    [rows], sum = x + residual in x's type, or None without a residual."""
+    import torch
+    types = _lm_types()
+    if x.dtype not in types or x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1):
+        raise _bad("x must be a 2-d bf16, f16 or f32 tensor with contiguous rows")
+    rows, d = x.shape
+    if mode == VOC_LM_GATED:
+        if d % 2:
+            raise _bad("gated rows need an even width")
+        d //= 2
+    made = []
+    if residual is not None:
+        _rows_ok(residual, "residual", rows, d)
+        if sum_out is None:
+            sum_out = torch.empty((rows, d), dtype=x.dtype, device=x.device)
+            made.append(sum_out)
+        else:
+            _rows_ok(sum_out, "sum_out", rows, d)
+        if residual.dtype != x.dtype or sum_out.dtype != x.dtype:
+            raise _bad("residual and sum_out must have x's type")
+    elif sum_out is not None:
+        raise _bad("sum_out without residual")
+    if weight is not None and (weight.dtype != x.dtype or weight.dim() != 1 or
+                               weight.shape[0] != d or (weight.stride(0) != 1 and d > 1)):
+        raise _bad("weight must be [d] in x's type")
+    if out is None:
+        out = torch.empty((rows, (d + 15) // 16 * 16), dtype=torch.float8_e4m3fn,
+                          device=x.device)
+        made.append(out)
+        if out.shape[1] != d:
+            out = out[:, :d]
+    else:
+        _rows_ok(out, "out", rows, d)
+        if out.dtype != torch.float8_e4m3fn:
+            raise _bad("out must be float8_e4m3fn")
+    if scale is None:
+        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+        made.append(scale)
+    elif scale.dtype != torch.float32 or scale.shape != (rows,) or not scale.is_contiguous():
+        raise _bad("scale must be contiguous fp32 [rows]")
+    _lm_on_device(x.device, residual, weight, sum_out, out, scale)
+    st = load_library().vocoder_lm_rows_fp8(
+        x.data_ptr(), _ld(x), _ptr(residual), 0 if residual is None else _ld(residual),
+        _ptr(weight), types[x.dtype], mode, rows, d, eps, _ptr(sum_out),
+        0 if sum_out is None else _ld(sum_out), out.data_ptr(), _ld(out), scale.data_ptr(),
+        _lm_stream(x.device, stream, *made), flags)
+    _check(st)
+    return out, scale, sum_out
+
+
+def linear_fp8(x, x_scale, w, w_scale, bias=None, out_dtype=None, out=None, stream=None,
+               flags: int = 0):
+    """x [M, K] and w [N, K] float8_e4m3fn (16-byte aligned, row strides multiples of 16) with fp32
+    scales [M] and [N], bias fp32 [N] -> [M, N] in out_dtype (bf16 by default; see
+    vocoder_lm_linear_fp8 in include/vocoder.h)."""
+    import torch
+    types = _lm_types()
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    if x.dim() != 2 or w.dim() != 2 or x.dtype != f8 or w.dtype != f8:
+        raise _bad("x and w must be 2-d float8_e4m3fn tensors")
+    (M, K), N = x.shape, w.shape[0]
+    if w.shape[1] != K or (K > 1 and (x.stride(1) != 1 or w.stride(1) != 1)):
+        raise _bad("x [M, K] and w [N, K] must have one K and contiguous rows")
+    if x_scale.dtype != f32 or x_scale.shape != (M,) or not x_scale.is_contiguous() or \
+            w_scale.dtype != f32 or w_scale.shape != (N,) or not w_scale.is_contiguous():
+        raise _bad("x_scale [M] and w_scale [N] must be contiguous fp32")
+    if bias is not None and (bias.dtype != f32 or bias.shape != (N,) or
+                             not bias.is_contiguous()):
+        raise _bad("bias must be contiguous fp32 [N]")
+    made = ()
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=x.device)
+        made = (out,)
+    else:
+        _rows_ok(out, "out", M, N)
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise _bad("out has another type than out_dtype")
+    if out.dtype not in types:
+        raise _bad("the output is bf16, f16 or f32")
+    _lm_on_device(x.device, x_scale, w, w_scale, bias, out)
+    up16 = lambda t: t.stride(0) if t.shape[0] > 1 else (max(K, t.stride(0)) + 15) // 16 * 16  # noqa: E731
+    st = load_library().vocoder_lm_linear_fp8(
+        x.data_ptr(), up16(x), x_scale.data_ptr(), w.data_ptr(), up16(w), w_scale.data_ptr(),
+        _ptr(bias), M, N, K, out.data_ptr(), _ld(out), types[out.dtype],
+        _lm_stream(x.device, stream, *made), flags)
+    _check(st)
+    return out
+
+
+class KVCacheFP8:
+    """A pool of 64-token blocks of e4m3 keys and values: k [pages, kv_heads, 64, d] and v [pages,
+    kv_heads, d, 64] float8_e4m3fn, k_scale and v_scale fp32 [pages, kv_heads] (see the cache in
+    include/vocoder.h)."""
+    __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "kv_heads", "head_dim")
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        f8, f32 = torch.float8_e4m3fn, torch.float32
+        if k.dim() != 4 or k.shape[2] != VOC_LM_BLOCK:
+            raise _bad("k must be [pages, kv_heads, 64, head_dim]")
+        self.pages, self.kv_heads, _, self.head_dim = k.shape
+        if v.shape != (self.pages, self.kv_heads, self.head_dim, VOC_LM_BLOCK):
+            raise _bad("v must be [pages, kv_heads, head_dim, 64]")
+        if k_scale.shape != k.shape[:2] or v_scale.shape != k.shape[:2]:
+            raise _bad("scales must be [pages, kv_heads]")
+        if k.dtype != f8 or v.dtype != f8 or k_scale.dtype != f32 or v_scale.dtype != f32:
+            raise _bad("the cache holds float8_e4m3fn codes and fp32 scales")
+        if not (k.is_contiguous() and v.is_contiguous() and k_scale.is_contiguous() and
+                v_scale.is_contiguous()):
+            raise _bad("cache tensors must be contiguous")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+
+    @classmethod
+    def empty(cls, pages: int, kv_heads: int, head_dim: int, device="cuda"):
+        """A new pool.  Blocks are written whole when their first token is appended."""
+        import torch
+        mk = lambda *s: torch.zeros(s, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)  # noqa: E731
+        sc = lambda: torch.zeros((pages, kv_heads), dtype=torch.float32, device=device)  # noqa: E731
+        return cls(mk(pages, kv_heads, VOC_LM_BLOCK, head_dim),
+                   mk(pages, kv_heads, head_dim, VOC_LM_BLOCK), sc(), sc())
+
+
+def _batch_ok(page_table, kv_lens, cu_q):
+    import torch
+    i32 = torch.int32
+    if page_table.dtype != i32 or page_table.dim() != 2 or \
+            (page_table.stride(1) != 1 and page_table.shape[1] > 1):
+        raise _bad("page_table must be int32 [sequences, blocks] with contiguous rows")
+    n = page_table.shape[0]
+    if kv_lens.dtype != i32 or kv_lens.shape != (n,) or not kv_lens.is_contiguous():
+        raise _bad("kv_lens must be contiguous int32 [sequences]")
+    if cu_q is not None and (cu_q.dtype != i32 or cu_q.shape != (n + 1,) or
+                             not cu_q.is_contiguous()):
+        raise _bad("cu_q must be contiguous int32 [sequences + 1]")
+    return n
+
+
+def kv_append_fp8(cache: KVCacheFP8, k, v, page_table, kv_lens, cu_q=None, max_q: int = 1,
+                  stream=None, flags: int = 0) -> None:
+    """Store k and v [tokens, kv_heads, head_dim] (bf16 or f16) of new tokens in the cache (see
+    vocoder_lm_kv_append in include/vocoder.h).  page_table int32 [sequences, blocks], kv_lens
+    int32 [sequences] with the new tokens counted, cu_q int32 [sequences + 1] or None when every
+    sequence has max_q new tokens."""
+    types = _lm_types()
+    n = _batch_ok(page_table, kv_lens, cu_q)
+    shape = (k.shape[0], cache.kv_heads, cache.head_dim)
+    if k.shape != shape or v.shape != shape or k.dtype not in types or v.dtype != k.dtype or \
+            k.stride(2) != 1 or v.stride(2) != 1:
+        raise _bad("k and v must be [tokens, kv_heads, head_dim] of one type, head_dim contiguous")
+    _lm_on_device(k.device, v, page_table, kv_lens, cu_q, cache.k, cache.v, cache.k_scale,
+                  cache.v_scale)
+    st = load_library().vocoder_lm_kv_append(
+        cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
+        cache.v_scale.data_ptr(), cache.pages, cache.kv_heads, cache.head_dim, k.data_ptr(),
+        k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), types[k.dtype],
+        page_table.data_ptr(), _ld(page_table), page_table.shape[1], kv_lens.data_ptr(),
+        _ptr(cu_q), n, shape[0], max_q, _lm_stream(k.device, stream), flags)
+    _check(st)
+
+
+def attention_fp8(q, cache: KVCacheFP8, page_table, kv_lens, cu_q=None, max_q: int = 1,
+                  max_kv: Optional[int] = None, softmax_scale: Optional[float] = None,
+                  causal: bool = True, window: int = 0, out=None, ws=None, stream=None,
+                  flags: int = 0):
+    """Attention of the newest tokens' queries q [tokens, heads, head_dim] over the cache (see
+    vocoder_lm_attention in include/vocoder.h; the batch as in kv_append_fp8).  max_kv: at least
+    the largest kv_len (default: what the page table can hold); softmax_scale defaults to
+    1/sqrt(head_dim); ws: uint8 workspace of vocoder_lm_attention_ws_bytes (a new one if None)."""
+    import torch
+    types = _lm_types()
+    n = _batch_ok(page_table, kv_lens, cu_q)
+    if q.dim() != 3 or q.shape[2] != cache.head_dim or q.dtype not in types or q.stride(2) != 1:
+        raise _bad("q must be [tokens, heads, head_dim], head_dim contiguous")
+    tokens, heads, d = q.shape
+    made = []
+    if out is None:
+        out = torch.empty((tokens, heads, d), dtype=q.dtype, device=q.device)
+        made.append(out)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.stride(2) != 1:
+        raise _bad("out must have q's shape and type, head_dim contiguous")
+    if max_kv is None:
+        max_kv = page_table.shape[1] * VOC_LM_BLOCK
+    if softmax_scale is None:
+        softmax_scale = d ** -0.5
+    lib = load_library()
+    if ws is None:
+        need = lib.vocoder_lm_attention_ws_bytes(n, max_q, heads, cache.kv_heads, d, max_kv, window)
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+            made.append(ws)
+    _lm_on_device(q.device, out, page_table, kv_lens, cu_q, ws, cache.k, cache.v, cache.k_scale,
+                  cache.v_scale)
+    st = lib.vocoder_lm_attention(
+        q.data_ptr(), q.stride(0), q.stride(1), types[q.dtype], heads, cache.k.data_ptr(),
+        cache.v.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), cache.pages,
+        cache.kv_heads, d, page_table.data_ptr(), _ld(page_table), page_table.shape[1],
+        kv_lens.data_ptr(), _ptr(cu_q), n, tokens, max_q, max_kv, softmax_scale, int(causal),
+        window, out.data_ptr(), out.stride(0), out.stride(1), _ptr(ws),
+        0 if ws is None else ws.numel(), _lm_stream(q.device, stream, *made), flags)
+    _check(st)
+    return out

@@ -46,20 +46,32 @@ def build(force: bool = False, verbose: bool = False, extra=None) -> str:
         return LIB
     os.makedirs(LIBDIR, exist_ok=True)
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-shared",
-           "-Xcompiler", "-fPIC,-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC,
-           "-o", tmp, os.path.join(CSRC, "vocoder.cu")]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    if extra:
-        cmd[1:1] = list(extra)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("nvcc failed building libvocoder.so")
-    if verbose:
-        sys.stderr.write(res.stdout + res.stderr)
-    os.replace(tmp, LIB)
+    base = [nvcc(), *(extra or []), *(["-Xptxas=-v"] if verbose else []), *ARCH_FLAGS, "-O3",
+            "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden", "-I", INCLUDE,
+            "-I", CSRC]
+    # one object per source file, compiled side by side
+    units = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    objs = [f"{tmp}.{os.path.basename(u)}.o" for u in units]
+    try:
+        procs = [subprocess.Popen([*base, "-c", "-o", o, u], stdout=subprocess.PIPE,
+                                  stderr=subprocess.STDOUT, text=True)
+                 for u, o in zip(units, objs)]
+        logs = [p.communicate()[0] for p in procs]
+        failed = any(p.returncode for p in procs)
+        if not failed:
+            res = subprocess.run([nvcc(), *ARCH_FLAGS, "-shared", "-o", tmp, *objs],
+                                 capture_output=True, text=True)
+            logs.append(res.stdout + res.stderr)
+            failed = res.returncode != 0
+        if failed or verbose:
+            sys.stderr.write("".join(logs))
+        if failed:
+            raise RuntimeError("nvcc failed building libvocoder.so")
+        os.replace(tmp, LIB)
+    finally:
+        for f in [*objs, tmp]:
+            if os.path.exists(f):
+                os.remove(f)
     return LIB
 
 

@@ -1,0 +1,462 @@
+// lm_ops.cu -- C entry points of the 8-bit operators of a token model (vocoder_lm_* in
+// include/vocoder.h): argument checks, choice of tiles and splits, launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <mutex>
+#include <new>
+#include <string>
+
+#include "vocoder.h"
+#include "lm_attention.cuh"
+#include "lm_cache.cuh"
+#include "lm_linear.cuh"
+#include "lm_rows.cuh"
+
+#define VOC_API extern "C" __attribute__((visibility("default")))
+
+namespace voc {
+std::string &last_error_slot();  // vocoder.cu: the thread's error without a context
+}
+
+namespace {
+
+constexpr long long kWaitBudget = 4000000000LL;  // cycles (~2 s) before a wait gives up
+constexpr int kMaxDevices = 64;
+
+// Set by a kernel that gave up a wait; read and cleared by calls with VOC_FLAG_SYNC.
+__device__ int g_timeout;
+
+voc_status fail(voc_status st, const char *msg) noexcept {
+  try {
+    voc::last_error_slot() = msg;
+  } catch (...) {
+  }
+  return st;
+}
+voc_status cuda_fail(cudaError_t e, const char *what) noexcept {
+  try {
+    voc::last_error_slot() = std::string(what) + ": " + cudaGetErrorString(e);
+  } catch (...) {
+  }
+  return e == cudaErrorMemoryAllocation ? VOC_OOM : VOC_CUDA_ERROR;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+struct Device {
+  std::once_flag once;
+  cudaError_t err = cudaSuccess;
+  int sms = 0;
+  int *timeout = nullptr;
+};
+Device g_devices[kMaxDevices];
+
+template <typename K>
+void allow_smem(cudaError_t &e, K kernel, size_t bytes) {
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(bytes));
+}
+constexpr size_t kLinSmem = 220 * 1024;
+
+// The current device, set up on first use (shared-memory limits of the kernels, SM count).
+voc_status device(Device **out) {
+  int d = 0;
+  cudaError_t e = cudaGetDevice(&d);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (d >= kMaxDevices) return fail(VOC_UNSUPPORTED, "lm: device index");
+  Device &dev = g_devices[d];
+  std::call_once(dev.once, [&] {
+    using namespace voc;
+    cudaError_t &er = dev.err;
+    er = cudaDeviceGetAttribute(&dev.sms, cudaDevAttrMultiProcessorCount, d);
+    void *t = nullptr;
+    if (er == cudaSuccess) er = cudaGetSymbolAddress(&t, g_timeout);
+    dev.timeout = static_cast<int *>(t);
+    allow_smem(er, attn_rows_kernel<__half, 64>, attn_smem<64>());
+    allow_smem(er, attn_rows_kernel<__half, 128>, attn_smem<128>());
+    allow_smem(er, attn_rows_kernel<__nv_bfloat16, 64>, attn_smem<64>());
+    allow_smem(er, attn_rows_kernel<__nv_bfloat16, 128>, attn_smem<128>());
+    allow_smem(er, linear_few_kernel<float>, kLinSmem);
+    allow_smem(er, linear_few_kernel<__half>, kLinSmem);
+    allow_smem(er, linear_few_kernel<__nv_bfloat16>, kLinSmem);
+  });
+  if (dev.err != cudaSuccess) return cuda_fail(dev.err, "lm: device set-up");
+  *out = &dev;
+  return VOC_OK;
+}
+
+// Launch with programmatic stream serialization (see pdl_wait), in clusters of `cluster` CTAs
+// along z where that is above 1.
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, int cluster,
+                   voc_stream_t stream, const Args &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cluster > 1) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = cluster;
+    cfg.numAttrs = 2;
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// With VOC_FLAG_SYNC: wait for the stream and report a kernel that gave up a wait.
+voc_status finish(const Device &dev, voc_stream_t stream, unsigned flags) {
+  if (!(flags & VOC_FLAG_SYNC)) return VOC_OK;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int t = 0;
+  cudaError_t e = cudaMemcpyAsync(&t, dev.timeout, sizeof t, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return cuda_fail(e, "lm: synchronise");
+  if (t) {
+    e = cudaMemsetAsync(dev.timeout, 0, sizeof t, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return cuda_fail(e, "lm: synchronise");
+    return fail(VOC_DEVICE_TIMEOUT, "lm: a kernel gave up a wait");
+  }
+  return VOC_OK;
+}
+
+bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+bool known_flags(unsigned f) { return (f & ~static_cast<unsigned>(VOC_FLAG_SYNC)) == 0; }
+
+template <int MODE>
+cudaError_t launch_rows(int dtype, const voc::LmRowsArgs &a, voc_stream_t stream) {
+  const dim3 grid(static_cast<unsigned>(a.rows));
+  if (dtype == VOC_LM_F32)
+    return launch(voc::rows_any_kernel<float, MODE>, grid, dim3(256), 0, 1, stream, a);
+  if (dtype == VOC_LM_F16)
+    return launch(voc::rows_any_kernel<__half, MODE>, grid, dim3(256), 0, 1, stream, a);
+  return launch(voc::rows_any_kernel<__nv_bfloat16, MODE>, grid, dim3(256), 0, 1, stream, a);
+}
+
+}  // namespace
+
+VOC_API voc_status vocoder_lm_rows_fp8(const void *x, long long ldx, const void *residual,
+                                       long long ldr, const void *weight, int dtype, int mode,
+                                       long long rows, int d, float eps, void *sum_out,
+                                       long long lds, void *out8, long long ldo, float *scale,
+                                       voc_stream_t stream, unsigned flags) {
+  if (dtype != VOC_LM_BF16 && dtype != VOC_LM_F16 && dtype != VOC_LM_F32)
+    return fail(VOC_INVALID_ARG, "rows: dtype");
+  if (mode != VOC_LM_RMS && mode != VOC_LM_NONE && mode != VOC_LM_GATED)
+    return fail(VOC_INVALID_ARG, "rows: mode");
+  if (rows < 0 || rows > 0x7fffffffll || d < 1 || d > (1 << 24))
+    return fail(VOC_INVALID_ARG, "rows: sizes");
+  if (!known_flags(flags)) return fail(VOC_INVALID_ARG, "rows: flags");
+  if (mode == VOC_LM_RMS && !weight) return fail(VOC_INVALID_ARG, "rows: weight is NULL");
+  if (mode != VOC_LM_RMS && weight) return fail(VOC_INVALID_ARG, "rows: weight without RMS");
+  if (mode == VOC_LM_RMS && !(eps >= 0.f && std::isfinite(eps)))
+    return fail(VOC_INVALID_ARG, "rows: eps");
+  if (mode == VOC_LM_GATED && residual)
+    return fail(VOC_INVALID_ARG, "rows: residual with a gated product");
+  if ((sum_out != nullptr) && !residual)
+    return fail(VOC_INVALID_ARG, "rows: sum_out without residual");
+  const long long width = mode == VOC_LM_GATED ? 2ll * d : d;
+  if (ldx < width || ldo < d || (residual && ldr < d) || (sum_out && lds < d))
+    return fail(VOC_INVALID_ARG, "rows: a row stride is below the width");
+  if (rows > 0 && (!x || !out8 || !scale)) return fail(VOC_INVALID_ARG, "rows: NULL buffer");
+  const size_t e = dtype == VOC_LM_F32 ? 4 : 2;
+  if (!aligned(x, e) || !aligned(residual, e) || !aligned(weight, e) || !aligned(sum_out, e) ||
+      !aligned(scale, 4))
+    return fail(VOC_INVALID_ARG, "rows: a buffer is not aligned to its type");
+  Device *dev;
+  if (voc_status st = device(&dev); st != VOC_OK) return st;
+  if (rows == 0) return finish(*dev, stream, flags);
+  voc::LmRowsArgs a{x, residual, weight, sum_out, static_cast<uint8_t *>(out8), scale,
+                    rows, ldx, ldr, lds, ldo, d, eps};
+  cudaError_t err;
+  if (mode == VOC_LM_RMS)
+    err = launch_rows<voc::kRowsRms>(dtype, a, stream);
+  else if (mode == VOC_LM_NONE)
+    err = launch_rows<voc::kRowsNone>(dtype, a, stream);
+  else
+    err = launch_rows<voc::kRowsGated>(dtype, a, stream);
+  if (err != cudaSuccess) return cuda_fail(err, "launch rows");
+  return finish(*dev, stream, flags);
+}
+
+// ------------------------------------------------------------------ product
+namespace {
+
+// [rows][k] bytes with row stride ld, read in boxes of 128 bytes x `box` rows, 128-byte swizzle;
+// what lies outside reads as 0.
+voc_status encode_rows(CUtensorMap *map, const void *base, long long rows, long long k,
+                       long long ld, int box) {
+  auto enc = encode_fn();
+  if (!enc) return fail(VOC_CUDA_ERROR, "linear: cuTensorMapEncodeTiled entry point unavailable");
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+  const cuuint32_t b[2] = {128u, static_cast<cuuint32_t>(box)};
+  const cuuint32_t es[2] = {1u, 1u};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides,
+                   b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(VOC_CUDA_ERROR, "linear: cuTensorMapEncodeTiled failed");
+  return VOC_OK;
+}
+
+template <typename T>
+cudaError_t launch_few(const CUtensorMap &xm, const CUtensorMap &wm, const voc::LmLinearArgs &a,
+                       int split, voc_stream_t stream) {
+  const dim3 grid((a.N + voc::kLinRows - 1) / voc::kLinRows, (a.M + a.nt - 1) / a.nt, split);
+  return launch(voc::linear_few_kernel<T>, grid, dim3(voc::kLinThreads), kLinSmem, split, stream,
+                xm, wm, a);
+}
+
+}  // namespace
+
+VOC_API voc_status vocoder_lm_linear_fp8(const void *x8, long long ldx, const float *x_scale,
+                                         const void *w8, long long ldw, const float *w_scale,
+                                         const float *bias, int M, int N, int K, void *out,
+                                         long long ldo, int out_dtype, voc_stream_t stream,
+                                         unsigned flags) {
+  if (out_dtype != VOC_LM_BF16 && out_dtype != VOC_LM_F16 && out_dtype != VOC_LM_F32)
+    return fail(VOC_INVALID_ARG, "linear: out_dtype");
+  if (M < 0 || N < 0 || K < 1 || M > (1 << 28) || N > (1 << 28) || K > (1 << 28))
+    return fail(VOC_INVALID_ARG, "linear: sizes");
+  if (!known_flags(flags)) return fail(VOC_INVALID_ARG, "linear: flags");
+  if (ldx < K || ldw < K || ldo < N)
+    return fail(VOC_INVALID_ARG, "linear: a row stride is below the width");
+  if (ldx % 16 || ldw % 16)
+    return fail(VOC_INVALID_ARG, "linear: row strides of x8 and w8 must be multiples of 16");
+  if (M > 0 && N > 0 && (!x8 || !w8 || !x_scale || !w_scale || !out))
+    return fail(VOC_INVALID_ARG, "linear: NULL buffer");
+  if (!aligned(x8, 16) || !aligned(w8, 16))
+    return fail(VOC_INVALID_ARG, "linear: x8 and w8 must be 16-byte aligned");
+  if (!aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(bias, 4) ||
+      !aligned(out, out_dtype == VOC_LM_F32 ? 4 : 2))
+    return fail(VOC_INVALID_ARG, "linear: a buffer is not aligned to its type");
+  Device *dev;
+  if (voc_status st = device(&dev); st != VOC_OK) return st;
+  if (M == 0 || N == 0) return finish(*dev, stream, flags);
+  voc::LmLinearArgs a{};
+  a.xs = x_scale, a.ws = w_scale, a.bias = bias, a.out = out, a.ldo = ldo;
+  a.M = M, a.N = N, a.K = K;
+  a.budget = kWaitBudget;
+  a.timeout = dev->timeout;
+  a.chunks = (K + voc::kLinK - 1) / voc::kLinK;
+  a.nt = std::min(256, (M + 15) / 16 * 16);
+  if ((M + a.nt - 1) / a.nt > 65535) return fail(VOC_UNSUPPORTED, "linear: too many rows");
+  a.tmem_cols = 32;
+  while (a.tmem_cols < a.nt) a.tmem_cols *= 2;
+  const int stage = (voc::kLinRows + a.nt) * voc::kLinK;
+  a.stages = std::min<int>(12, (kLinSmem - 1024) / stage);
+  const int tiles = ((N + voc::kLinRows - 1) / voc::kLinRows) * ((M + a.nt - 1) / a.nt);
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= dev->sms && split * 2 <= a.chunks) split *= 2;
+  CUtensorMap xm, wm;
+  if (voc_status st = encode_rows(&xm, x8, M, K, ldx, a.nt); st != VOC_OK) return st;
+  if (voc_status st = encode_rows(&wm, w8, N, K, ldw, voc::kLinRows); st != VOC_OK) return st;
+  cudaError_t e;
+  if (out_dtype == VOC_LM_F32)
+    e = launch_few<float>(xm, wm, a, split, stream);
+  else if (out_dtype == VOC_LM_F16)
+    e = launch_few<__half>(xm, wm, a, split, stream);
+  else
+    e = launch_few<__nv_bfloat16>(xm, wm, a, split, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "launch linear");
+  return finish(*dev, stream, flags);
+}
+
+// ------------------------------------------------------------------ cache and attention
+namespace {
+
+// What append and attention ask of the cache and of the batch.
+voc_status check_cache(const void *kc, const void *vc, const float *ks, const float *vs,
+                       int n_pages, int kv_heads, int head_dim, int dtype, const int *table,
+                       long long ldt, int table_cols, const int *lens, const int *cu, int n_seq,
+                       int n_tokens, int max_q) {
+  if (dtype != VOC_LM_BF16 && dtype != VOC_LM_F16) return fail(VOC_INVALID_ARG, "cache: dtype");
+  if (head_dim != 64 && head_dim != 128)
+    return fail(VOC_UNSUPPORTED, "cache: head_dim must be 64 or 128");
+  if (n_pages < 1 || kv_heads < 1 || kv_heads > 4096 || table_cols < 1 || ldt < table_cols)
+    return fail(VOC_INVALID_ARG, "cache: sizes");
+  if (n_seq < 0 || n_seq > 65535 || n_tokens < 0 || max_q < 0)
+    return fail(VOC_INVALID_ARG, "cache: batch sizes");
+  if (n_seq == 0 && n_tokens > 0) return fail(VOC_INVALID_ARG, "cache: tokens without sequences");
+  if (n_seq > 0 && !cu && static_cast<long long>(n_seq) * max_q != n_tokens)
+    return fail(VOC_INVALID_ARG, "cache: without cu_q every sequence has max_q tokens");
+  if (max_q > n_tokens) return fail(VOC_INVALID_ARG, "cache: max_q above the number of tokens");
+  if (!kc || !vc || !ks || !vs || (n_seq > 0 && (!table || !lens)))
+    return fail(VOC_INVALID_ARG, "cache: NULL buffer");
+  if (!aligned(kc, 16) || !aligned(vc, 16) || !aligned(ks, 4) || !aligned(vs, 4) ||
+      !aligned(table, 4) || !aligned(lens, 4) || !aligned(cu, 4))
+    return fail(VOC_INVALID_ARG, "cache: alignment");
+  return VOC_OK;
+}
+
+}  // namespace
+
+VOC_API voc_status vocoder_lm_kv_append(void *k_cache, void *v_cache, float *k_scale,
+                                        float *v_scale, int n_pages, int kv_heads, int head_dim,
+                                        const void *k, long long ldk, long long hsk, const void *v,
+                                        long long ldv, long long hsv, int dtype,
+                                        const int *page_table, long long ldt, int table_cols,
+                                        const int *kv_lens, const int *cu_q, int n_seq,
+                                        int n_tokens, int max_q, voc_stream_t stream,
+                                        unsigned flags) {
+  if (voc_status st = check_cache(k_cache, v_cache, k_scale, v_scale, n_pages, kv_heads, head_dim,
+                                  dtype, page_table, ldt, table_cols, kv_lens, cu_q, n_seq,
+                                  n_tokens, max_q);
+      st != VOC_OK)
+    return st;
+  if (!known_flags(flags)) return fail(VOC_INVALID_ARG, "append: flags");
+  if (n_tokens > 0 && (!k || !v)) return fail(VOC_INVALID_ARG, "append: NULL buffer");
+  if (!aligned(k, 16) || !aligned(v, 16) || ldk % 8 || hsk % 8 || ldv % 8 || hsv % 8)
+    return fail(VOC_INVALID_ARG, "append: k and v must be 16-byte aligned, strides multiples of 8");
+  Device *dev;
+  if (voc_status st = device(&dev); st != VOC_OK) return st;
+  if (n_tokens == 0 || max_q == 0) return finish(*dev, stream, flags);
+  voc::LmAppendArgs a{static_cast<uint8_t *>(k_cache), static_cast<uint8_t *>(v_cache), k_scale,
+                      v_scale, k, v, ldk, hsk, ldv, hsv, page_table, kv_lens, cu_q, ldt, n_pages,
+                      table_cols, kv_heads, n_seq, n_tokens, max_q};
+  const dim3 grid((max_q - 1 + voc::kBlockTokens - 1) / voc::kBlockTokens + 1, kv_heads, n_seq);
+  cudaError_t e;
+  if (dtype == VOC_LM_F16)
+    e = head_dim == 64 ? launch(voc::append_kernel<__half, 64>, grid, dim3(256), 0, 1, stream, a)
+                       : launch(voc::append_kernel<__half, 128>, grid, dim3(256), 0, 1, stream, a);
+  else
+    e = head_dim == 64
+            ? launch(voc::append_kernel<__nv_bfloat16, 64>, grid, dim3(256), 0, 1, stream, a)
+            : launch(voc::append_kernel<__nv_bfloat16, 128>, grid, dim3(256), 0, 1, stream, a);
+  if (e != cudaSuccess) return cuda_fail(e, "launch append");
+  return finish(*dev, stream, flags);
+}
+
+namespace {
+
+struct AttnPlan {
+  int row_tiles = 0, splits = 1;
+  long long tiles = 0;
+  size_t ws_bytes = 0;
+};
+
+// How far a sequence's keys are split: enough parts to give every SM one when there are few
+// tiles of rows, each of at least 4 blocks (one round of a CTA's warps).
+AttnPlan plan_attention(int sms, int n_seq, int max_q, int heads, int kv_heads, int head_dim,
+                        int max_kv, int window) {
+  AttnPlan p;
+  const long long group = heads / kv_heads;
+  p.row_tiles = static_cast<int>((group * max_q + voc::kAttnRows - 1) / voc::kAttnRows);
+  p.tiles = static_cast<long long>(n_seq) * kv_heads * p.row_tiles;
+  long long keys = max_kv;
+  if (window > 0) keys = std::min<long long>(keys, static_cast<long long>(window) + max_q);
+  const long long blocks = keys / voc::kBlockTokens + 1;
+  long long splits = p.tiles >= sms ? 1 : (2 * sms) / std::max(1ll, p.tiles);
+  splits = std::max(1ll, std::min(splits, blocks / 4));
+  p.splits = static_cast<int>(std::min(splits, 1024ll));
+  if (p.splits > 1)
+    p.ws_bytes = static_cast<size_t>(p.tiles) * p.splits * voc::kAttnRows *
+                 (static_cast<size_t>(head_dim) * 4 + 8);
+  return p;
+}
+
+template <typename T, int D>
+cudaError_t launch_attention(const voc::LmAttnArgs &a, voc_stream_t stream) {
+  cudaError_t e = launch(voc::attn_rows_kernel<T, D>,
+                         dim3(a.splits, a.kv_heads * a.row_tiles, a.n_seq),
+                         dim3(voc::kAttnThreads), voc::attn_smem<D>(), 1, stream, a);
+  if (e != cudaSuccess || a.splits == 1) return e;
+  const int rows = a.group * a.max_q;
+  return launch(voc::attn_join_kernel<T, D>, dim3((rows + 3) / 4, a.kv_heads, a.n_seq), dim3(128),
+                0, 1, stream, a);
+}
+
+}  // namespace
+
+VOC_API size_t vocoder_lm_attention_ws_bytes(int n_seq, int max_q, int heads, int kv_heads,
+                                             int head_dim, int max_kv, int window) {
+  if (n_seq < 1 || max_q < 1 || kv_heads < 1 || heads < kv_heads || heads % kv_heads ||
+      (head_dim != 64 && head_dim != 128) || max_kv < 0 || window < 0)
+    return 0;
+  Device *dev;
+  if (device(&dev) != VOC_OK) return 0;
+  return plan_attention(dev->sms, n_seq, max_q, heads, kv_heads, head_dim, max_kv, window).ws_bytes;
+}
+
+VOC_API voc_status vocoder_lm_attention(
+    const void *q, long long ldq, long long hsq, int dtype, int heads, const void *k_cache,
+    const void *v_cache, const float *k_scale, const float *v_scale, int n_pages, int kv_heads,
+    int head_dim, const int *page_table, long long ldt, int table_cols, const int *kv_lens,
+    const int *cu_q, int n_seq, int n_tokens, int max_q, int max_kv, float softmax_scale,
+    int causal, int window, void *out, long long ldo, long long hso, void *ws, size_t ws_bytes,
+    voc_stream_t stream, unsigned flags) {
+  if (voc_status st = check_cache(k_cache, v_cache, k_scale, v_scale, n_pages, kv_heads, head_dim,
+                                  dtype, page_table, ldt, table_cols, kv_lens, cu_q, n_seq,
+                                  n_tokens, max_q);
+      st != VOC_OK)
+    return st;
+  if (!known_flags(flags)) return fail(VOC_INVALID_ARG, "attention: flags");
+  if (heads < kv_heads || heads % kv_heads)
+    return fail(VOC_INVALID_ARG, "attention: heads must be a multiple of kv_heads");
+  if (max_kv < 0 || window < 0 || (causal != 0 && causal != 1))
+    return fail(VOC_INVALID_ARG, "attention: max_kv, window or causal");
+  if (!std::isfinite(softmax_scale)) return fail(VOC_INVALID_ARG, "attention: softmax_scale");
+  if (n_tokens > 0 && (!q || !out)) return fail(VOC_INVALID_ARG, "attention: NULL buffer");
+  if (!aligned(q, 2) || !aligned(out, 2) || !aligned(ws, 16))
+    return fail(VOC_INVALID_ARG, "attention: alignment");
+  Device *dev;
+  if (voc_status st = device(&dev); st != VOC_OK) return st;
+  if (n_tokens == 0 || max_q == 0) return finish(*dev, stream, flags);
+  const AttnPlan plan =
+      plan_attention(dev->sms, n_seq, max_q, heads, kv_heads, head_dim, max_kv, window);
+  if (static_cast<long long>(plan.row_tiles) * kv_heads > 65535)
+    return fail(VOC_UNSUPPORTED, "attention: too many queries per sequence");
+  if (plan.ws_bytes && (!ws || ws_bytes < plan.ws_bytes))
+    return fail(VOC_WORKSPACE_TOO_SMALL, "attention: workspace below vocoder_lm_attention_ws_bytes");
+  voc::LmAttnArgs a{};
+  a.q = q, a.out = out, a.ldq = ldq, a.hsq = hsq, a.ldo = ldo, a.hso = hso;
+  a.kc = static_cast<const uint8_t *>(k_cache), a.vc = static_cast<const uint8_t *>(v_cache);
+  a.ks = k_scale, a.vs = v_scale;
+  a.table = page_table, a.lens = kv_lens, a.cu = cu_q, a.ldt = ldt;
+  a.n_pages = n_pages, a.table_cols = table_cols;
+  a.heads = heads, a.kv_heads = kv_heads, a.group = heads / kv_heads;
+  a.n_seq = n_seq, a.n_tokens = n_tokens, a.max_q = max_q;
+  a.scale_log2 = softmax_scale * 1.44269504f;
+  a.causal = causal, a.window = window;
+  a.row_tiles = plan.row_tiles, a.splits = plan.splits;
+  if (plan.splits > 1) {
+    a.part_o = static_cast<float *>(ws);
+    a.part_ml = reinterpret_cast<float2 *>(
+        a.part_o + static_cast<size_t>(plan.tiles) * plan.splits * voc::kAttnRows * head_dim);
+  }
+  a.budget = kWaitBudget;
+  a.timeout = dev->timeout;
+  cudaError_t e;
+  if (dtype == VOC_LM_F16)
+    e = head_dim == 64 ? launch_attention<__half, 64>(a, stream)
+                       : launch_attention<__half, 128>(a, stream);
+  else
+    e = head_dim == 64 ? launch_attention<__nv_bfloat16, 64>(a, stream)
+                       : launch_attention<__nv_bfloat16, 128>(a, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "launch attention");
+  return finish(*dev, stream, flags);
+}

@@ -120,6 +120,11 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
@@ -127,6 +132,15 @@ __device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v
 // ------------------------------------------------------------------ TMA
 __device__ __forceinline__ void prefetch_tmap(const void *tmap) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
+}
+// 2-D tiled tensor load into shared memory, completion counted on `bar`.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void *tmap, uint32_t bar, int x,
+                                            int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(tmap), "r"(bar), "r"(x), "r"(y)
+      : "memory");
 }
 // 4-D tiled tensor load into shared memory, completion counted on `bar`.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, uint32_t bar, int x,
@@ -238,6 +252,22 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
          | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// Shared-memory matrix descriptor of a K-major operand in the 128-byte swizzle: rows of 128 bytes,
+// groups of 8 rows 1024 bytes apart (the tile starts on a 1024-byte boundary).  Low word for the
+// address, and the common high word; a step of 32 bytes along K adds 2 to the low word.
+__device__ __forceinline__ uint32_t sw128_desc_lo(uint32_t addr) {
+  return ((addr & 0x3FFFFu) >> 4) | (1u << 16);
+}
+constexpr uint32_t kSw128DescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+// Instruction descriptor for kind::f8f6f4 with e4m3 A and B, fp32 accumulator, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
+  return (1u << 4)      // D format: f32
+         | (0u << 7)    // A format: e4m3
+         | (0u << 10)   // B format: e4m3
+         | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
 // Warp-wide MMA issue: the whole warp executes the call with identical operands and one
 // elected lane issues the instruction.  Keeping the issuing loop convergent lets the
 // descriptors stay in uniform registers; issued from a single divergent lane, every MMA
@@ -297,6 +327,27 @@ __device__ __forceinline__ void mma_bf16_warp_lo_col(uint32_t d_tmem, uint32_t a
     if (COL == 1) VOC_MMA_COL_ASM("1", "fill"); else VOC_MMA_COL_ASM("1", "lastuse");
   }
 #undef VOC_MMA_COL_ASM
+}
+// The e4m3 form (K = 32 bytes per instruction).
+template <bool PAIR>
+__device__ __forceinline__ void mma_e4m3_warp_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                                 uint32_t desc_hi, uint32_t idesc,
+                                                 uint32_t accumulate) {
+#define VOC_MMA_F8_ASM(GROUP)                                                                \
+  asm volatile(                                                                              \
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"                                    \
+      "mov.b64 da, {%1, %3};\n\t"                                                            \
+      "mov.b64 db, {%2, %3};\n\t"                                                            \
+      "setp.ne.b32 p, %5, 0;\n\t"                                                            \
+      "elect.sync _|e, 0xffffffff;\n\t"                                                      \
+      "@e tcgen05.mma.cta_group::" GROUP ".kind::f8f6f4 [%0], da, db, %4, p;\n\t}\n" ::       \
+          "r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(desc_hi), "r"(idesc), "r"(accumulate)       \
+      : "memory")
+  if (PAIR)
+    VOC_MMA_F8_ASM("2");
+  else
+    VOC_MMA_F8_ASM("1");
+#undef VOC_MMA_F8_ASM
 }
 // Warp-wide commits (one elected lane): arrive once on `bar` when every tcgen05 operation this
 // thread issued so far is done; the pair form arrives on the barrier at the same shared::cta

@@ -24,6 +24,14 @@
 
 #define VOC_API extern "C" __attribute__((visibility("default")))
 
+namespace voc {
+// Last error without a context, of this thread (the entry points of lm_ops.cu write it too).
+std::string &last_error_slot() {
+  static thread_local std::string err;
+  return err;
+}
+}  // namespace voc
+
 namespace {
 
 using voc::ConvGemmArgs;
@@ -41,7 +49,7 @@ constexpr int kBStageMax = 36 * 1024;  // bytes of one weight stage (per CTA)
 constexpr double kBandWeightBytes = 32e6;  // weights from which a layer takes the band job order
 constexpr int kBandRows = 12;             // row tiles of one band
 
-thread_local std::string g_err;  // last error without a context
+#define g_err voc::last_error_slot()
 
 // Every device allocation of the library goes through dev_alloc / dev_free, which keep a
 // count of the live ones and can be told to fail one on purpose (the allocation-failure

@@ -498,6 +498,92 @@ const char *vocoder_encoder_last_error(const vocoder_encoder_t *enc);
 /* Free the encoder (NULL is ignored). */
 void vocoder_encoder_destroy(vocoder_encoder_t *enc);
 
+/* ---------------------------------------------------------------- 8-bit operators
+ * The latents that vocoder_decode and vocoder_stream_decode take come from a transformer that
+ * runs in front of the decoder: over a whole prompt, or frame by frame beside a stream object.
+ * These four operators are its layer over e4m3 values (8-bit floats: 3 mantissa bits, largest
+ * value 448): rows to e4m3, product with e4m3 weights, append to an e4m3 cache of keys and values,
+ * attention over that cache.  They take no context: they run on the current device, on the
+ * caller's stream, asynchronously unless flags = VOC_FLAG_SYNC, allocate nothing, and report
+ * through vocoder_last_error(NULL).  All pointers are device memory unless named otherwise;
+ * strides (ld*: rows or tokens, hs*: heads) count elements.  A call with no rows or tokens does
+ * nothing.  Sums, softmax statistics and scales are 32-bit.  Every wait inside the kernels is
+ * bounded (about 2 s) and a kernel that gave up is reported as VOC_DEVICE_TIMEOUT by the next
+ * call made with VOC_FLAG_SYNC. */
+enum { VOC_LM_BF16 = 0, VOC_LM_F16 = 1, VOC_LM_F32 = 2 };
+enum { VOC_LM_RMS = 0, VOC_LM_NONE = 1, VOC_LM_GATED = 2 };
+#define VOC_LM_BLOCK 64 /* tokens of one cache block */
+
+/* Rows to e4m3 with one scale per row.  h = x (+ residual, added in 32 bits), then
+ *   VOC_LM_RMS    n = h / sqrt(mean(h^2) + eps) * weight[i]
+ *   VOC_LM_NONE   n = h
+ *   VOC_LM_GATED  n = silu(x[i]) * x[d + i], x rows of 2d values, no residual
+ *   scale[row] = max(max|n|, 2^-96) / 448,  out8[row][i] = e4m3(n / scale), round to nearest even.
+ * x, residual, weight and sum_out have the type `dtype`; sum_out (NULL: not wanted) receives h
+ * rounded once and may be the buffer of x or residual (same stride).  The norm takes the
+ * unrounded h.  A row that holds a NaN gets a NaN scale and NaN codes, a row that holds an
+ * infinity products that are NaN; other rows are not touched by it.  Any d from 1 to 2^24, any
+ * stride >= the width; 16-byte aligned buffers and strides run fastest. */
+voc_status vocoder_lm_rows_fp8(const void *x, long long ldx, const void *residual, long long ldr,
+                               const void *weight, int dtype, int mode, long long rows, int d,
+                               float eps, void *sum_out, long long lds, void *out8, long long ldo,
+                               float *scale, voc_stream_t stream, unsigned flags);
+
+/* y[m][n] = x_scale[m] * w_scale[n] * sum_k x8[m][k] * w8[n][k] (+ bias[n], fp32 or NULL), rounded
+ * once to out_dtype.  x8 [M][K] and w8 [N][K] e4m3, K contiguous, 16-byte aligned with row strides
+ * that are multiples of 16; out [M][N] with row stride ldo >= N.  K >= 1. */
+voc_status vocoder_lm_linear_fp8(const void *x8, long long ldx, const float *x_scale,
+                                 const void *w8, long long ldw, const float *w_scale,
+                                 const float *bias, int M, int N, int K, void *out, long long ldo,
+                                 int out_dtype, voc_stream_t stream, unsigned flags);
+
+/* The cache: a pool of n_pages blocks of 64 tokens, shared by all sequences.
+ *   k_cache [n_pages][kv_heads][64][head_dim], v_cache [n_pages][kv_heads][head_dim][64], e4m3
+ *   (v with the tokens innermost); k_scale, v_scale [n_pages][kv_heads] fp32: one scale for each
+ *   block and head, a stored code c stands for c * scale.  head_dim is 64 or 128.
+ * The batch: n_seq sequences with n_tokens new tokens in all, those of one sequence in a row;
+ *   page_table [n_seq][table_cols] int32 (row stride ldt): the page of each block of a sequence;
+ *   a page outside 0..n_pages-1 holds no tokens (nothing is written to or read from it);
+ *   kv_lens [n_seq] int32: tokens of the sequence, the new ones included;
+ *   cu_q [n_seq + 1] int32: first new token of each sequence, or NULL when each has max_q;
+ *   max_q: the largest number of new tokens of a sequence.
+ * New token i of a sequence with q of them has position kv_len - q + i.
+ *
+ * Append stores the new tokens' k and v [n_tokens][kv_heads][head_dim] (bf16 or f16, head_dim
+ * contiguous, 16-byte aligned, strides multiples of 8).  Scales are powers of two: the smallest
+ * 2^e with e >= -96 and max|value| <= 448 * 2^e over the block's finite new values.  A block whose
+ * first token is new is written whole, zeros beyond its tokens.  A block with earlier tokens keeps
+ * its scale if it suffices; otherwise its codes move to the larger one.  Infinities saturate.  A
+ * token with a NaN in k or v gets a NaN key and zeros in place of v's NaN values, so queries that
+ * see it are NaN and no others.  No two sequences may append to one page.  Tokens beyond the page
+ * table are dropped. */
+voc_status vocoder_lm_kv_append(void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                                int n_pages, int kv_heads, int head_dim, const void *k,
+                                long long ldk, long long hsk, const void *v, long long ldv,
+                                long long hsv, int dtype, const int *page_table, long long ldt,
+                                int table_cols, const int *kv_lens, const int *cu_q, int n_seq,
+                                int n_tokens, int max_q, voc_stream_t stream, unsigned flags);
+
+/* out = softmax(softmax_scale * q k^T) v for the new tokens' queries q [n_tokens][heads][head_dim]
+ * (bf16 or f16, out the same type), over the tokens of the own sequence that the query sees:
+ * causal = 1: positions up to its own, causal = 0: all kv_len; window > 0: only positions above
+ * its own minus window.  heads is a multiple of kv_heads (query head h uses key head
+ * h / (heads / kv_heads)).  A query that sees no token gets zeros.  What lies in the cache outside
+ * a query's tokens does not reach it, except that stored values (v_cache) of tokens other queries
+ * of the call see must not be NaN codes (append never stores one).  max_kv: at least the largest
+ * kv_len (it bounds the split of long caches, not the result).  ws: 16-byte aligned, at least
+ * vocoder_lm_attention_ws_bytes (0: NULL will do), not used by anything else meanwhile. */
+size_t vocoder_lm_attention_ws_bytes(int n_seq, int max_q, int heads, int kv_heads, int head_dim,
+                                     int max_kv, int window);
+voc_status vocoder_lm_attention(const void *q, long long ldq, long long hsq, int dtype, int heads,
+                                const void *k_cache, const void *v_cache, const float *k_scale,
+                                const float *v_scale, int n_pages, int kv_heads, int head_dim,
+                                const int *page_table, long long ldt, int table_cols,
+                                const int *kv_lens, const int *cu_q, int n_seq, int n_tokens,
+                                int max_q, int max_kv, float softmax_scale, int causal, int window,
+                                void *out, long long ldo, long long hso, void *ws,
+                                size_t ws_bytes, voc_stream_t stream, unsigned flags);
+
 #ifdef __cplusplus
 }
 #endif
