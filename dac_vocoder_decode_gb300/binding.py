@@ -756,62 +756,71 @@ class Encoder:
 
 
 # ------------------------------------------------------------------ 8-bit operators
-_LM_TYPES = None
+# One call of these is a few microseconds of host time beside kernels of the same length, so the
+# checks below stay with what is cheap to ask of a tensor; the library checks the rest.
+class _LM:
+    """What the wrappers need of torch and the library, looked up with the first call."""
+    ready = False
 
 
-def _lm_types():
-    """torch dtype -> VOC_LM_* (torch is imported with the first call only)."""
-    global _LM_TYPES
-    if _LM_TYPES is None:
-        import torch
-        _LM_TYPES = {torch.bfloat16: VOC_LM_BF16, torch.float16: VOC_LM_F16,
-                     torch.float32: VOC_LM_F32}
-    return _LM_TYPES
+def _lm_setup():
+    import torch
+    lib = load_library()
+    _LM.torch, _LM.empty = torch, torch.empty
+    _LM.f8, _LM.f32, _LM.i32 = torch.float8_e4m3fn, torch.float32, torch.int32
+    _LM.types = {torch.bfloat16: VOC_LM_BF16, torch.float16: VOC_LM_F16,
+                 torch.float32: VOC_LM_F32}
+    _LM.rows, _LM.linear = lib.vocoder_lm_rows_fp8, lib.vocoder_lm_linear_fp8
+    _LM.append, _LM.attention = lib.vocoder_lm_kv_append, lib.vocoder_lm_attention
+    _LM.attention_ws = lib.vocoder_lm_attention_ws_bytes
+    # the current stream as an integer, without building a Stream object where torch allows it
+    _LM.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                             lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _LM.ready = True
 
 
 def _bad(msg: str):
     return VocoderError(VOC_INVALID_ARG, msg)
 
 
-def _lm_on_device(device, *tensors):
-    """All operands live on the current CUDA device."""
-    import torch
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise _bad(f"tensors must be on the current CUDA device, got {device}")
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise _bad("tensors must be on one CUDA device")
-
-
-def _lm_stream(device, stream, *made):
-    """Raw stream; tensors `made` here are kept until the work on a stream of the caller's ends."""
-    import torch
-    current = torch.cuda.current_stream(device)
+def _lm_stream(dev, stream, made):
+    """Raw stream.  Tensors `made` by the call belong to the current stream; one of the caller's
+    that is another keeps them until its work is done."""
     if stream is None:
-        return current.cuda_stream
+        return _LM.raw_stream(dev)
+    torch = _LM.torch
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    if stream.cuda_stream != current.cuda_stream:
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    if stream.cuda_stream != _LM.raw_stream(dev):
         for t in made:
             if t is not None:
                 t.record_stream(stream)
     return stream.cuda_stream
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _lm_device(x):
+    """Index of x's device, which has to be the current one."""
+    dev = x.get_device()
+    if dev < 0 or dev != _LM.torch.cuda.current_device():
+        raise _bad(f"tensors must be on the current CUDA device, got {x.device}")
+    return dev
 
 
-def _rows_ok(t, name, rows, width):
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width or \
-            (t.stride(1) != 1 and width > 1):
-        raise _bad(f"{name} must be [{rows}, {width}] with contiguous rows, got "
-                   f"{tuple(t.shape)} with strides {tuple(t.stride())}")
+def _rows_strides(t, name, rows, width, dtype, dev):
+    """Row stride of a [rows, width] operand; that of a single row does not count."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != rows or shape[1] != width or t.dtype != dtype or \
+            (stride[1] != 1 and width > 1) or t.get_device() != dev:
+        raise _bad(f"{name} must be {dtype} [{rows}, {width}] with contiguous rows on x's device, "
+                   f"got {t.dtype} {tuple(shape)} with strides {stride} on {t.device}")
+    return stride[0] if rows > 1 else max(width, stride[0])
 
 
-def _ld(t):
-    """Row stride; that of a single row may be anything and does not count."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+def _vector_ok(t, name, n, dtype, dev):
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or t.get_device() != dev or \
+            (n > 1 and t.stride(0) != 1):
+        raise _bad(f"{name} must be contiguous {dtype} [{n}] on x's device")
+    return t.data_ptr()
 
 
 def rows_fp8(x, mode: int = VOC_LM_RMS, weight=None, residual=None, eps: float = 1e-6,
@@ -820,52 +829,52 @@ def rows_fp8(x, mode: int = VOC_LM_RMS, weight=None, residual=None, eps: float =
     vocoder_lm_rows_fp8 in include/vocoder.h).  Returns (out, scale, sum): out float8_e4m3fn
     [rows, d] (a new one has its row stride padded to 16, as linear_fp8 takes it), scale fp32
     [rows], sum = x + residual in x's type, or None without a residual."""
-    import torch
-    types = _lm_types()
-    if x.dtype not in types or x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1):
-        raise _bad("x must be a 2-d bf16, f16 or f32 tensor with contiguous rows")
-    rows, d = x.shape
+    if not _LM.ready:
+        _lm_setup()
+    dtype, shape = x.dtype, x.shape
+    code = _LM.types.get(dtype)
+    if code is None or len(shape) != 2:
+        raise _bad("x must be a 2-d bf16, f16 or f32 tensor")
+    rows, width = shape
+    d = width
     if mode == VOC_LM_GATED:
-        if d % 2:
+        if width % 2:
             raise _bad("gated rows need an even width")
-        d //= 2
-    made = []
+        d = width // 2
+    dev = _lm_device(x)
+    ldx = _rows_strides(x, "x", rows, width, dtype, dev)
+    wp = rp = sp = None
+    ldr = lds = 0
+    made_sum = made_out = made_scale = None
+    if weight is not None:
+        wp = _vector_ok(weight, "weight", d, dtype, dev)
     if residual is not None:
-        _rows_ok(residual, "residual", rows, d)
+        ldr = _rows_strides(residual, "residual", rows, d, dtype, dev)
+        rp = residual.data_ptr()
         if sum_out is None:
-            sum_out = torch.empty((rows, d), dtype=x.dtype, device=x.device)
-            made.append(sum_out)
+            sum_out = made_sum = _LM.empty((rows, d), dtype=dtype, device=x.device)
+            lds = d
         else:
-            _rows_ok(sum_out, "sum_out", rows, d)
-        if residual.dtype != x.dtype or sum_out.dtype != x.dtype:
-            raise _bad("residual and sum_out must have x's type")
+            lds = _rows_strides(sum_out, "sum_out", rows, d, dtype, dev)
+        sp = sum_out.data_ptr()
     elif sum_out is not None:
         raise _bad("sum_out without residual")
-    if weight is not None and (weight.dtype != x.dtype or weight.dim() != 1 or
-                               weight.shape[0] != d or (weight.stride(0) != 1 and d > 1)):
-        raise _bad("weight must be [d] in x's type")
     if out is None:
-        out = torch.empty((rows, (d + 15) // 16 * 16), dtype=torch.float8_e4m3fn,
-                          device=x.device)
-        made.append(out)
-        if out.shape[1] != d:
+        ldo = (d + 15) // 16 * 16
+        out = made_out = _LM.empty((rows, ldo), dtype=_LM.f8, device=x.device)
+        if ldo != d:
             out = out[:, :d]
     else:
-        _rows_ok(out, "out", rows, d)
-        if out.dtype != torch.float8_e4m3fn:
-            raise _bad("out must be float8_e4m3fn")
+        ldo = _rows_strides(out, "out", rows, d, _LM.f8, dev)
     if scale is None:
-        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
-        made.append(scale)
-    elif scale.dtype != torch.float32 or scale.shape != (rows,) or not scale.is_contiguous():
-        raise _bad("scale must be contiguous fp32 [rows]")
-    _lm_on_device(x.device, residual, weight, sum_out, out, scale)
-    st = load_library().vocoder_lm_rows_fp8(
-        x.data_ptr(), _ld(x), _ptr(residual), 0 if residual is None else _ld(residual),
-        _ptr(weight), types[x.dtype], mode, rows, d, eps, _ptr(sum_out),
-        0 if sum_out is None else _ld(sum_out), out.data_ptr(), _ld(out), scale.data_ptr(),
-        _lm_stream(x.device, stream, *made), flags)
-    _check(st)
+        scale = made_scale = _LM.empty((rows,), dtype=_LM.f32, device=x.device)
+    else:
+        _vector_ok(scale, "scale", rows, _LM.f32, dev)
+    st = _LM.rows(x.data_ptr(), ldx, rp, ldr, wp, code, mode, rows, d, eps, sp, lds,
+                  out.data_ptr(), ldo, scale.data_ptr(),
+                  _lm_stream(dev, stream, (made_sum, made_out, made_scale)), flags)
+    if st:
+        _check(st)
     return out, scale, sum_out
 
 
@@ -874,37 +883,41 @@ def linear_fp8(x, x_scale, w, w_scale, bias=None, out_dtype=None, out=None, stre
     """x [M, K] and w [N, K] float8_e4m3fn (16-byte aligned, row strides multiples of 16) with fp32
     scales [M] and [N], bias fp32 [N] -> [M, N] in out_dtype (bf16 by default; see
     vocoder_lm_linear_fp8 in include/vocoder.h)."""
-    import torch
-    types = _lm_types()
-    f8, f32 = torch.float8_e4m3fn, torch.float32
-    if x.dim() != 2 or w.dim() != 2 or x.dtype != f8 or w.dtype != f8:
+    if not _LM.ready:
+        _lm_setup()
+    if x.dim() != 2 or w.dim() != 2:
         raise _bad("x and w must be 2-d float8_e4m3fn tensors")
-    (M, K), N = x.shape, w.shape[0]
-    if w.shape[1] != K or (K > 1 and (x.stride(1) != 1 or w.stride(1) != 1)):
-        raise _bad("x [M, K] and w [N, K] must have one K and contiguous rows")
-    if x_scale.dtype != f32 or x_scale.shape != (M,) or not x_scale.is_contiguous() or \
-            w_scale.dtype != f32 or w_scale.shape != (N,) or not w_scale.is_contiguous():
-        raise _bad("x_scale [M] and w_scale [N] must be contiguous fp32")
-    if bias is not None and (bias.dtype != f32 or bias.shape != (N,) or
-                             not bias.is_contiguous()):
-        raise _bad("bias must be contiguous fp32 [N]")
-    made = ()
+    f32 = _LM.f32
+    M, K = x.shape
+    N = w.shape[0]
+    dev = _lm_device(x)
+    ldx = _rows_strides(x, "x", M, K, _LM.f8, dev)
+    ldw = _rows_strides(w, "w", N, K, _LM.f8, dev)
+    if M == 1:
+        ldx = (ldx + 15) // 16 * 16
+    if N == 1:
+        ldw = (ldw + 15) // 16 * 16
+    xsp = _vector_ok(x_scale, "x_scale", M, f32, dev)
+    wsp = _vector_ok(w_scale, "w_scale", N, f32, dev)
+    bp = None if bias is None else _vector_ok(bias, "bias", N, f32, dev)
+    made = None
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=x.device)
-        made = (out,)
+        if out_dtype is None:
+            out_dtype = _LM.torch.bfloat16
+        code = _LM.types.get(out_dtype)
+        if code is None:
+            raise _bad("the output is bf16, f16 or f32")
+        out = made = _LM.empty((M, N), dtype=out_dtype, device=x.device)
+        ldo = N
     else:
-        _rows_ok(out, "out", M, N)
-        if out_dtype is not None and out.dtype != out_dtype:
-            raise _bad("out has another type than out_dtype")
-    if out.dtype not in types:
-        raise _bad("the output is bf16, f16 or f32")
-    _lm_on_device(x.device, x_scale, w, w_scale, bias, out)
-    up16 = lambda t: t.stride(0) if t.shape[0] > 1 else (max(K, t.stride(0)) + 15) // 16 * 16  # noqa: E731
-    st = load_library().vocoder_lm_linear_fp8(
-        x.data_ptr(), up16(x), x_scale.data_ptr(), w.data_ptr(), up16(w), w_scale.data_ptr(),
-        _ptr(bias), M, N, K, out.data_ptr(), _ld(out), types[out.dtype],
-        _lm_stream(x.device, stream, *made), flags)
-    _check(st)
+        code = _LM.types.get(out.dtype)
+        if code is None or (out_dtype is not None and out.dtype != out_dtype):
+            raise _bad("out is bf16, f16 or f32, and of out_dtype where that is given")
+        ldo = _rows_strides(out, "out", M, N, out.dtype, dev)
+    st = _LM.linear(x.data_ptr(), ldx, xsp, w.data_ptr(), ldw, wsp, bp, M, N, K, out.data_ptr(),
+                    ldo, code, _lm_stream(dev, stream, (made,)), flags)
+    if st:
+        _check(st)
     return out
 
 
@@ -912,24 +925,29 @@ class KVCacheFP8:
     """A pool of 64-token blocks of e4m3 keys and values: k [pages, kv_heads, 64, d] and v [pages,
     kv_heads, d, 64] float8_e4m3fn, k_scale and v_scale fp32 [pages, kv_heads] (see the cache in
     include/vocoder.h)."""
-    __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "kv_heads", "head_dim")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "kv_heads", "head_dim", "device_index",
+                 "_args")
 
     def __init__(self, k, v, k_scale, v_scale):
-        import torch
-        f8, f32 = torch.float8_e4m3fn, torch.float32
-        if k.dim() != 4 or k.shape[2] != VOC_LM_BLOCK:
+        if not _LM.ready:
+            _lm_setup()
+        shape = k.shape
+        if len(shape) != 4 or shape[2] != VOC_LM_BLOCK:
             raise _bad("k must be [pages, kv_heads, 64, head_dim]")
-        self.pages, self.kv_heads, _, self.head_dim = k.shape
-        if v.shape != (self.pages, self.kv_heads, self.head_dim, VOC_LM_BLOCK):
+        pages, heads, _, d = shape
+        if v.shape != (pages, heads, d, VOC_LM_BLOCK):
             raise _bad("v must be [pages, kv_heads, head_dim, 64]")
-        if k_scale.shape != k.shape[:2] or v_scale.shape != k.shape[:2]:
+        if k_scale.shape != (pages, heads) or v_scale.shape != (pages, heads):
             raise _bad("scales must be [pages, kv_heads]")
-        if k.dtype != f8 or v.dtype != f8 or k_scale.dtype != f32 or v_scale.dtype != f32:
-            raise _bad("the cache holds float8_e4m3fn codes and fp32 scales")
-        if not (k.is_contiguous() and v.is_contiguous() and k_scale.is_contiguous() and
-                v_scale.is_contiguous()):
-            raise _bad("cache tensors must be contiguous")
+        f8, f32, dev = _LM.f8, _LM.f32, k.get_device()
+        for t, dtype in ((k, f8), (v, f8), (k_scale, f32), (v_scale, f32)):
+            if t.dtype != dtype or not t.is_contiguous() or t.get_device() != dev:
+                raise _bad("the cache is contiguous float8_e4m3fn codes and fp32 scales on one "
+                           "device")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.kv_heads, self.head_dim, self.device_index = pages, heads, d, dev
+        self._args = (k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages,
+                      heads, d)
 
     @classmethod
     def empty(cls, pages: int, kv_heads: int, head_dim: int, device="cuda"):
@@ -941,19 +959,20 @@ class KVCacheFP8:
                    mk(pages, kv_heads, head_dim, VOC_LM_BLOCK), sc(), sc())
 
 
-def _batch_ok(page_table, kv_lens, cu_q):
-    import torch
-    i32 = torch.int32
-    if page_table.dtype != i32 or page_table.dim() != 2 or \
-            (page_table.stride(1) != 1 and page_table.shape[1] > 1):
-        raise _bad("page_table must be int32 [sequences, blocks] with contiguous rows")
-    n = page_table.shape[0]
-    if kv_lens.dtype != i32 or kv_lens.shape != (n,) or not kv_lens.is_contiguous():
-        raise _bad("kv_lens must be contiguous int32 [sequences]")
-    if cu_q is not None and (cu_q.dtype != i32 or cu_q.shape != (n + 1,) or
-                             not cu_q.is_contiguous()):
-        raise _bad("cu_q must be contiguous int32 [sequences + 1]")
-    return n
+def _batch_args(cache, x, page_table, kv_lens, cu_q):
+    """(device, pointers and sizes of the batch) after the checks that cache and batch share."""
+    dev = _lm_device(x)
+    i32 = _LM.i32
+    shape, stride = page_table.shape, page_table.stride()
+    if len(shape) != 2 or page_table.dtype != i32 or (stride[1] != 1 and shape[1] > 1) or \
+            page_table.get_device() != dev or cache.device_index != dev:
+        raise _bad("page_table must be int32 [sequences, blocks] with contiguous rows, on one "
+                   "device with the cache and the tokens")
+    n, cols = shape
+    lens = _vector_ok(kv_lens, "kv_lens", n, i32, dev)
+    cu = None if cu_q is None else _vector_ok(cu_q, "cu_q", n + 1, i32, dev)
+    return dev, (page_table.data_ptr(), stride[0] if n > 1 else max(cols, stride[0]), cols, lens,
+                 cu, n)
 
 
 def kv_append_fp8(cache: KVCacheFP8, k, v, page_table, kv_lens, cu_q=None, max_q: int = 1,
@@ -962,21 +981,17 @@ def kv_append_fp8(cache: KVCacheFP8, k, v, page_table, kv_lens, cu_q=None, max_q
     vocoder_lm_kv_append in include/vocoder.h).  page_table int32 [sequences, blocks], kv_lens
     int32 [sequences] with the new tokens counted, cu_q int32 [sequences + 1] or None when every
     sequence has max_q new tokens."""
-    types = _lm_types()
-    n = _batch_ok(page_table, kv_lens, cu_q)
-    shape = (k.shape[0], cache.kv_heads, cache.head_dim)
-    if k.shape != shape or v.shape != shape or k.dtype not in types or v.dtype != k.dtype or \
-            k.stride(2) != 1 or v.stride(2) != 1:
+    dev, batch = _batch_args(cache, k, page_table, kv_lens, cu_q)
+    shape, ks, vs = k.shape, k.stride(), v.stride()
+    code = _LM.types.get(k.dtype)
+    if len(shape) != 3 or shape[1] != cache.kv_heads or shape[2] != cache.head_dim or \
+            v.shape != shape or code is None or v.dtype != k.dtype or ks[2] != 1 or \
+            vs[2] != 1 or v.get_device() != dev:
         raise _bad("k and v must be [tokens, kv_heads, head_dim] of one type, head_dim contiguous")
-    _lm_on_device(k.device, v, page_table, kv_lens, cu_q, cache.k, cache.v, cache.k_scale,
-                  cache.v_scale)
-    st = load_library().vocoder_lm_kv_append(
-        cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
-        cache.v_scale.data_ptr(), cache.pages, cache.kv_heads, cache.head_dim, k.data_ptr(),
-        k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), types[k.dtype],
-        page_table.data_ptr(), _ld(page_table), page_table.shape[1], kv_lens.data_ptr(),
-        _ptr(cu_q), n, shape[0], max_q, _lm_stream(k.device, stream), flags)
-    _check(st)
+    st = _LM.append(*cache._args, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], code,
+                    *batch, shape[0], max_q, _lm_stream(dev, stream, ()), flags)
+    if st:
+        _check(st)
 
 
 def attention_fp8(q, cache: KVCacheFP8, page_table, kv_lens, cu_q=None, max_q: int = 1,
@@ -987,36 +1002,35 @@ def attention_fp8(q, cache: KVCacheFP8, page_table, kv_lens, cu_q=None, max_q: i
     vocoder_lm_attention in include/vocoder.h; the batch as in kv_append_fp8).  max_kv: at least
     the largest kv_len (default: what the page table can hold); softmax_scale defaults to
     1/sqrt(head_dim); ws: uint8 workspace of vocoder_lm_attention_ws_bytes (a new one if None)."""
-    import torch
-    types = _lm_types()
-    n = _batch_ok(page_table, kv_lens, cu_q)
-    if q.dim() != 3 or q.shape[2] != cache.head_dim or q.dtype not in types or q.stride(2) != 1:
+    dev, batch = _batch_args(cache, q, page_table, kv_lens, cu_q)
+    shape, qs, dtype = q.shape, q.stride(), q.dtype
+    code = _LM.types.get(dtype)
+    if len(shape) != 3 or shape[2] != cache.head_dim or code is None or qs[2] != 1:
         raise _bad("q must be [tokens, heads, head_dim], head_dim contiguous")
-    tokens, heads, d = q.shape
-    made = []
+    tokens, heads, d = shape
+    made_out = made_ws = None
     if out is None:
-        out = torch.empty((tokens, heads, d), dtype=q.dtype, device=q.device)
-        made.append(out)
-    elif out.shape != q.shape or out.dtype != q.dtype or out.stride(2) != 1:
-        raise _bad("out must have q's shape and type, head_dim contiguous")
+        out = made_out = _LM.empty(shape, dtype=dtype, device=q.device)
+        os_ = (heads * d, d)
+    else:
+        os_ = out.stride()
+        if out.shape != shape or out.dtype != dtype or os_[2] != 1 or out.get_device() != dev:
+            raise _bad("out must have q's shape, type and device, head_dim contiguous")
     if max_kv is None:
-        max_kv = page_table.shape[1] * VOC_LM_BLOCK
+        max_kv = batch[2] * VOC_LM_BLOCK
     if softmax_scale is None:
         softmax_scale = d ** -0.5
-    lib = load_library()
     if ws is None:
-        need = lib.vocoder_lm_attention_ws_bytes(n, max_q, heads, cache.kv_heads, d, max_kv, window)
+        need = _LM.attention_ws(batch[5], max_q, heads, cache.kv_heads, d, max_kv, window)
         if need:
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-            made.append(ws)
-    _lm_on_device(q.device, out, page_table, kv_lens, cu_q, ws, cache.k, cache.v, cache.k_scale,
-                  cache.v_scale)
-    st = lib.vocoder_lm_attention(
-        q.data_ptr(), q.stride(0), q.stride(1), types[q.dtype], heads, cache.k.data_ptr(),
-        cache.v.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), cache.pages,
-        cache.kv_heads, d, page_table.data_ptr(), _ld(page_table), page_table.shape[1],
-        kv_lens.data_ptr(), _ptr(cu_q), n, tokens, max_q, max_kv, softmax_scale, int(causal),
-        window, out.data_ptr(), out.stride(0), out.stride(1), _ptr(ws),
-        0 if ws is None else ws.numel(), _lm_stream(q.device, stream, *made), flags)
-    _check(st)
+            ws = made_ws = _LM.empty((need,), dtype=_LM.torch.uint8, device=q.device)
+    elif ws.dtype != _LM.torch.uint8 or not ws.is_contiguous() or ws.get_device() != dev:
+        raise _bad("ws must be contiguous uint8 on q's device")
+    st = _LM.attention(q.data_ptr(), qs[0], qs[1], code, heads, *cache._args, *batch, tokens,
+                       max_q, max_kv, softmax_scale, causal, window, out.data_ptr(), os_[0],
+                       os_[1], None if ws is None else ws.data_ptr(),
+                       0 if ws is None else ws.numel(),
+                       _lm_stream(dev, stream, (made_out, made_ws)), flags)
+    if st:
+        _check(st)
     return out
