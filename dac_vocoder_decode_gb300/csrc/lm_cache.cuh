@@ -54,17 +54,44 @@ __device__ __forceinline__ int block_exponent(float a) {
   return max(kScaleMinExp, x - ((u & 0x7fffffu) <= 0x600000u ? 9 : 8));
 }
 
-// One CTA per (touched block, head, sequence).  Registers hold the block's new tokens (64 x D
-// values of K and of V over 256 threads), so k and v are read once; the transposed V goes through
-// shared memory.
+// Finite 16-bit values: the first bits that are not, and the value of |bits|.
+template <typename T>
+struct Bits16;
+template <>
+struct Bits16<__half> {
+  static constexpr uint32_t kInf = 0x7c00u;
+  static __device__ __forceinline__ float value(uint32_t b) {
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(b)));
+  }
+};
+template <>
+struct Bits16<__nv_bfloat16> {
+  static constexpr uint32_t kInf = 0x7f80u;
+  static __device__ __forceinline__ float value(uint32_t b) { return __uint_as_float(b << 16); }
+};
+
+// Four codes times `f`, rounded again.
+__device__ __forceinline__ uint32_t move_codes(uint32_t w, float f) {
+  const float2 a = e4m3x2_to_f32(w & 0xffff), b = e4m3x2_to_f32(w >> 16);
+  return e4m3x4(a.x * f, a.y * f, b.x * f, b.y * f);
+}
+
+template <int D>
+struct AppendShape {
+  static constexpr int kThreads = 2 * D;  // 16 groups of 4 tokens x D / 8 groups of 8 channels
+};
+
+// One CTA per (touched block, head, sequence); a thread holds 4 tokens x 8 channels of k and of v
+// as they were read, so both are read once.  A warp covers 32 tokens x 32 channels: its loads and
+// its stores of K rows and of V rows (4 tokens of a channel are one word) all fill 32-byte sectors,
+// without a pass through shared memory.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) append_kernel(const LmAppendArgs p) {
-  constexpr int kChunks = D / 8;                        // 8-value chunks of a token's row
-  constexpr int kPer = kBlockTokens * kChunks / 256;    // chunks per thread: 2 (D 64) or 4 (D 128)
-  __shared__ float red[32];
-  __shared__ uint32_t bad[2];                           // tokens of the block with a NaN
-  __shared__ __align__(16) uint8_t vt[D][kBlockTokens];
-  const int tid = threadIdx.x;
+__global__ void __launch_bounds__(AppendShape<D>::kThreads) append_kernel(const LmAppendArgs p) {
+  constexpr int kThreads = AppendShape<D>::kThreads, kWarps = kThreads / 32;
+  __shared__ uint32_t red[2][kWarps];
+  __shared__ uint32_t bad[2];  // tokens of the block with a NaN
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int t4 = (warp % 2) * 32 + lane / 4 * 4, ch = (warp / 2) * 32 + lane % 4 * 8;
   pdl_wait();
   const int b = blockIdx.z, head = blockIdx.y;
   const SeqSpan span = seq_span(p.cu, b, p.n_seq, p.n_tokens, p.max_q);
@@ -79,103 +106,124 @@ __global__ void __launch_bounds__(256) append_kernel(const LmAppendArgs p) {
   const int lo = static_cast<int>(start > base ? start - base : 0);
   const int hi = static_cast<int>(len - base < kBlockTokens ? len - base : kBlockTokens);
   const bool fresh = lo == 0;
-  if (tid < 2) bad[tid] = 0;
-  __syncthreads();
+  const long long slot = static_cast<long long>(page) * p.heads + head;
+  const float old[2] = {fresh ? 0.f : p.ks[slot], fresh ? 0.f : p.vs[slot]};
 
-  float kv[2][kPer][8];
-  uint32_t m[2] = {0, 0};
+  uint4 raw[2][4];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int c = tid + 256 * i, tok = c / kChunks, ch = c % kChunks;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) kv[0][i][j] = kv[1][i][j] = 0.f;
-    if (tok >= lo && tok < hi) {
-      const long long row = span.first + (base + tok - p0);
-      const T *src[2] = {static_cast<const T *>(p.k) + row * p.ldk + head * p.hsk + ch * 8,
-                         static_cast<const T *>(p.v) + row * p.ldv + head * p.hsv + ch * 8};
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        float f[8];
-        Vec16<T>::unpack(*reinterpret_cast<const uint4 *>(src[t]), f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t a = abs_bits(f[j]);
-          if (a < kInfBits) m[t] = max(m[t], a);
-          if (a > kInfBits) {
-            atomicOr(&bad[tok / 32], 1u << (tok % 32));
-            f[j] = 0.f;
-          }
-          kv[t][i][j] = f[j];
-        }
-      }
+  for (int i = 0; i < 4; ++i) {
+    raw[0][i] = raw[1][i] = make_uint4(0, 0, 0, 0);
+    if (t4 + i >= lo && t4 + i < hi) {
+      const long long row = span.first + (base + t4 + i - p0);
+      raw[0][i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.k) + row * p.ldk +
+                                                   head * p.hsk + ch);
+      raw[1][i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.v) + row * p.ldv +
+                                                   head * p.hsv + ch);
     }
   }
-  const long long slot = static_cast<long long>(page) * p.heads + head;
-  uint8_t *kb = p.kc + slot * (kBlockTokens * D), *vb = p.vc + slot * (kBlockTokens * D);
+  uint32_t m[2] = {0, 0};  // largest |value| of k and v, two at a time in the words' halves
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w[4] = {raw[t][i].x, raw[t][i].y, raw[t][i].z, raw[t][i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m[t] = __vmaxu2(m[t], w[j] & 0x7fff7fffu);
+    }
+  auto block_max = [&]() {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) m[t] = __vmaxu2(m[t], __shfl_xor_sync(0xffffffffu, m[t], o));
+      if (lane == 0) red[t][warp] = m[t];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m[t] = __vmaxu2(m[t], red[t][w]);
+      m[t] = max(m[t] & 0xffffu, m[t] >> 16);
+    }
+  };
+  if (tid < 2) bad[tid] = 0;
+  block_max();
+  if (m[0] >= Bits16<T>::kInf || m[1] >= Bits16<T>::kInf) {  // an infinity or NaN in the block
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      m[t] = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w[4] = {raw[t][i].x, raw[t][i].y, raw[t][i].z, raw[t][i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t fin = w[j] & 0x7fff7fffu;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t half = fin >> 16 * h & 0xffffu;
+            if (half >= Bits16<T>::kInf) fin &= ~(0xffffu << 16 * h);
+            if (half > Bits16<T>::kInf) {
+              atomicOr(&bad[(t4 + i) / 32], 1u << (t4 + i) % 32);
+              w[j] &= ~(0xffffu << 16 * h);
+            }
+          }
+          m[t] = __vmaxu2(m[t], fin);
+        }
+        raw[t][i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    block_max();
+  }
+  float inv[2], move[2];
   float *scales[2] = {p.ks + slot, p.vs + slot};
-  float inv[2], move[2] = {1.f, 1.f};
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const uint32_t a = group_max<256>(m[t], red);
-    float s = pow2(block_exponent(__uint_as_float(a)));
-    if (!fresh) {
-      const float old = *scales[t];
-      if (old > s) s = old;
-      move[t] = old / s;
-    }
+    // `old` was read before block_max's barrier, so the store cannot overtake another's read
+    float s = pow2(block_exponent(Bits16<T>::value(m[t])));
+    move[t] = 1.f;
+    if (!fresh && old[t] > s) s = old[t];
+    if (!fresh) move[t] = old[t] / s;
     inv[t] = 1.f / s;
-    __syncthreads();  // everybody has read the old scale
     if (tid == 0) *scales[t] = s;
   }
 
+  uint8_t *kb = p.kc + slot * (kBlockTokens * D), *vb = p.vc + slot * (kBlockTokens * D);
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int c = tid + 256 * i, tok = c / kChunks, ch = c % kChunks;
-    const bool is_new = tok >= lo && tok < hi;
-    uint2 *dst = reinterpret_cast<uint2 *>(kb + tok * D + ch * 8);
-    if (is_new || fresh) {
+  for (int i = 0; i < 4; ++i) {
+    const int tok = t4 + i;
+    uint2 *dst = reinterpret_cast<uint2 *>(kb + tok * D + ch);
+    if (fresh || (tok >= lo && tok < hi)) {
       float f[8];
+      Vec16<T>::unpack(raw[0][i], f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = kv[0][i][j] * inv[0];
+      for (int j = 0; j < 8; ++j) f[j] *= inv[0];
       uint2 w = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
       if (bad[tok / 32] >> (tok % 32) & 1u) w = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
       *dst = w;
     } else if (move[0] != 1.f) {
       const uint2 o = *dst;
-      const uint32_t w[2] = {o.x, o.y};
-      uint32_t r[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float2 a = e4m3x2_to_f32(w[j] & 0xffff), c2 = e4m3x2_to_f32(w[j] >> 16);
-        r[j] = e4m3x4(a.x * move[0], a.y * move[0], c2.x * move[0], c2.y * move[0]);
-      }
-      *dst = make_uint2(r[0], r[1]);
-    }
-    if (is_new || fresh) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) vt[ch * 8 + j][tok] = e4m3(kv[1][i][j] * inv[1]);
+      *dst = make_uint2(move_codes(o.x, move[0]), move_codes(o.y, move[0]));
     }
   }
-  __syncthreads();
-  // V: 4 tokens of one channel at a time; a block without earlier tokens is stored whole
-  const bool moved = move[1] != 1.f;
-  for (int c = tid; c < D * (kBlockTokens / 4); c += 256) {
-    const int d = c / (kBlockTokens / 4), t4 = c % (kBlockTokens / 4) * 4;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(vb + d * kBlockTokens + t4);
-    const uint32_t n = *reinterpret_cast<const uint32_t *>(&vt[d][t4]);
-    if (fresh || (t4 >= lo && t4 + 4 <= hi)) {
-      *dst = n;
-    } else if (moved || (t4 + 4 > lo && t4 < hi)) {
-      const uint32_t o = *dst;
-      uint32_t r = o;
-      if (moved) {
-        const float2 a = e4m3x2_to_f32(o & 0xffff), c2 = e4m3x2_to_f32(o >> 16);
-        r = e4m3x4(a.x * move[1], a.y * move[1], c2.x * move[1], c2.y * move[1]);
-      }
+  const bool some = t4 + 4 > lo && t4 < hi, all = fresh || (t4 >= lo && t4 + 4 <= hi);
+  if (some || fresh || move[1] != 1.f) {
+    uint32_t mine = 0;  // bytes of the words that are new
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (t4 + j >= lo && t4 + j < hi) r = (r & ~(0xffu << 8 * j)) | (n & (0xffu << 8 * j));
-      *dst = r;
+    for (int i = 0; i < 4; ++i)
+      if (t4 + i >= lo && t4 + i < hi) mine |= 0xffu << 8 * i;
+    float f[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) Vec16<T>::unpack(raw[1][i], f[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint32_t *dst = reinterpret_cast<uint32_t *>(vb + (ch + j) * kBlockTokens + t4);
+      uint32_t w = e4m3x4(f[0][j] * inv[1], f[1][j] * inv[1], f[2][j] * inv[1], f[3][j] * inv[1]);
+      if (!all) {
+        uint32_t o = *dst;
+        if (move[1] != 1.f) o = move_codes(o, move[1]);
+        w = (w & mine) | (o & ~mine);
+      }
+      *dst = w;
     }
   }
 }

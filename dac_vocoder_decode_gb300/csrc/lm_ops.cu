@@ -147,14 +147,51 @@ voc_status finish(const Device &dev, voc_stream_t stream, unsigned flags) {
 bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 bool known_flags(unsigned f) { return (f & ~static_cast<unsigned>(VOC_FLAG_SYNC)) == 0; }
 
+// Threads of a row: as few as hold it in registers, and more of them while there are too few rows
+// to fill the GPU (up to a chunk of values per thread).
+int row_threads(int sms, long long rows, int d, int chunk) {
+  int t = 32;
+  while (t * voc::kRowValues < d) t *= 2;
+  while (t < voc::kRowThreads && t * chunk < d && rows * t < sms * 256ll) t *= 2;
+  return t;
+}
+
+template <typename T, int MODE, int VB>
+cudaError_t launch_rows_vec(int sms, const voc::LmRowsArgs &a, voc_stream_t stream) {
+  constexpr int n = VB / static_cast<int>(sizeof(T));
+  const int tpr = row_threads(sms, a.rows, a.d, n), threads = std::max(128, tpr);
+  const long long per = threads / tpr;
+  return launch(voc::rows_kernel<T, MODE, VB>, dim3(static_cast<unsigned>((a.rows + per - 1) / per)),
+                dim3(threads), 0, 1, stream, a, tpr);
+}
+
+// The widest access that the width, the strides and the buffers allow.
+template <typename T, int MODE>
+cudaError_t launch_rows(int sms, const voc::LmRowsArgs &a, voc_stream_t stream) {
+  if (a.d > voc::kRowThreads * voc::kRowValues)
+    return launch(voc::rows_any_kernel<T, MODE>, dim3(static_cast<unsigned>(a.rows)), dim3(256), 0,
+                  1, stream, a);
+  const size_t e = sizeof(T);
+  auto fits = [&](size_t vb) {  // rows start on vb bytes, codes on as many values
+    const long long n = static_cast<long long>(vb / e);
+    return a.d % n == 0 && a.ldx % n == 0 && (!a.res || a.ldr % n == 0) &&
+           (!a.sum || a.lds % n == 0) && a.ldo % n == 0 && aligned(a.x, vb) &&
+           aligned(a.res, vb) && aligned(a.sum, vb) && aligned(a.w, vb) && aligned(a.out, n);
+  };
+  if (fits(16)) return launch_rows_vec<T, MODE, 16>(sms, a, stream);
+  if (fits(8)) return launch_rows_vec<T, MODE, 8>(sms, a, stream);
+  if (fits(4)) return launch_rows_vec<T, MODE, 4>(sms, a, stream);
+  if constexpr (sizeof(T) == 2)
+    return launch_rows_vec<T, MODE, 2>(sms, a, stream);
+  else
+    return cudaErrorInvalidValue;  // not reached: every f32 buffer is aligned to 4
+}
+
 template <int MODE>
-cudaError_t launch_rows(int dtype, const voc::LmRowsArgs &a, voc_stream_t stream) {
-  const dim3 grid(static_cast<unsigned>(a.rows));
-  if (dtype == VOC_LM_F32)
-    return launch(voc::rows_any_kernel<float, MODE>, grid, dim3(256), 0, 1, stream, a);
-  if (dtype == VOC_LM_F16)
-    return launch(voc::rows_any_kernel<__half, MODE>, grid, dim3(256), 0, 1, stream, a);
-  return launch(voc::rows_any_kernel<__nv_bfloat16, MODE>, grid, dim3(256), 0, 1, stream, a);
+cudaError_t launch_rows(int sms, int dtype, const voc::LmRowsArgs &a, voc_stream_t stream) {
+  if (dtype == VOC_LM_F32) return launch_rows<float, MODE>(sms, a, stream);
+  if (dtype == VOC_LM_F16) return launch_rows<__half, MODE>(sms, a, stream);
+  return launch_rows<__nv_bfloat16, MODE>(sms, a, stream);
 }
 
 }  // namespace
@@ -194,11 +231,11 @@ VOC_API voc_status vocoder_lm_rows_fp8(const void *x, long long ldx, const void 
                     rows, ldx, ldr, lds, ldo, d, eps};
   cudaError_t err;
   if (mode == VOC_LM_RMS)
-    err = launch_rows<voc::kRowsRms>(dtype, a, stream);
+    err = launch_rows<voc::kRowsRms>(dev->sms, dtype, a, stream);
   else if (mode == VOC_LM_NONE)
-    err = launch_rows<voc::kRowsNone>(dtype, a, stream);
+    err = launch_rows<voc::kRowsNone>(dev->sms, dtype, a, stream);
   else
-    err = launch_rows<voc::kRowsGated>(dtype, a, stream);
+    err = launch_rows<voc::kRowsGated>(dev->sms, dtype, a, stream);
   if (err != cudaSuccess) return cuda_fail(err, "launch rows");
   return finish(*dev, stream, flags);
 }
@@ -313,6 +350,12 @@ voc_status check_cache(const void *kc, const void *vc, const float *ks, const fl
   return VOC_OK;
 }
 
+template <typename T, int D>
+cudaError_t launch_append(dim3 grid, const voc::LmAppendArgs &a, voc_stream_t stream) {
+  return launch(voc::append_kernel<T, D>, grid, dim3(voc::AppendShape<D>::kThreads), 0, 1, stream,
+                a);
+}
+
 }  // namespace
 
 VOC_API voc_status vocoder_lm_kv_append(void *k_cache, void *v_cache, float *k_scale,
@@ -341,12 +384,11 @@ VOC_API voc_status vocoder_lm_kv_append(void *k_cache, void *v_cache, float *k_s
   const dim3 grid((max_q - 1 + voc::kBlockTokens - 1) / voc::kBlockTokens + 1, kv_heads, n_seq);
   cudaError_t e;
   if (dtype == VOC_LM_F16)
-    e = head_dim == 64 ? launch(voc::append_kernel<__half, 64>, grid, dim3(256), 0, 1, stream, a)
-                       : launch(voc::append_kernel<__half, 128>, grid, dim3(256), 0, 1, stream, a);
+    e = head_dim == 64 ? launch_append<__half, 64>(grid, a, stream)
+                       : launch_append<__half, 128>(grid, a, stream);
   else
-    e = head_dim == 64
-            ? launch(voc::append_kernel<__nv_bfloat16, 64>, grid, dim3(256), 0, 1, stream, a)
-            : launch(voc::append_kernel<__nv_bfloat16, 128>, grid, dim3(256), 0, 1, stream, a);
+    e = head_dim == 64 ? launch_append<__nv_bfloat16, 64>(grid, a, stream)
+                       : launch_append<__nv_bfloat16, 128>(grid, a, stream);
   if (e != cudaSuccess) return cuda_fail(e, "launch append");
   return finish(*dev, stream, flags);
 }
