@@ -15,6 +15,7 @@
 #include "lm_attention.cuh"
 #include "lm_cache.cuh"
 #include "lm_linear.cuh"
+#include "lm_prompt.cuh"
 #include "lm_rows.cuh"
 
 #define VOC_API extern "C" __attribute__((visibility("default")))
@@ -93,6 +94,10 @@ voc_status device(Device **out) {
     allow_smem(er, attn_rows_kernel<__half, 128>, attn_smem<128>());
     allow_smem(er, attn_rows_kernel<__nv_bfloat16, 64>, attn_smem<64>());
     allow_smem(er, attn_rows_kernel<__nv_bfloat16, 128>, attn_smem<128>());
+    allow_smem(er, attn_prompt_kernel<__half, 64>, PromptSmem<64>::kBytes);
+    allow_smem(er, attn_prompt_kernel<__half, 128>, PromptSmem<128>::kBytes);
+    allow_smem(er, attn_prompt_kernel<__nv_bfloat16, 64>, PromptSmem<64>::kBytes);
+    allow_smem(er, attn_prompt_kernel<__nv_bfloat16, 128>, PromptSmem<128>::kBytes);
     allow_smem(er, linear_few_kernel<float>, kLinSmem);
     allow_smem(er, linear_few_kernel<__half>, kLinSmem);
     allow_smem(er, linear_few_kernel<__nv_bfloat16>, kLinSmem);
@@ -395,39 +400,52 @@ VOC_API voc_status vocoder_lm_kv_append(void *k_cache, void *v_cache, float *k_s
 
 namespace {
 
+// From this many rows (queries that share a key head) of a sequence the attention runs on tiles of
+// 256 rows, below on tiles of 16.
+constexpr int kPromptRows = 33;
+
 struct AttnPlan {
-  int row_tiles = 0, splits = 1;
-  long long tiles = 0;
+  bool prompt = false;
+  int row_tiles = 0;  // tiles of 16 rows
+  int splits = 1;
   size_t ws_bytes = 0;
 };
 
-// How far a sequence's keys are split: enough parts to give every SM one when there are few
-// tiles of rows, each of at least 4 blocks (one round of a CTA's warps).
+// How far a sequence's keys are split: enough parts to give every SM work when there are few tiles
+// of rows, each of at least 4 blocks (one round of the 16-row kernel's warps) or 4 key tiles.
 AttnPlan plan_attention(int sms, int n_seq, int max_q, int heads, int kv_heads, int head_dim,
                         int max_kv, int window) {
   AttnPlan p;
-  const long long group = heads / kv_heads;
-  p.row_tiles = static_cast<int>((group * max_q + voc::kAttnRows - 1) / voc::kAttnRows);
-  p.tiles = static_cast<long long>(n_seq) * kv_heads * p.row_tiles;
+  const long long rows = static_cast<long long>(heads / kv_heads) * max_q;
+  p.prompt = rows >= kPromptRows;
+  p.row_tiles = static_cast<int>((rows + voc::kAttnRows - 1) / voc::kAttnRows);
+  const long long heads_all = static_cast<long long>(n_seq) * kv_heads;
+  const long long tiles =
+      heads_all * (p.prompt ? (rows + voc::kPrRows - 1) / voc::kPrRows : p.row_tiles);
   long long keys = max_kv;
   if (window > 0) keys = std::min<long long>(keys, static_cast<long long>(window) + max_q);
-  const long long blocks = keys / voc::kBlockTokens + 1;
-  long long splits = p.tiles >= sms ? 1 : (2 * sms) / std::max(1ll, p.tiles);
-  splits = std::max(1ll, std::min(splits, blocks / 4));
-  p.splits = static_cast<int>(std::min(splits, 1024ll));
+  const long long steps = keys / (p.prompt ? voc::kPrKeys : voc::kBlockTokens) + 1;
+  long long splits = tiles >= sms ? 1 : (p.prompt ? sms : 2 * sms) / tiles;
+  splits = std::max(1ll, std::min({splits, steps / 4, 65535ll / n_seq, 1024ll}));
+  p.splits = static_cast<int>(splits);
   if (p.splits > 1)
-    p.ws_bytes = static_cast<size_t>(p.tiles) * p.splits * voc::kAttnRows *
+    p.ws_bytes = static_cast<size_t>(heads_all) * p.row_tiles * p.splits * voc::kAttnRows *
                  (static_cast<size_t>(head_dim) * 4 + 8);
   return p;
 }
 
 template <typename T, int D>
-cudaError_t launch_attention(const voc::LmAttnArgs &a, voc_stream_t stream) {
-  cudaError_t e = launch(voc::attn_rows_kernel<T, D>,
-                         dim3(a.splits, a.kv_heads * a.row_tiles, a.n_seq),
-                         dim3(voc::kAttnThreads), voc::attn_smem<D>(), 1, stream, a);
-  if (e != cudaSuccess || a.splits == 1) return e;
+cudaError_t launch_attention(const voc::LmAttnArgs &a, bool prompt, voc_stream_t stream) {
   const int rows = a.group * a.max_q;
+  cudaError_t e;
+  if (prompt)
+    e = launch(voc::attn_prompt_kernel<T, D>,
+               dim3((rows + voc::kPrRows - 1) / voc::kPrRows, a.kv_heads, a.n_seq * a.splits),
+               dim3(voc::kPrThreads), voc::PromptSmem<D>::kBytes, 1, stream, a);
+  else
+    e = launch(voc::attn_rows_kernel<T, D>, dim3(a.splits, a.kv_heads * a.row_tiles, a.n_seq),
+               dim3(voc::kAttnThreads), voc::attn_smem<D>(), 1, stream, a);
+  if (e != cudaSuccess || a.splits == 1) return e;
   return launch(voc::attn_join_kernel<T, D>, dim3((rows + 3) / 4, a.kv_heads, a.n_seq), dim3(128),
                 0, 1, stream, a);
 }
@@ -457,7 +475,7 @@ VOC_API voc_status vocoder_lm_attention(
       st != VOC_OK)
     return st;
   if (!known_flags(flags)) return fail(VOC_INVALID_ARG, "attention: flags");
-  if (heads < kv_heads || heads % kv_heads)
+  if (heads < kv_heads || heads % kv_heads || heads > 65536)
     return fail(VOC_INVALID_ARG, "attention: heads must be a multiple of kv_heads");
   if (max_kv < 0 || window < 0 || (causal != 0 && causal != 1))
     return fail(VOC_INVALID_ARG, "attention: max_kv, window or causal");
@@ -470,8 +488,6 @@ VOC_API voc_status vocoder_lm_attention(
   if (n_tokens == 0 || max_q == 0) return finish(*dev, stream, flags);
   const AttnPlan plan =
       plan_attention(dev->sms, n_seq, max_q, heads, kv_heads, head_dim, max_kv, window);
-  if (static_cast<long long>(plan.row_tiles) * kv_heads > 65535)
-    return fail(VOC_UNSUPPORTED, "attention: too many queries per sequence");
   if (plan.ws_bytes && (!ws || ws_bytes < plan.ws_bytes))
     return fail(VOC_WORKSPACE_TOO_SMALL, "attention: workspace below vocoder_lm_attention_ws_bytes");
   voc::LmAttnArgs a{};
@@ -488,17 +504,18 @@ VOC_API voc_status vocoder_lm_attention(
   if (plan.splits > 1) {
     a.part_o = static_cast<float *>(ws);
     a.part_ml = reinterpret_cast<float2 *>(
-        a.part_o + static_cast<size_t>(plan.tiles) * plan.splits * voc::kAttnRows * head_dim);
+        a.part_o + static_cast<size_t>(n_seq) * kv_heads * plan.row_tiles * plan.splits *
+                       voc::kAttnRows * head_dim);
   }
   a.budget = kWaitBudget;
   a.timeout = dev->timeout;
   cudaError_t e;
   if (dtype == VOC_LM_F16)
-    e = head_dim == 64 ? launch_attention<__half, 64>(a, stream)
-                       : launch_attention<__half, 128>(a, stream);
+    e = head_dim == 64 ? launch_attention<__half, 64>(a, plan.prompt, stream)
+                       : launch_attention<__half, 128>(a, plan.prompt, stream);
   else
-    e = head_dim == 64 ? launch_attention<__nv_bfloat16, 64>(a, stream)
-                       : launch_attention<__nv_bfloat16, 128>(a, stream);
+    e = head_dim == 64 ? launch_attention<__nv_bfloat16, 64>(a, plan.prompt, stream)
+                       : launch_attention<__nv_bfloat16, 128>(a, plan.prompt, stream);
   if (e != cudaSuccess) return cuda_fail(e, "launch attention");
   return finish(*dev, stream, flags);
 }
