@@ -166,4 +166,218 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   if (warp == 5) tmem_dealloc(tmem, p.tmem_cols);
 }
 
+// Many tokens: 256 tokens x 256 channels by a pair of CTAs that share one MMA (cta_group::2).  Each
+// CTA stages its 128 token rows and half of the channels, so the tensor core reads 64 bytes a clock
+// from each SM's shared memory where a 128 x 256 tile of one CTA would read 96 beside the copies'
+// writes.  Persistent; two accumulators, so a tile's output runs beside the next tile's products.
+constexpr int kManyTile = 256;
+constexpr int kManyStage = 2 * 128 * kLinK;  // bytes of a stage in each CTA
+constexpr int kManyStages = 6;
+constexpr int kManyOut = 4 * 32 * 128;       // output staging: 32 rows of 128 bytes for each warp
+constexpr size_t kManySmem = static_cast<size_t>(kManyStages) * kManyStage + kManyOut + 1024;
+
+// 16 bytes of an output row, as far as the row goes (`left` values).
+template <typename T>
+__device__ __forceinline__ void store_out16(T *dst, const uint4 &v, int left) {
+  constexpr int kPer = 16 / static_cast<int>(sizeof(T));
+  if (left >= kPer && (reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
+    *reinterpret_cast<uint4 *>(dst) = v;
+  } else {
+    T e[kPer];
+    memcpy(e, &v, 16);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (i < left) dst[i] = e[i];
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLinThreads, 1) __cluster_dims__(2, 1, 1)
+    linear_many_kernel(const __grid_constant__ CUtensorMap xmap,
+                       const __grid_constant__ CUtensorMap wmap, const LmLinearArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *ring = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  // full: both halves of a stage have landed (the even CTA's barriers count both CTAs' copies)
+  __shared__ __align__(8) uint64_t full[kManyStages], empty[kManyStages], acc_full[2],
+      acc_empty[2], drain, unused;
+  __shared__ __align__(16) float col_scale[2][kManyTile], col_bias[2][kManyTile];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_ctarank();
+  const int m_tiles = (p.M + kManyTile - 1) / kManyTile, n_tiles = (p.N + kManyTile - 1) / kManyTile;
+  const long long jobs = static_cast<long long>(m_tiles) * n_tiles;
+  const long long job0 = cluster_id_x(), step = cluster_count_x();
+  volatile int *abort = &abort_flag;
+  const int never = 0;
+  auto raise = [&]() {
+    *abort = 1;
+    st_cluster_u32(mapa_shared(smem_u32(&abort_flag), rank ^ 1u), 1u);
+    if (p.timeout) *p.timeout = 1;
+  };
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kManyStages; ++i) {
+      mbar_init(smem_u32(full + i), 1);
+      mbar_init(smem_u32(empty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(acc_full + i), 1);
+      mbar_init(smem_u32(acc_empty + i), 2 * 4);  // the epilogue warps of both CTAs
+    }
+    mbar_init(smem_u32(&drain), 1);
+    mbar_init(smem_u32(&unused), 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 5) {
+    tmem_alloc_pair(smem_u32(&tmem_slot), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();  // the other CTA's barriers stand before anything arrives there
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      pdl_wait();
+      const uint32_t full0 = mapa_shared(smem_u32(full), 0u);
+      int it = 0;
+      bool ok = true;
+      for (long long job = job0; job < jobs && ok; job += step) {
+        const int m0 = static_cast<int>(job / n_tiles) * kManyTile + 128 * static_cast<int>(rank);
+        const int n0 = static_cast<int>(job % n_tiles) * kManyTile + 128 * static_cast<int>(rank);
+        for (int c = 0; c < p.chunks; ++c, ++it) {
+          const int st = it % kManyStages;
+          if (it >= kManyStages &&
+              !mbar_wait_cluster(smem_u32(empty + st), (it / kManyStages - 1) & 1, p.budget, abort)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = smem_u32(ring) + st * kManyStage;
+          if (rank == 0) mbar_arrive_expect_tx(smem_u32(full + st), 2 * kManyStage);
+          tma_load_2d_pair(dst, &xmap, full0 + st * 8, c * kLinK, m0);
+          tma_load_2d_pair(dst + kManyStage / 2, &wmap, full0 + st * 8, c * kLinK, n0);
+        }
+      }
+      if (!ok) {
+        raise();
+        // copies in flight land well within this wait, which nothing ends early
+        mbar_wait(smem_u32(&unused), 0, p.budget, &never);
+      }
+    }
+  } else if (warp == 5 && rank == 0) {
+    constexpr uint32_t kId = idesc_e4m3_f32(256, kManyTile);
+    auto wait = [&](uint64_t *bar, int parity) {
+      const bool got = mbar_wait_cluster(smem_u32(bar), parity, p.budget, abort);
+      return __all_sync(0xffffffffu, got) != 0;
+    };
+    int it = 0, k = 0;
+    bool ok = true;
+    for (long long job = job0; job < jobs && ok; job += step, ++k) {
+      const int acc = k & 1;
+      if (k >= 2 && !wait(acc_empty + acc, (k / 2 - 1) & 1)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      for (int c = 0; c < p.chunks; ++c, ++it) {
+        const int st = it % kManyStages, ph = (it / kManyStages) & 1;
+        if (!wait(full + st, ph)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t a = sw128_desc_lo(smem_u32(ring) + st * kManyStage);
+        const uint32_t b = sw128_desc_lo(smem_u32(ring) + st * kManyStage + kManyStage / 2);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          mma_e4m3_warp_lo<true>(tmem + acc * kManyTile, a + 2 * s, b + 2 * s, kSw128DescHi, kId,
+                                 c > 0 || s > 0 ? 1u : 0u);
+        mma_commit_pair_warp(smem_u32(empty + st), 3);
+      }
+      if (ok) mma_commit_pair_warp(smem_u32(acc_full + acc), 3);
+    }
+    if (!ok) raise();
+    mma_commit_pair_warp(smem_u32(&drain), 1);
+    mbar_wait_cluster(smem_u32(&drain), 0, 4 * p.budget, &never);
+    __syncwarp();
+  } else if (warp < 4) {
+    // The accumulator's lanes are token rows.  A warp turns 32 rows x 128 bytes around in shared
+    // memory, so that its stores cover whole lines of 4 rows instead of a sector of 32 rows.
+    pdl_wait();
+    constexpr int kCols = 128 / static_cast<int>(sizeof(T));  // columns of a staged piece
+    constexpr int kPer = 16 / static_cast<int>(sizeof(T));
+    T *out = static_cast<T *>(p.out);
+    const uint32_t empty0 = mapa_shared(smem_u32(acc_empty), 0u);
+    const uint32_t stage = smem_u32(ring) + kManyStages * kManyStage + warp * (32 * 128);
+    int k = 0;
+    for (long long job = job0; job < jobs; job += step, ++k) {
+      const int acc = k & 1;
+      const int row0 = static_cast<int>(job / n_tiles) * kManyTile + 128 * static_cast<int>(rank) +
+                       warp * 32;
+      const int n0 = static_cast<int>(job % n_tiles) * kManyTile;
+      const int cols = min(kManyTile, p.N - n0);
+      for (int c = threadIdx.x; c < kManyTile; c += 128) {
+        col_scale[acc][c] = c < cols ? p.ws[n0 + c] : 0.f;
+        col_bias[acc][c] = p.bias && c < cols ? p.bias[n0 + c] : 0.f;
+      }
+      const float xs = row0 + lane < p.M ? p.xs[row0 + lane] : 0.f;
+      asm volatile("bar.sync 1, 128;" ::: "memory");  // the epilogue warps
+      const bool got = mbar_wait_cluster(smem_u32(acc_full + acc), (k / 2) & 1, 4 * p.budget, abort);
+      if (!__all_sync(0xffffffffu, got)) {
+        if (lane == 0) raise();
+        break;
+      }
+      tc_fence_after();
+      for (int c0 = 0; c0 < cols; c0 += kCols) {
+        uint32_t r[kCols];
+#pragma unroll
+        for (int i = 0; i < kCols / 32; ++i)
+          tmem_ld32_issue(tmem + (static_cast<uint32_t>(warp * 32) << 16) + acc * kManyTile + c0 +
+                              32 * i, r + 32 * i);
+        tmem_ld_wait_all();
+#pragma unroll
+        for (int i = 0; i < kCols / 32; ++i) tmem_ld32_after_wait(r + 32 * i);
+        __syncwarp();  // the previous piece has been read
+#pragma unroll
+        for (int i = 0; i < kCols; i += kPer) {
+          T e[kPer];
+#pragma unroll
+          for (int j = 0; j < kPer; j += 4) {
+            const float4 w = *reinterpret_cast<const float4 *>(&col_scale[acc][c0 + i + j]);
+            const float4 z = *reinterpret_cast<const float4 *>(&col_bias[acc][c0 + i + j]);
+            e[j] = from_f32<T>(fmaf(__uint_as_float(r[i + j]) * xs, w.x, z.x));
+            e[j + 1] = from_f32<T>(fmaf(__uint_as_float(r[i + j + 1]) * xs, w.y, z.y));
+            e[j + 2] = from_f32<T>(fmaf(__uint_as_float(r[i + j + 2]) * xs, w.z, z.z));
+            e[j + 3] = from_f32<T>(fmaf(__uint_as_float(r[i + j + 3]) * xs, w.w, z.w));
+          }
+          uint4 v;
+          memcpy(&v, e, 16);
+          sts128(stage + lane * 128 + (((i / kPer) ^ (lane & 7)) << 4), v);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = 4 * i + lane / 8, u = lane % 8, c = c0 + u * kPer;
+          const uint4 v = lds128(stage + rr * 128 + ((u ^ (rr & 7)) << 4));
+          if (row0 + rr < p.M && c < cols)
+            store_out16(out + static_cast<long long>(row0 + rr) * p.ldo + n0 + c, v, cols - c);
+        }
+      }
+      __syncwarp();
+      tc_fence_before();
+      if (lane == 0) mbar_arrive_cluster(empty0 + acc * 8);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();  // neither CTA leaves while the other may reach its barriers
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
 }  // namespace voc

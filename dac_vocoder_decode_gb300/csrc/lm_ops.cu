@@ -98,6 +98,9 @@ voc_status device(Device **out) {
     allow_smem(er, attn_prompt_kernel<__half, 128>, PromptSmem<128>::kBytes);
     allow_smem(er, attn_prompt_kernel<__nv_bfloat16, 64>, PromptSmem<64>::kBytes);
     allow_smem(er, attn_prompt_kernel<__nv_bfloat16, 128>, PromptSmem<128>::kBytes);
+    allow_smem(er, linear_many_kernel<float>, kManySmem);
+    allow_smem(er, linear_many_kernel<__half>, kManySmem);
+    allow_smem(er, linear_many_kernel<__nv_bfloat16>, kManySmem);
     allow_smem(er, linear_few_kernel<float>, kLinSmem);
     allow_smem(er, linear_few_kernel<__half>, kLinSmem);
     allow_smem(er, linear_few_kernel<__nv_bfloat16>, kLinSmem);
@@ -265,6 +268,19 @@ voc_status encode_rows(CUtensorMap *map, const void *base, long long rows, long 
   return VOC_OK;
 }
 
+// From this many tokens a product runs on 256 x 256 tiles of CTA pairs.
+constexpr int kManyTokens = 512;
+
+template <typename T>
+cudaError_t launch_many(int sms, const CUtensorMap &xm, const CUtensorMap &wm,
+                        const voc::LmLinearArgs &a, voc_stream_t stream) {
+  const long long jobs = static_cast<long long>((a.M + voc::kManyTile - 1) / voc::kManyTile) *
+                         ((a.N + voc::kManyTile - 1) / voc::kManyTile);
+  const unsigned pairs = static_cast<unsigned>(std::min<long long>(sms / 2, jobs));
+  return launch(voc::linear_many_kernel<T>, dim3(2 * pairs), dim3(voc::kLinThreads),
+                voc::kManySmem, 1, stream, xm, wm, a);
+}
+
 template <typename T>
 cudaError_t launch_few(const CUtensorMap &xm, const CUtensorMap &wm, const voc::LmLinearArgs &a,
                        int split, voc_stream_t stream) {
@@ -305,6 +321,20 @@ VOC_API voc_status vocoder_lm_linear_fp8(const void *x8, long long ldx, const fl
   a.budget = kWaitBudget;
   a.timeout = dev->timeout;
   a.chunks = (K + voc::kLinK - 1) / voc::kLinK;
+  CUtensorMap xm, wm;
+  cudaError_t e;
+  if (M >= kManyTokens) {
+    if (voc_status st = encode_rows(&xm, x8, M, K, ldx, 128); st != VOC_OK) return st;
+    if (voc_status st = encode_rows(&wm, w8, N, K, ldw, 128); st != VOC_OK) return st;
+    if (out_dtype == VOC_LM_F32)
+      e = launch_many<float>(dev->sms, xm, wm, a, stream);
+    else if (out_dtype == VOC_LM_F16)
+      e = launch_many<__half>(dev->sms, xm, wm, a, stream);
+    else
+      e = launch_many<__nv_bfloat16>(dev->sms, xm, wm, a, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "launch linear");
+    return finish(*dev, stream, flags);
+  }
   a.nt = std::min(256, (M + 15) / 16 * 16);
   if ((M + a.nt - 1) / a.nt > 65535) return fail(VOC_UNSUPPORTED, "linear: too many rows");
   a.tmem_cols = 32;
@@ -314,10 +344,8 @@ VOC_API voc_status vocoder_lm_linear_fp8(const void *x8, long long ldx, const fl
   const int tiles = ((N + voc::kLinRows - 1) / voc::kLinRows) * ((M + a.nt - 1) / a.nt);
   int split = 1;
   while (split < 8 && tiles * split * 2 <= dev->sms && split * 2 <= a.chunks) split *= 2;
-  CUtensorMap xm, wm;
   if (voc_status st = encode_rows(&xm, x8, M, K, ldx, a.nt); st != VOC_OK) return st;
   if (voc_status st = encode_rows(&wm, w8, N, K, ldw, voc::kLinRows); st != VOC_OK) return st;
-  cudaError_t e;
   if (out_dtype == VOC_LM_F32)
     e = launch_few<float>(xm, wm, a, split, stream);
   else if (out_dtype == VOC_LM_F16)
