@@ -12,10 +12,12 @@
 
 namespace voc {
 
-constexpr int kAttnWarps = 8;                      // consumer warps; one more warp copies
+constexpr int kAttnWarps = 4;                      // consumer warps; one more warp copies
 constexpr int kAttnThreads = 32 * (kAttnWarps + 1);
-constexpr int kAttnRows = 16;                      // rows of a tile (one MMA's M)
-constexpr int kPShift = 14;                        // weights are kept times 2^14 in 16 bits
+constexpr float kLazy = 8.f;    // log2 of how far the weights' maximum may run ahead
+constexpr float kPShift = 7.f;  // weights are kept times 2^7 in 16 bits, so below 2^15
+constexpr int kShareSeqs = 512;   // sequences up to which CTAs take equal shares of the work
+constexpr int kShareMin = 4;      // blocks of the smallest share
 
 struct LmAttnArgs {
   const void *q;
@@ -28,12 +30,22 @@ struct LmAttnArgs {
   int n_pages, table_cols, heads, kv_heads, group, n_seq, n_tokens, max_q;
   float scale_log2;  // softmax_scale * log2(e)
   int causal, window;
-  int row_tiles, splits;
-  float *part_o;     // [tile][split][16][D], splits > 1
-  float2 *part_ml;   // [tile][split][16]
+  int row_tiles;     // of the kernel's own tile size, for max_q tokens
+  int splits;        // prompt kernel: parts of a tile's keys
+  int ctas;          // row kernel: CTAs that share the work, or 0 (one tile each)
+  float *part_o;     // partial outputs [slot][row][D] and their maxima and sums [slot][row]
+  float2 *part_ml;
   long long budget;
   int *timeout;
 };
+
+// The transpose of an 8 x 8 matrix of 16-bit values spread over the warp (row lane/4, columns
+// 2 (lane%4) and the next).
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
 
 // m16n8k16, f16 operands, f32 accumulators.
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -70,29 +82,79 @@ __device__ __forceinline__ KeySpan visible(const LmAttnArgs &p, long long pos, l
   return s;
 }
 
-template <int D>
-__host__ __device__ constexpr int attn_stages() { return D == 128 ? 12 : 24; }
-template <int D>
-__host__ __device__ constexpr size_t attn_smem() {
-  return static_cast<size_t>(attn_stages<D>()) * 2 * kBlockTokens * D + 1024;
+// What the row kernel does for one sequence: its rows, the blocks [blk0, blk0 + blocks) that any of
+// them sees, and the work in blocks over all key heads and row tiles.
+struct SeqWork {
+  SeqSpan span;
+  long long len, p0;
+  int rows, tiles;
+  int blk0, blocks;
+  long long units;
+};
+template <int ROWS>
+__device__ __forceinline__ SeqWork seq_work(const LmAttnArgs &p, int b) {
+  SeqWork w;
+  w.span = seq_span(p.cu, b, p.n_seq, p.n_tokens, p.max_q);
+  w.len = max(0ll, min(static_cast<long long>(p.lens[b]),
+                       static_cast<long long>(p.table_cols) * kBlockTokens));
+  w.p0 = static_cast<long long>(p.lens[b]) - w.span.count;
+  w.rows = w.span.count * p.group;
+  w.tiles = (w.rows + ROWS - 1) / ROWS;
+  const long long lo = visible(p, w.p0, w.len).lo;
+  const long long hi = visible(p, w.p0 + w.span.count - 1, w.len).hi;
+  w.blk0 = static_cast<int>(lo / kBlockTokens);
+  w.blocks = hi > lo ? static_cast<int>((hi - 1) / kBlockTokens) + 1 - w.blk0 : 0;
+  // a tile without keys still has zeros to write: one unit of work
+  w.units = static_cast<long long>(max(w.blocks, 1)) * p.kv_heads * w.tiles;
+  return w;
 }
 
-// 16 rows (queries that share a key head) of one sequence over one part of its keys.  K and V
-// blocks come through a ring of shared-memory stages, one bulk copy each; two warps share a
-// block, 32 keys each, so that a stage is held for half the time.  Both products are 16-bit MMAs:
-// e4m3 converts exactly to f16, and the weights keep 11 bits there (as e4m3 they would keep 4).
-// The order in which a thread holds channels and keys is chosen so that its operands are whole
-// words of the stored rows: the sums do not depend on it.
-template <typename T, int D>
-__global__ void __launch_bounds__(kAttnThreads, 1) attn_rows_kernel(const LmAttnArgs p) {
-  constexpr int kStages = attn_stages<D>();
+// Share of the total work: CTA c has the units [c q, (c + 1) q) in the order (sequence, key head, row
+// tile, block).
+__device__ __forceinline__ long long share_of(long long total, int ctas) {
+  return max((total + ctas - 1) / ctas, static_cast<long long>(kShareMin));
+}
+
+// Ring stages: as many as leave room for two CTAs on an SM.
+template <int D, int NT>
+__host__ __device__ constexpr int attn_stages() { return D == 128 ? (NT == 1 ? 6 : 5) : 12; }
+template <int D, int NT>
+__host__ __device__ constexpr size_t attn_smem() {
+  return static_cast<size_t>(attn_stages<D, NT>()) * 2 * kBlockTokens * D +
+         sizeof(float) * (kAttnWarps / 2) * 8 * NT * (D + 4) + 128;
+}
+
+// One piece of a CTA's share: blocks [first, first + count) of one (sequence, key head, row tile).
+struct Segment {
+  SeqWork w;
+  int b, hk, rt, first, count;
+  bool begins, ends;  // the tile's work starts / ends in this CTA
+};
+
+// Rows (queries that share a key head) in tiles of 8 NT, for the few rows of single tokens.  K and
+// V blocks come through a ring of shared-memory stages, one bulk copy each; two warps share a
+// block, 32 keys each.  The products are taken transposed, S^T = K Q^T and O^T = V^T P^T, so that
+// keys and channels fill the MMA's 16 rows and 8 query rows its columns: with few rows the other
+// way round would leave most of each product empty.  e4m3 converts exactly to f16, and the weights
+// keep 11 bits there (as e4m3 they would keep 4).  The order in which a thread holds channels and
+// keys makes its operands whole words of the stored rows; the sums do not depend on it.
+//
+// The CTAs take equal shares of all blocks of all sequences, whatever their lengths, and a tile
+// that several CTAs share is joined by attn_join_kernel.  Two CTAs per SM.
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttnArgs p) {
+  constexpr int kStages = attn_stages<D, NT>();
   constexpr int kBytes = kBlockTokens * D;
-  constexpr int kSteps = D / 16;   // MMA steps over the channels
-  constexpr int kTilesD = D / 8;   // output column tiles
-  extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr int kRows = 8 * NT;
+  constexpr int kSteps = D / 16;   // MMA steps over the channels, and output tiles of 16 channels
+  constexpr int kLd = D + 4;       // row stride of the join buffer: a warp's stores spread over banks
+  extern __shared__ __align__(128) uint8_t smem[];
+  float *acc = reinterpret_cast<float *>(smem + kStages * 2 * kBytes);  // [two warps][row][kLd]
   __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
+  __shared__ float4 scales[kStages];  // key scale, log2 and reciprocal of the value scale, page or none
+  __shared__ long long prefix[kShareSeqs + 1];
+  __shared__ float2 ml[kAttnWarps][kRows];
   __shared__ int abort_flag;
-  __shared__ float2 ml[kAttnWarps][kAttnRows];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int g = lane / 4, t = lane % 4;
   if (tid == 0) {
@@ -103,282 +165,469 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_rows_kernel(const LmAttn
     abort_flag = 0;
     fence_barrier_init();
   }
-  __syncthreads();
   pdl_wait();
-
-  const int b = blockIdx.z, hk = blockIdx.y / p.row_tiles, rt = blockIdx.y % p.row_tiles;
-  const int split = blockIdx.x;
-  const SeqSpan span = seq_span(p.cu, b, p.n_seq, p.n_tokens, p.max_q);
-  const int rows = span.count * p.group;
-  const int r0 = rt * kAttnRows;
-  if (r0 >= rows) return;  // the whole block
-  const int r_last = min(rows, r0 + kAttnRows) - 1;
-  const long long len = max(0ll, min(static_cast<long long>(p.lens[b]),
-                                     static_cast<long long>(p.table_cols) * kBlockTokens));
-  const long long p0 = static_cast<long long>(p.lens[b]) - span.count;
-  const long long key_lo = visible(p, p0 + r0 / p.group, len).lo;
-  const long long key_hi = visible(p, p0 + r_last / p.group, len).hi;
-  const long long blk0 = key_lo / kBlockTokens;
-  const long long n_blk = key_hi > key_lo ? (key_hi - 1) / kBlockTokens + 1 - blk0 : 0;
-  const long long per = (n_blk + p.splits - 1) / p.splits;
-  const int first = static_cast<int>(blk0 + min(n_blk, split * per));
-  const int count = static_cast<int>(min(n_blk, (split + 1) * per) - min(n_blk, split * per));
-  const int *table = p.table + b * p.ldt;
-
-  float o[kTilesD][4];
+  pdl_launch_dependents();
+  long long lo, hi;  // this CTA's units
+  if (p.ctas) {
+    for (int i = tid; i < p.n_seq; i += kAttnThreads) prefix[i + 1] = seq_work<kRows>(p, i).units;
+    __syncthreads();
+    if (warp == 0) {  // running sums, 32 at a time
+      long long base = 0;
+      for (int i0 = 0; i0 < p.n_seq; i0 += 32) {
+        long long v = i0 + lane < p.n_seq ? prefix[i0 + lane + 1] : 0;
 #pragma unroll
-  for (int i = 0; i < kTilesD; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        for (int o = 1; o < 32; o *= 2) {
+          const long long u = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += u;
+        }
+        if (i0 + lane < p.n_seq) prefix[i0 + lane + 1] = base + v;
+        base += __shfl_sync(0xffffffffu, v, 31);
+      }
+      if (lane == 0) prefix[0] = 0;
+    }
+    __syncthreads();
+    const long long total = prefix[p.n_seq], q = share_of(total, p.ctas);
+    lo = min(total, blockIdx.x * q);
+    hi = min(total, lo + q);
+  } else {
+    __syncthreads();
+    lo = 0, hi = 1;
+  }
+  if (lo >= hi) return;  // the whole block
+  // the piece of work that starts at unit `at`, and the unit after it
+  auto segment = [&](long long at, long long &next) {
+    Segment s;
+    if (p.ctas) {
+      int a = 0, z = p.n_seq - 1;
+      while (a < z) {
+        const int mid = (a + z + 1) / 2;
+        if (prefix[mid] <= at)
+          a = mid;
+        else
+          z = mid - 1;
+      }
+      s.b = a;
+      s.w = seq_work<kRows>(p, a);
+      const int per = max(s.w.blocks, 1);
+      const int tile = static_cast<int>((at - prefix[a]) / per);
+      const int begin = static_cast<int>((at - prefix[a]) % per);
+      const int end = static_cast<int>(min(static_cast<long long>(per), begin + (hi - at)));
+      s.hk = tile / s.w.tiles, s.rt = tile % s.w.tiles;
+      s.begins = begin == 0, s.ends = end == per;
+      s.first = s.w.blk0 + begin;
+      s.count = min(end, s.w.blocks) - begin;
+      next = at + (end - begin);
+    } else {
+      s.b = blockIdx.z, s.hk = blockIdx.y, s.rt = blockIdx.x;
+      s.w = seq_work<kRows>(p, s.b);
+      s.begins = s.ends = true;
+      s.first = s.w.blk0;
+      s.count = s.rt < s.w.tiles ? s.w.blocks : 0;
+      next = hi;
+    }
+    return s;
+  };
 
   if (warp == kAttnWarps) {
-    if (lane == 0) {
-      int done = 0;
-      for (int i = 0; i < count; ++i) {
-        const int st = i % kStages;
-        if (i >= kStages &&
-            !mbar_wait(smem_u32(empty + st), (i / kStages - 1) & 1, p.budget, &abort_flag)) {
-          *static_cast<volatile int *>(&abort_flag) = 1;
-          break;
+    // ---------------------------------------------------------------- copies
+    int it = 0;
+    bool ok = true;
+    for (long long at = lo, next; at < hi && ok; at = next) {
+      const Segment s = segment(at, next);
+      const int *table = p.table + s.b * p.ldt;
+      // pages and scales of 32 blocks at a time, a lane each, the next 32 while these are copied
+      auto fetch = [&](int i0, int &page, float &ks, float &vs) {
+        page = -1, ks = 1.f, vs = 1.f;
+        if (i0 + lane < s.count) {
+          page = table[s.first + i0 + lane];
+          if (page < 0 || page >= p.n_pages) {
+            page = -1;
+          } else {
+            const long long slot = static_cast<long long>(page) * p.kv_heads + s.hk;
+            ks = p.ks[slot], vs = fmaxf(p.vs[slot], kScaleMin);
+          }
         }
-        const int page = table[first + i];
-        if (page < 0 || page >= p.n_pages) {
-          mbar_arrive(smem_u32(full + st));
-        } else {
-          const long long at = (static_cast<long long>(page) * p.kv_heads + hk) * kBytes;
-          const uint32_t bar = smem_u32(full + st), dst = smem_u32(smem + st * 2 * kBytes);
-          mbar_arrive_expect_tx(bar, 2 * kBytes);
-          bulk_load(dst, p.kc + at, kBytes, bar);
-          bulk_load(dst + kBytes, p.vc + at, kBytes, bar);
+      };
+      int page, page2;
+      float ks, vs, ks2, vs2;
+      fetch(0, page, ks, vs);
+      for (int i0 = 0; i0 < s.count && ok; i0 += 32) {
+        fetch(i0 + 32, page2, ks2, vs2);
+        const float lvs = log2f(vs), ivs = 1.f / vs;
+        for (int j = 0; j < 32 && i0 + j < s.count; ++j, ++it) {
+          const int st = it % kStages;
+          if (it >= kStages) {
+            const bool free = mbar_wait(smem_u32(empty + st), (it / kStages - 1) & 1, p.budget,
+                                        &abort_flag);
+            if (!__all_sync(0xffffffffu, free)) {
+              *static_cast<volatile int *>(&abort_flag) = 1;
+              ok = false;
+              break;
+            }
+          }
+          const int pg = __shfl_sync(0xffffffffu, page, j);
+          if (lane == j) scales[st] = make_float4(ks, lvs, ivs, page < 0 ? 0.f : 1.f);
+          __syncwarp();
+          if (lane == 0) {
+            const uint32_t bar = smem_u32(full + st), dst = smem_u32(smem + st * 2 * kBytes);
+            if (pg < 0) {
+              mbar_arrive(bar);
+            } else {
+              const long long from = (static_cast<long long>(pg) * p.kv_heads + s.hk) * kBytes;
+              mbar_arrive_expect_tx(bar, 2 * kBytes);
+              bulk_load(dst, p.kc + from, kBytes, bar);
+              bulk_load(dst + kBytes, p.vc + from, kBytes, bar);
+            }
+          }
         }
-        done = i + 1;
-      }
-      if (*static_cast<volatile int *>(&abort_flag)) {  // leave with no copy in flight
-        const int never = 0;
-        for (int i = max(0, done - kStages); i < done; ++i)
-          mbar_wait(smem_u32(full + i % kStages), (i / kStages) & 1, p.budget, &never);
-        if (p.timeout) *p.timeout = 1;
+        page = page2, ks = ks2, vs = vs2;
       }
     }
-  } else {
-    // queries: rows g and g + 8 of the tile, scaled into f16
-    uint32_t qa[kSteps][4];
-    float qc[2];
-    int row_tok[2];
-    KeySpan see[2];
+    if (!ok && lane == 0) {  // leave with no copy in flight
+      const int never = 0;
+      for (int i = max(0, it - kStages); i < it; ++i)
+        mbar_wait(smem_u32(full + i % kStages), (i / kStages) & 1, p.budget, &never);
+      if (p.timeout) *p.timeout = 1;
+    }
+    return;
+  }
+
+  // ------------------------------------------------------------------ products
+  const int pair = warp / 2, half = warp % 2;
+  int it = 0;
+  bool ok = true;
+  for (long long at = lo, next; at < hi; at = next) {
+    const Segment s = segment(at, next);
+    const int r0 = s.rt * kRows, r_last = min(s.w.rows, r0 + kRows) - 1;
+    if (r0 > r_last) continue;  // whole-tile launches cover max_q tokens
+    // queries as the second operand: row g of each 8 rows, two halves of f16 per step
+    uint32_t qb[NT][kSteps][2];
+    float qc[NT][2];
+    int see_lo[NT][2], see_hi[NT][2];  // of rows 2t and 2t + 1, relative to the segment's first key
+    const long long key0 = static_cast<long long>(s.first) * kBlockTokens;
+    const long long key_lo = visible(p, s.w.p0 + r0 / p.group, s.w.len).lo;
+    const long long key_hi = visible(p, s.w.p0 + r_last / p.group, s.w.len).hi;
+    auto rel = [&](long long key) {
+      return static_cast<int>(max(-1ll, min(key - key0, 0x7fffffffll)));
+    };
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = min(r0 + g + 8 * h, r_last);  // spare rows repeat the last one
-      row_tok[h] = r / p.group;
-      see[h] = visible(p, p0 + row_tok[h], len);
-      const T *src = static_cast<const T *>(p.q) + (span.first + row_tok[h]) * p.ldq +
-                     (hk * p.group + r % p.group) * p.hsq;
-      float f[D / 4];
+    for (int n = 0; n < NT; ++n) {
+      const int r = min(r0 + 8 * n + g, r_last);  // spare rows repeat the last one
+      const T *src = static_cast<const T *>(p.q) +
+                     (s.w.span.first + r / p.group) * p.ldq + (s.hk * p.group + r % p.group) * p.hsq;
+      const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
+      uint4 raw[D / 64][2];
       uint32_t a = 0;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s)
+      for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float v = to_f32(src[64 * (s / 4) + 16 * t + 4 * (s % 4) + j]);
-          f[4 * s + j] = v;
-          if (abs_bits(v) < kInfBits) a = max(a, abs_bits(v));
+        for (int h = 0; h < 2; ++h) {
+          const T *at16 = src + 64 * c + 16 * t + 8 * h;
+          if (vec) {
+            raw[c][h] = *reinterpret_cast<const uint4 *>(at16);
+          } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint16_t *u = reinterpret_cast<const uint16_t *>(at16) + 2 * j;
+              w[j] = u[0] | static_cast<uint32_t>(u[1]) << 16;
+            }
+            raw[c][h] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          float f[8];
+          Vec16<T>::unpack(raw[c][h], f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (abs_bits(f[j]) < kInfBits) a = max(a, abs_bits(f[j]));
         }
       a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
       a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
       const int e = query_exponent(a);
-      const float up = pow2(e);
-      qc[h] = p.scale_log2 * pow2(-e);
+      const float up = p.scale_log2 < 0.f ? -pow2(e) : pow2(e);  // scores are scaled by >= 0
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        qa[s][h] = f16x2(f[4 * s] * up, f[4 * s + 1] * up);
-        qa[s][2 + h] = f16x2(f[4 * s + 2] * up, f[4 * s + 3] * up);
-      }
-    }
-    const int half = warp % 2;
-    for (int i = warp / 2; i < count; i += kAttnWarps / 2) {
-      const int st = i % kStages;
-      const bool landed = mbar_wait(smem_u32(full + st), (i / kStages) & 1, p.budget, &abort_flag);
-      if (!__all_sync(0xffffffffu, landed)) {
-        *static_cast<volatile int *>(&abort_flag) = 1;
-        break;
-      }
-      const int page = table[first + i];
-      const long long base = static_cast<long long>(first + i) * kBlockTokens + 32 * half;
-      if (page >= 0 && page < p.n_pages && base < key_hi && base + 32 > key_lo) {
-        const long long slot = static_cast<long long>(page) * p.kv_heads + hk;
-        const float ks = p.ks[slot], vs = fmaxf(p.vs[slot], kScaleMin);
-        const float lvs = log2f(vs), ivs = 1.f / vs;
-        const uint32_t kb = smem_u32(smem + st * 2 * kBytes), vb = kb + kBytes;
-        // scores: column 2t + e of tile j is key 8t + 2j + e
-        float sc[4][4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) sc[j][x] = 0.f;
-          const uint32_t row = kb + (32 * half + 8 * (g >> 1) + 2 * j + (g & 1)) * D + 16 * t;
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            const uint4 w = lds128(row + 64 * c);
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-              mma_f16(sc[j], qa[4 * c + s], e4m3x2_to_f16x2(ww[s] & 0xffff),
-                      e4m3x2_to_f16x2(ww[s] >> 16));
-          }
-        }
-        // u = s + log2(vs), -inf where the row does not see the key
-        const bool whole = base >= max(see[0].lo, see[1].lo) && base + 32 <= min(see[0].hi, see[1].hi);
-        float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int h = x / 2;
-            float u = fmaf(sc[j][x], qc[h] * ks, lvs);
-            if (!whole) {
-              const long long key = base + 8 * t + 2 * j + x % 2;
-              if (key < see[h].lo || key >= see[h].hi) u = -INFINITY;
-            }
-            sc[j][x] = u;
-            top[h] = fmaxf(top[h], u);
-          }
-        float alpha[2], off[2];
+      for (int c = 0; c < D / 64; ++c)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-          top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-          const float nm = fmaxf(m[h], top[h]);
-          alpha[h] = m[h] == nm ? 1.f : exp2f(m[h] - nm);
-          m[h] = nm;
-          off[h] = (nm == -INFINITY ? 0.f : nm) - kPShift;
+          float f[8];
+          Vec16<T>::unpack(raw[c][h], f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            qb[n][4 * c + 2 * h + j / 2][j % 2] = f16x2(f[2 * j] * up, f[2 * j + 1] * up);
         }
-        float sum[2] = {0.f, 0.f};
-        uint32_t pa[2][4];
+      const float mine = fabsf(p.scale_log2) * pow2(-e);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float w[4];
+      for (int x = 0; x < 2; ++x) {
+        qc[n][x] = __shfl_sync(0xffffffffu, mine, 4 * (2 * t + x));
+        const int rr = min(r0 + 8 * n + 2 * t + x, r_last);
+        const KeySpan k = visible(p, s.w.p0 + rr / p.group, s.w.len);
+        see_lo[n][x] = rel(k.lo), see_hi[n][x] = rel(k.hi);
+      }
+    }
+    const int all_lo = rel(visible(p, s.w.p0 + r_last / p.group, s.w.len).lo);   // seen by every row
+    const int all_hi = rel(visible(p, s.w.p0 + r0 / p.group, s.w.len).hi);
+    const int any_lo = rel(key_lo), any_hi = rel(key_hi);                        // seen by some row
+
+    float o[NT][kSteps][4];
+    float m[NT][2], l[NT][2];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            w[x] = exp2f(sc[j][x] - off[x / 2]);
-            sum[x / 2] += w[x];
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[n][i][j] = 0.f;
+      m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
+    }
+
+    for (int i = 0; i < s.count; ++i, ++it) {
+      if ((it & 1) != pair) continue;
+      const int st = it % kStages;
+      if (ok) {
+        ok = mbar_wait(smem_u32(full + st), (it / kStages) & 1, p.budget, &abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) *static_cast<volatile int *>(&abort_flag) = 1;
+      }
+      const int base = i * kBlockTokens + 32 * half;  // relative to key0
+      const float4 sc4 = scales[st];
+      if (ok && sc4.w != 0.f && base < any_hi && base + 32 > any_lo) {
+        const uint32_t kb = smem_u32(smem + st * 2 * kBytes), vb = kb + kBytes;
+        // scores: row g (g + 8) of tile j is key 8 (g / 2) + 4 j + g % 2 (+ 2)
+        float sc[NT][2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) sc[n][j][x] = 0.f;
+          const uint32_t row = kb + (32 * half + 8 * (g >> 1) + 4 * j + (g & 1)) * D + 16 * t;
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            const uint4 w0 = lds128(row + 64 * c), w1 = lds128(row + 2 * D + 64 * c);
+            const uint32_t a0[4] = {w0.x, w0.y, w0.z, w0.w}, a1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t a[4] = {e4m3x2_to_f16x2(a0[k] & 0xffff), e4m3x2_to_f16x2(a1[k] & 0xffff),
+                                     e4m3x2_to_f16x2(a0[k] >> 16), e4m3x2_to_f16x2(a1[k] >> 16)};
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma_f16(sc[n][j], a, qb[n][4 * c + k][0], qb[n][4 * c + k][1]);
+            }
           }
-          pa[j / 2][2 * (j % 2)] = f16x2(w[0], w[1]);
-          pa[j / 2][2 * (j % 2) + 1] = f16x2(w[2], w[3]);
         }
+        if (base < all_lo || base + 32 > all_hi) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) l[h] = l[h] * alpha[h] + sum[h] * ivs;
-        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int n = 0; n < kTilesD; ++n) {
-            o[n][0] *= alpha[0], o[n][1] *= alpha[0];
-            o[n][2] *= alpha[1], o[n][3] *= alpha[1];
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const int key = base + 8 * (g >> 1) + 4 * j + (g & 1) + x / 2 * 2;
+                if (key < see_lo[n][x % 2] || key >= see_hi[n][x % 2]) sc[n][j][x] = -INFINITY;
+              }
+        }
+        // u = s + log2(vs); the maximum is raised only when some weight would leave f16
+        bool raise = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float c = fmaxf(qc[n][x] * sc4.x, 1e-37f);  // above 0: masked scores stay -inf
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              sc[n][j][x] = fmaf(sc[n][j][x], c, sc4.y);
+              sc[n][j][x + 2] = fmaf(sc[n][j][x + 2], c, sc4.y);
+            }
+            const float top = fmaxf(fmaxf(sc[n][0][x], sc[n][0][x + 2]),
+                                    fmaxf(sc[n][1][x], sc[n][1][x + 2]));
+            raise |= top > m[n][x] + kLazy;
           }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float top = fmaxf(fmaxf(sc[n][0][x], sc[n][0][x + 2]),
+                                fmaxf(sc[n][1][x], sc[n][1][x + 2]));
+#pragma unroll
+              for (int z = 4; z < 32; z *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, z));
+              const float nm = fmaxf(m[n][x], top);
+              const float alpha = m[n][x] == nm ? 1.f : ex2(m[n][x] - nm);
+              m[n][x] = nm;
+              l[n][x] *= alpha;
+#pragma unroll
+              for (int i2 = 0; i2 < kSteps; ++i2) o[n][i2][x] *= alpha, o[n][i2][x + 2] *= alpha;
+            }
         }
-        // codes of keys outside the tile's span count as zero, whatever they hold
+        uint32_t pb[NT][2][2];  // weights as the second operand: keys by row
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float off[2], sum[2] = {0.f, 0.f};
+#pragma unroll
+          for (int x = 0; x < 2; ++x) off[x] = (m[n][x] == -INFINITY ? 0.f : m[n][x]) - kPShift;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              w[x] = ex2(sc[n][j][x] - off[x % 2]);
+              sum[x % 2] += w[x];
+            }
+            pb[n][j][0] = transpose8(f16x2(w[0], w[1]));
+            pb[n][j][1] = transpose8(f16x2(w[2], w[3]));
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) l[n][x] = fmaf(sum[x], sc4.z, l[n][x]);
+        }
+        // codes of keys that no row sees count as zero, whatever they hold
         uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-        if (base < key_lo || base + 32 > key_hi) {
+        if (base < any_lo || base + 32 > any_hi) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const long long key = base + 8 * t + j;
-            if (key < key_lo || key >= key_hi) keep[j / 4] &= ~(0xffu << 8 * (j % 4));
+            const int key = base + 8 * t + j;
+            if (key < any_lo || key >= any_hi) keep[j / 4] &= ~(0xffu << 8 * (j % 4));
           }
         }
 #pragma unroll
-        for (int n = 0; n < kTilesD; ++n) {
-          uint32_t v0, v1;
-          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                       : "=r"(v0), "=r"(v1)
-                       : "r"(vb + (8 * n + g) * kBlockTokens + 32 * half + 8 * t)
-                       : "memory");
-          v0 &= keep[0], v1 &= keep[1];
-          mma_f16(o[n], pa[0], e4m3x2_to_f16x2(v0 & 0xffff), e4m3x2_to_f16x2(v0 >> 16));
-          mma_f16(o[n], pa[1], e4m3x2_to_f16x2(v1 & 0xffff), e4m3x2_to_f16x2(v1 >> 16));
+        for (int i2 = 0; i2 < kSteps; ++i2) {
+          uint32_t v[2][2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                         : "=r"(v[x][0]), "=r"(v[x][1])
+                         : "r"(vb + (16 * i2 + 8 * x + g) * kBlockTokens + 32 * half + 8 * t)
+                         : "memory");
+            v[x][0] &= keep[0], v[x][1] &= keep[1];
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t a[4] = {e4m3x2_to_f16x2(v[0][j] & 0xffff),
+                                   e4m3x2_to_f16x2(v[1][j] & 0xffff),
+                                   e4m3x2_to_f16x2(v[0][j] >> 16), e4m3x2_to_f16x2(v[1][j] >> 16)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16(o[n][i2], a, pb[n][j][0], pb[n][j][1]);
+          }
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(empty + st));
     }
+
+    // join the warps: each scales its rows to the common maximum
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-    }
-    if (t == 0) {
-      ml[warp][g] = make_float2(m[0], l[0]);
-      ml[warp][g + 8] = make_float2(m[1], l[1]);
-    }
-  }
-  __syncthreads();  // the ring is free: every copy has been waited for
-  // join the warps: each scales its rows to the common maximum
-  float *acc = reinterpret_cast<float *>(smem);  // [warp][16][D]
-  if (warp < kAttnWarps) {
-    float f[2];
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+      for (int x = 0; x < 2; ++x) {
+#pragma unroll
+        for (int z = 4; z < 32; z *= 2) l[n][x] += __shfl_xor_sync(0xffffffffu, l[n][x], z);
+        if (g == 0) ml[warp][8 * n + 2 * t + x] = make_float2(m[n][x], l[n][x]);
+      }
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    // warps 2 and 3 hand their parts to 0 and 1, which add their own
+#pragma unroll
+    for (int turn = 1; turn >= 0; --turn) {
+      if (warp / 2 == turn) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float top = -INFINITY;
+            for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, ml[w][8 * n + 2 * t + x].x);
+            const float f = top == -INFINITY ? 0.f : ex2(m[n][x] - top);
+            float *row = acc + (warp % 2 * kRows + 8 * n + 2 * t + x) * kLd + g;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+              row[16 * i] = fmaf(o[n][i][x], f, turn ? 0.f : row[16 * i]);
+              row[16 * i + 8] = fmaf(o[n][i][x + 2], f, turn ? 0.f : row[16 * i + 8]);
+            }
+          }
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+    }
+    for (int i = tid; i < kRows * D; i += 32 * kAttnWarps) {
+      const int r = i / D, d = i % D;
+      if (r0 + r > r_last) break;
       float top = -INFINITY;
-      for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, ml[w][g + 8 * h].x);
-      f[h] = top == -INFINITY ? 0.f : exp2f(m[h] - top);
+      for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, ml[w][r].x);
+      float sum = 0.f, v = 0.f;
+      for (int w = 0; w < kAttnWarps; ++w)
+        // a warp that saw no key has a sum of 0, or NaN where it met NaN alone
+        sum += ml[w][r].x == -INFINITY ? ml[w][r].y : ml[w][r].y * ex2(ml[w][r].x - top);
+      v = acc[r * kLd + d] + acc[(kRows + r) * kLd + d];
+      if (s.begins && s.ends) {
+        const int tok = (r0 + r) / p.group, h = s.hk * p.group + (r0 + r) % p.group;
+        static_cast<T *>(p.out)[(s.w.span.first + tok) * p.ldo + h * p.hso + d] =
+            from_f32<T>(sum == 0.f ? 0.f : v / sum);
+      } else {  // slot 2c: the tile began in an earlier CTA, 2c + 1: it begins here
+        const long long slot = (2ll * blockIdx.x + (s.begins ? 1 : 0)) * kRows + r;
+        p.part_o[slot * D + d] = v;
+        if (d == 0) p.part_ml[slot] = make_float2(top, sum);
+      }
     }
-#pragma unroll
-    for (int n = 0; n < kTilesD; ++n) {
-      float *row = acc + (warp * kAttnRows + g) * D + 8 * n + 2 * t;
-      *reinterpret_cast<float2 *>(row) = make_float2(o[n][0] * f[0], o[n][1] * f[0]);
-      *reinterpret_cast<float2 *>(row + 8 * D) = make_float2(o[n][2] * f[1], o[n][3] * f[1]);
-    }
-  }
-  __syncthreads();
-  const long long tile = (static_cast<long long>(b) * p.kv_heads + hk) * p.row_tiles + rt;
-  for (int i = tid; i < kAttnRows * D; i += kAttnThreads) {
-    const int r = i / D, d = i % D;
-    float top = -INFINITY;
-    for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, ml[w][r].x);
-    float sum = 0.f, v = 0.f;
-    for (int w = 0; w < kAttnWarps; ++w) {
-      // a warp that saw no key has a sum of 0, or NaN where it met NaN alone
-      sum += ml[w][r].x == -INFINITY ? ml[w][r].y : ml[w][r].y * exp2f(ml[w][r].x - top);
-      v += acc[(w * kAttnRows + r) * D + d];
-    }
-    if (p.splits > 1) {
-      const long long at = (tile * p.splits + split) * kAttnRows + r;
-      p.part_o[at * D + d] = v;
-      if (d == 0) p.part_ml[at] = make_float2(top, sum);
-    } else if (r0 + r <= r_last) {
-      const int tok = (r0 + r) / p.group, h = hk * p.group + (r0 + r) % p.group;
-      static_cast<T *>(p.out)[(span.first + tok) * p.ldo + h * p.hso + d] =
-          from_f32<T>(sum == 0.f ? 0.f : v / sum);
-    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");  // the buffers are free for the next piece
   }
 }
 
-// Joins the parts of a row: one warp per row.
-template <typename T, int D>
+// Joins the parts of a tile's row, one warp per row.  ROWS = 8 NT: the row kernel's shares;
+// ROWS = 16: the prompt kernel's splits, [tile of 16 rows][split][16].
+template <typename T, int D, int ROWS, bool SHARES>
 __global__ void __launch_bounds__(128) attn_join_kernel(const LmAttnArgs p) {
+  __shared__ long long red[4];
   pdl_wait();
-  const int lane = threadIdx.x % 32;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int b = blockIdx.z, hk = blockIdx.y;
+  const int row = blockIdx.x * 4 + warp;
   const SeqSpan span = seq_span(p.cu, b, p.n_seq, p.n_tokens, p.max_q);
-  const int row = blockIdx.x * 4 + threadIdx.x / 32;
+  long long c0 = 0, c1 = 0;
+  if (SHARES) {
+    // the work before this sequence and in all, as attn_rows_kernel counts it
+    long long before = 0, total = 0;
+    for (int i = threadIdx.x; i < p.n_seq; i += 128) {
+      const long long u = seq_work<ROWS>(p, i).units;
+      total += u;
+      if (i < b) before += u;
+    }
+    long long both[2] = {before, total};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int o = 16; o; o /= 2) both[k] += __shfl_xor_sync(0xffffffffu, both[k], o);
+      __syncthreads();
+      if (lane == 0) red[warp] = both[k];
+      __syncthreads();
+      both[k] = red[0] + red[1] + red[2] + red[3];
+    }
+    const SeqWork w = seq_work<ROWS>(p, b);
+    const int per = max(w.blocks, 1);
+    const long long q = share_of(both[1], p.ctas);
+    const long long at = both[0] + (static_cast<long long>(hk) * w.tiles + row / ROWS) * per;
+    c0 = at / q, c1 = (at + per - 1) / q;
+  }
   if (row >= span.count * p.group) return;
+  if (SHARES && c0 == c1) return;  // one CTA had the whole tile
   const long long tile =
-      (static_cast<long long>(b) * p.kv_heads + hk) * p.row_tiles + row / kAttnRows;
-  const long long at = tile * p.splits * kAttnRows + row % kAttnRows;
+      (static_cast<long long>(b) * p.kv_heads + hk) * p.row_tiles + row / ROWS;
+  const int parts = SHARES ? static_cast<int>(c1 - c0 + 1) : p.splits;
+  auto slot_of = [&](int s) {
+    const long long slot = SHARES ? (s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) : tile * p.splits + s;
+    return slot * ROWS + row % ROWS;
+  };
   float top = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_ml[at + s * kAttnRows].x);
+  for (int s = lane; s < parts; s += 32) top = fmaxf(top, p.part_ml[slot_of(s)].x);
+#pragma unroll
+  for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   float sum = 0.f, v[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) v[i] = 0.f;
-  for (int s = 0; s < p.splits; ++s) {
-    const float2 x = p.part_ml[at + s * kAttnRows];
+  for (int s = 0; s < parts; ++s) {
+    const long long at = slot_of(s);
+    const float2 x = p.part_ml[at];
     if (x.x == -INFINITY) {  // nothing visible in this part, or NaN alone
       sum += x.y;
       continue;
     }
-    const float f = exp2f(x.x - top);
+    const float f = ex2(x.x - top);
     sum += x.y * f;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-      v[i] += f * p.part_o[(at + s * kAttnRows) * D + lane + 32 * i];
+    for (int i = 0; i < D / 32; ++i) v[i] += f * p.part_o[at * D + lane + 32 * i];
   }
   const int tok = row / p.group, h = hk * p.group + row % p.group;
   T *dst = static_cast<T *>(p.out) + (span.first + tok) * p.ldo + h * p.hso;

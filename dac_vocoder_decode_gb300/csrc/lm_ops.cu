@@ -90,10 +90,14 @@ voc_status device(Device **out) {
     void *t = nullptr;
     if (er == cudaSuccess) er = cudaGetSymbolAddress(&t, g_timeout);
     dev.timeout = static_cast<int *>(t);
-    allow_smem(er, attn_rows_kernel<__half, 64>, attn_smem<64>());
-    allow_smem(er, attn_rows_kernel<__half, 128>, attn_smem<128>());
-    allow_smem(er, attn_rows_kernel<__nv_bfloat16, 64>, attn_smem<64>());
-    allow_smem(er, attn_rows_kernel<__nv_bfloat16, 128>, attn_smem<128>());
+    allow_smem(er, attn_rows_kernel<__half, 64, 1>, attn_smem<64, 1>());
+    allow_smem(er, attn_rows_kernel<__half, 64, 2>, attn_smem<64, 2>());
+    allow_smem(er, attn_rows_kernel<__half, 128, 1>, attn_smem<128, 1>());
+    allow_smem(er, attn_rows_kernel<__half, 128, 2>, attn_smem<128, 2>());
+    allow_smem(er, attn_rows_kernel<__nv_bfloat16, 64, 1>, attn_smem<64, 1>());
+    allow_smem(er, attn_rows_kernel<__nv_bfloat16, 64, 2>, attn_smem<64, 2>());
+    allow_smem(er, attn_rows_kernel<__nv_bfloat16, 128, 1>, attn_smem<128, 1>());
+    allow_smem(er, attn_rows_kernel<__nv_bfloat16, 128, 2>, attn_smem<128, 2>());
     allow_smem(er, attn_prompt_kernel<__half, 64>, PromptSmem<64>::kBytes);
     allow_smem(er, attn_prompt_kernel<__half, 128>, PromptSmem<128>::kBytes);
     allow_smem(er, attn_prompt_kernel<__nv_bfloat16, 64>, PromptSmem<64>::kBytes);
@@ -429,53 +433,76 @@ VOC_API voc_status vocoder_lm_kv_append(void *k_cache, void *v_cache, float *k_s
 namespace {
 
 // From this many rows (queries that share a key head) of a sequence the attention runs on tiles of
-// 256 rows, below on tiles of 16.
+// 256 rows, below on tiles of 8 or 16.
 constexpr int kPromptRows = 33;
 
 struct AttnPlan {
   bool prompt = false;
-  int row_tiles = 0;  // tiles of 16 rows
-  int splits = 1;
+  int tile = 8;       // rows of a tile of the row kernel
+  int row_tiles = 0;  // of `tile` rows, or for the prompt kernel's partial outputs of 16 rows
+  int splits = 1;     // prompt kernel: parts of the keys
+  int ctas = 0;       // row kernel: CTAs that share the work; 0: a CTA has whole tiles
+  size_t slots = 0;   // partial rows in the workspace
   size_t ws_bytes = 0;
 };
 
-// How far a sequence's keys are split: enough parts to give every SM work when there are few tiles
-// of rows, each of at least 4 blocks (one round of the 16-row kernel's warps) or 4 key tiles.
+// Row kernel: two CTAs per SM in equal shares, unless no tile has more than two of the smallest
+// shares' blocks (then a tile is a CTA's) or there are too many sequences to count through.  Prompt
+// kernel: keys are split while there are fewer tiles than SMs, into parts of 4 key tiles or more.
 AttnPlan plan_attention(int sms, int n_seq, int max_q, int heads, int kv_heads, int head_dim,
                         int max_kv, int window) {
   AttnPlan p;
   const long long rows = static_cast<long long>(heads / kv_heads) * max_q;
-  p.prompt = rows >= kPromptRows;
-  p.row_tiles = static_cast<int>((rows + voc::kAttnRows - 1) / voc::kAttnRows);
   const long long heads_all = static_cast<long long>(n_seq) * kv_heads;
-  const long long tiles =
-      heads_all * (p.prompt ? (rows + voc::kPrRows - 1) / voc::kPrRows : p.row_tiles);
   long long keys = max_kv;
   if (window > 0) keys = std::min<long long>(keys, static_cast<long long>(window) + max_q);
-  const long long steps = keys / (p.prompt ? voc::kPrKeys : voc::kBlockTokens) + 1;
-  long long splits = tiles >= sms ? 1 : (p.prompt ? sms : 2 * sms) / tiles;
-  splits = std::max(1ll, std::min({splits, steps / 4, 65535ll / n_seq, 1024ll}));
-  p.splits = static_cast<int>(splits);
-  if (p.splits > 1)
-    p.ws_bytes = static_cast<size_t>(heads_all) * p.row_tiles * p.splits * voc::kAttnRows *
-                 (static_cast<size_t>(head_dim) * 4 + 8);
+  p.prompt = rows >= kPromptRows;
+  if (p.prompt) {
+    p.row_tiles = static_cast<int>((rows + voc::kPartRows - 1) / voc::kPartRows);
+    const long long tiles = heads_all * ((rows + voc::kPrRows - 1) / voc::kPrRows);
+    const long long steps = keys / voc::kPrKeys + 1;
+    const long long splits = tiles >= sms ? 1 : sms / tiles;
+    p.splits = static_cast<int>(std::max(1ll, std::min({splits, steps / 4, 65535ll / n_seq})));
+    if (p.splits > 1)
+      p.slots = static_cast<size_t>(heads_all) * p.row_tiles * p.splits * voc::kPartRows;
+  } else {
+    p.tile = rows <= 8 ? 8 : 16;
+    p.row_tiles = static_cast<int>((rows + p.tile - 1) / p.tile);
+    const long long blocks = keys / voc::kBlockTokens + 1;
+    const long long units = heads_all * p.row_tiles * blocks;
+    if (n_seq <= voc::kShareSeqs && blocks > 2 * voc::kShareMin) {
+      p.ctas = static_cast<int>(
+          std::min<long long>(2 * sms, (units + voc::kShareMin - 1) / voc::kShareMin));
+      p.slots = 2ull * p.ctas * p.tile;
+    }
+  }
+  p.ws_bytes = p.slots * (static_cast<size_t>(head_dim) * 4 + 8);
   return p;
 }
 
+template <typename T, int D, int NT>
+cudaError_t launch_rows_attention(const voc::LmAttnArgs &a, voc_stream_t stream) {
+  const dim3 grid = a.ctas ? dim3(a.ctas) : dim3(a.row_tiles, a.kv_heads, a.n_seq);
+  cudaError_t e = launch(voc::attn_rows_kernel<T, D, NT>, grid, dim3(voc::kAttnThreads),
+                         voc::attn_smem<D, NT>(), 1, stream, a);
+  if (e != cudaSuccess || !a.ctas) return e;
+  return launch(voc::attn_join_kernel<T, D, 8 * NT, true>,
+                dim3((a.group * a.max_q + 3) / 4, a.kv_heads, a.n_seq), dim3(128), 0, 1, stream, a);
+}
+
 template <typename T, int D>
-cudaError_t launch_attention(const voc::LmAttnArgs &a, bool prompt, voc_stream_t stream) {
+cudaError_t launch_attention(const voc::LmAttnArgs &a, const AttnPlan &plan, voc_stream_t stream) {
+  if (!plan.prompt)
+    return plan.tile == 8 ? launch_rows_attention<T, D, 1>(a, stream)
+                          : launch_rows_attention<T, D, 2>(a, stream);
   const int rows = a.group * a.max_q;
-  cudaError_t e;
-  if (prompt)
-    e = launch(voc::attn_prompt_kernel<T, D>,
-               dim3((rows + voc::kPrRows - 1) / voc::kPrRows, a.kv_heads, a.n_seq * a.splits),
-               dim3(voc::kPrThreads), voc::PromptSmem<D>::kBytes, 1, stream, a);
-  else
-    e = launch(voc::attn_rows_kernel<T, D>, dim3(a.splits, a.kv_heads * a.row_tiles, a.n_seq),
-               dim3(voc::kAttnThreads), voc::attn_smem<D>(), 1, stream, a);
+  cudaError_t e =
+      launch(voc::attn_prompt_kernel<T, D>,
+             dim3((rows + voc::kPrRows - 1) / voc::kPrRows, a.kv_heads, a.n_seq * a.splits),
+             dim3(voc::kPrThreads), voc::PromptSmem<D>::kBytes, 1, stream, a);
   if (e != cudaSuccess || a.splits == 1) return e;
-  return launch(voc::attn_join_kernel<T, D>, dim3((rows + 3) / 4, a.kv_heads, a.n_seq), dim3(128),
-                0, 1, stream, a);
+  return launch(voc::attn_join_kernel<T, D, voc::kPartRows, false>,
+                dim3((rows + 3) / 4, a.kv_heads, a.n_seq), dim3(128), 0, 1, stream, a);
 }
 
 }  // namespace
@@ -528,22 +555,20 @@ VOC_API voc_status vocoder_lm_attention(
   a.n_seq = n_seq, a.n_tokens = n_tokens, a.max_q = max_q;
   a.scale_log2 = softmax_scale * 1.44269504f;
   a.causal = causal, a.window = window;
-  a.row_tiles = plan.row_tiles, a.splits = plan.splits;
-  if (plan.splits > 1) {
+  a.row_tiles = plan.row_tiles, a.splits = plan.splits, a.ctas = plan.ctas;
+  if (plan.slots) {
     a.part_o = static_cast<float *>(ws);
-    a.part_ml = reinterpret_cast<float2 *>(
-        a.part_o + static_cast<size_t>(n_seq) * kv_heads * plan.row_tiles * plan.splits *
-                       voc::kAttnRows * head_dim);
+    a.part_ml = reinterpret_cast<float2 *>(a.part_o + plan.slots * head_dim);
   }
   a.budget = kWaitBudget;
   a.timeout = dev->timeout;
   cudaError_t e;
   if (dtype == VOC_LM_F16)
-    e = head_dim == 64 ? launch_attention<__half, 64>(a, plan.prompt, stream)
-                       : launch_attention<__half, 128>(a, plan.prompt, stream);
+    e = head_dim == 64 ? launch_attention<__half, 64>(a, plan, stream)
+                       : launch_attention<__half, 128>(a, plan, stream);
   else
-    e = head_dim == 64 ? launch_attention<__nv_bfloat16, 64>(a, plan.prompt, stream)
-                       : launch_attention<__nv_bfloat16, 128>(a, plan.prompt, stream);
+    e = head_dim == 64 ? launch_attention<__nv_bfloat16, 64>(a, plan, stream)
+                       : launch_attention<__nv_bfloat16, 128>(a, plan, stream);
   if (e != cudaSuccess) return cuda_fail(e, "launch attention");
   return finish(*dev, stream, flags);
 }

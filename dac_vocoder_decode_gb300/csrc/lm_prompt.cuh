@@ -22,8 +22,7 @@ namespace voc {
 constexpr int kPrThreads = 512;
 constexpr int kPrRows = 256;       // rows of a CTA
 constexpr int kPrKeys = 128;       // keys of a tile
-constexpr float kPrLazy = 8.f;     // log2 of how far the maximum may run ahead
-constexpr float kPrShift = 7.f;    // weights are kept times 2^7
+constexpr int kPartRows = 16;      // rows of a tile of partial outputs
 // Registers: 256 softmax threads, 128 converting, 128 others: 256 x 184 + 128 x 104 + 128 x 40 =
 // 65536, the block's registers at launch (512 x 128).
 constexpr int kPrSoftRegs = 184, kPrConvRegs = 104, kPrRestRegs = 40;
@@ -239,11 +238,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
         }
         const float nm = fmaxf(top[0], top[1]);
         float alpha = 1.f;
-        if (nm > m + kPrLazy || (m == -INFINITY && nm > m)) {
+        if (nm > m + kLazy || (m == -INFINITY && nm > m)) {
           alpha = ex2(m - nm);
           m = nm;
         }
-        const float off = (m == -INFINITY ? 0.f : m) - kPrShift;
+        const float off = (m == -INFINITY ? 0.f : m) - kPShift;
         l *= alpha;
         if (kt > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
           // the products that this tile's scores were issued behind are done: O is at rest
@@ -293,8 +292,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
       T *dst = static_cast<T *>(p.out) + (span.first + tok) * p.ldo + head * p.hso;
       const bool vec = (reinterpret_cast<uintptr_t>(dst) & 15) == 0;
       const long long tile16 =
-          (static_cast<long long>(b) * p.kv_heads + hk) * p.row_tiles + r / kAttnRows;
-      const long long at = (tile16 * p.splits + split) * kAttnRows + r % kAttnRows;
+          (static_cast<long long>(b) * p.kv_heads + hk) * p.row_tiles + r / kPartRows;
+      const long long at = (tile16 * p.splits + split) * kPartRows + r % kPartRows;
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
