@@ -89,7 +89,7 @@ struct SeqWork {
   long long len, p0;
   int rows, tiles;
   int blk0, blocks;
-  long long units;
+  int units;
 };
 template <int ROWS>
 __device__ __forceinline__ SeqWork seq_work(const LmAttnArgs &p, int b) {
@@ -105,14 +105,14 @@ __device__ __forceinline__ SeqWork seq_work(const LmAttnArgs &p, int b) {
   w.blk0 = static_cast<int>(lo / kBlockTokens);
   w.blocks = hi > lo ? static_cast<int>((hi - 1) / kBlockTokens) + 1 - w.blk0 : 0;
   // a tile without keys still has zeros to write: one unit of work
-  w.units = static_cast<long long>(max(w.blocks, 1)) * p.kv_heads * w.tiles;
+  w.units = max(w.blocks, 1) * p.kv_heads * w.tiles;
   return w;
 }
 
 // Share of the total work: CTA c has the units [c q, (c + 1) q) in the order (sequence, key head, row
-// tile, block).
-__device__ __forceinline__ long long share_of(long long total, int ctas) {
-  return max((total + ctas - 1) / ctas, static_cast<long long>(kShareMin));
+// tile, block).  The host shares only where the units fit 30 bits.
+__device__ __forceinline__ int share_of(int total, int ctas) {
+  return max((total + ctas - 1) / ctas, kShareMin);
 }
 
 // Ring stages: as many as leave room for two CTAs on an SM.
@@ -151,8 +151,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttn
   extern __shared__ __align__(128) uint8_t smem[];
   float *acc = reinterpret_cast<float *>(smem + kStages * 2 * kBytes);  // [two warps][row][kLd]
   __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
-  __shared__ float4 scales[kStages];  // key scale, log2 and reciprocal of the value scale, page or none
-  __shared__ long long prefix[kShareSeqs + 1];
+  __shared__ int prefix[kShareSeqs + 1];
   __shared__ float2 ml[kAttnWarps][kRows];
   __shared__ int abort_flag;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -167,17 +166,17 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttn
   }
   pdl_wait();
   pdl_launch_dependents();
-  long long lo, hi;  // this CTA's units
+  int lo, hi;  // this CTA's units
   if (p.ctas) {
     for (int i = tid; i < p.n_seq; i += kAttnThreads) prefix[i + 1] = seq_work<kRows>(p, i).units;
     __syncthreads();
     if (warp == 0) {  // running sums, 32 at a time
-      long long base = 0;
+      int base = 0;
       for (int i0 = 0; i0 < p.n_seq; i0 += 32) {
-        long long v = i0 + lane < p.n_seq ? prefix[i0 + lane + 1] : 0;
+        int v = i0 + lane < p.n_seq ? prefix[i0 + lane + 1] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
-          const long long u = __shfl_up_sync(0xffffffffu, v, o);
+          const int u = __shfl_up_sync(0xffffffffu, v, o);
           if (lane >= o) v += u;
         }
         if (i0 + lane < p.n_seq) prefix[i0 + lane + 1] = base + v;
@@ -186,8 +185,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttn
       if (lane == 0) prefix[0] = 0;
     }
     __syncthreads();
-    const long long total = prefix[p.n_seq], q = share_of(total, p.ctas);
-    lo = min(total, blockIdx.x * q);
+    const int total = prefix[p.n_seq], q = share_of(total, p.ctas);
+    lo = min(total, static_cast<int>(blockIdx.x) * q);
     hi = min(total, lo + q);
   } else {
     __syncthreads();
@@ -195,7 +194,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttn
   }
   if (lo >= hi) return;  // the whole block
   // the piece of work that starts at unit `at`, and the unit after it
-  auto segment = [&](long long at, long long &next) {
+  auto segment = [&](int at, int &next) {
     Segment s;
     if (p.ctas) {
       int a = 0, z = p.n_seq - 1;
@@ -209,9 +208,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttn
       s.b = a;
       s.w = seq_work<kRows>(p, a);
       const int per = max(s.w.blocks, 1);
-      const int tile = static_cast<int>((at - prefix[a]) / per);
-      const int begin = static_cast<int>((at - prefix[a]) % per);
-      const int end = static_cast<int>(min(static_cast<long long>(per), begin + (hi - at)));
+      const int tile = (at - prefix[a]) / per;
+      const int begin = (at - prefix[a]) % per;
+      const int end = min(per, begin + (hi - at));
       s.hk = tile / s.w.tiles, s.rt = tile % s.w.tiles;
       s.begins = begin == 0, s.ends = end == per;
       s.first = s.w.blk0 + begin;
@@ -232,30 +231,17 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttn
     // ---------------------------------------------------------------- copies
     int it = 0;
     bool ok = true;
-    for (long long at = lo, next; at < hi && ok; at = next) {
+    for (int at = lo, next; at < hi && ok; at = next) {
       const Segment s = segment(at, next);
       const int *table = p.table + s.b * p.ldt;
-      // pages and scales of 32 blocks at a time, a lane each, the next 32 while these are copied
-      auto fetch = [&](int i0, int &page, float &ks, float &vs) {
-        page = -1, ks = 1.f, vs = 1.f;
-        if (i0 + lane < s.count) {
-          page = table[s.first + i0 + lane];
-          if (page < 0 || page >= p.n_pages) {
-            page = -1;
-          } else {
-            const long long slot = static_cast<long long>(page) * p.kv_heads + s.hk;
-            ks = p.ks[slot], vs = fmaxf(p.vs[slot], kScaleMin);
-          }
-        }
-      };
-      int page, page2;
-      float ks, vs, ks2, vs2;
-      fetch(0, page, ks, vs);
+      // pages of 32 blocks at a time, a lane each, the next 32 while these are copied
+      auto fetch = [&](int i) { return i + lane < s.count ? table[s.first + i + lane] : -1; };
+      int page = fetch(0);
       for (int i0 = 0; i0 < s.count && ok; i0 += 32) {
-        fetch(i0 + 32, page2, ks2, vs2);
-        const float lvs = log2f(vs), ivs = 1.f / vs;
+        const int next_page = fetch(i0 + 32);
         for (int j = 0; j < 32 && i0 + j < s.count; ++j, ++it) {
           const int st = it % kStages;
+          const int pg = __shfl_sync(0xffffffffu, page, j);
           if (it >= kStages) {
             const bool free = mbar_wait(smem_u32(empty + st), (it / kStages - 1) & 1, p.budget,
                                         &abort_flag);
@@ -265,12 +251,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttn
               break;
             }
           }
-          const int pg = __shfl_sync(0xffffffffu, page, j);
-          if (lane == j) scales[st] = make_float4(ks, lvs, ivs, page < 0 ? 0.f : 1.f);
-          __syncwarp();
           if (lane == 0) {
             const uint32_t bar = smem_u32(full + st), dst = smem_u32(smem + st * 2 * kBytes);
-            if (pg < 0) {
+            if (pg < 0 || pg >= p.n_pages) {
               mbar_arrive(bar);
             } else {
               const long long from = (static_cast<long long>(pg) * p.kv_heads + s.hk) * kBytes;
@@ -280,7 +263,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttn
             }
           }
         }
-        page = page2, ks = ks2, vs = vs2;
+        page = next_page;
       }
     }
     if (!ok && lane == 0) {  // leave with no copy in flight
@@ -296,10 +279,25 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttn
   const int pair = warp / 2, half = warp % 2;
   int it = 0;
   bool ok = true;
-  for (long long at = lo, next; at < hi; at = next) {
+  for (int at = lo, next; at < hi; at = next) {
     const Segment s = segment(at, next);
     const int r0 = s.rt * kRows, r_last = min(s.w.rows, r0 + kRows) - 1;
     if (r0 > r_last) continue;  // whole-tile launches cover max_q tokens
+    // scales of this warp's blocks (every other one): loaded one of them ahead of their use, the
+    // pages two ahead
+    const int *table = p.table + s.b * p.ldt + s.first;
+    const int i_first = (it ^ pair) & 1;
+    auto page_at = [&](int i) {
+      const int page = i < s.count ? table[i] : -1;
+      return page >= 0 && page < p.n_pages ? page : -1;
+    };
+    float ks = 1.f, vs = 1.f;
+    auto load_scales = [&](int page) {
+      const long long slot = static_cast<long long>(page) * p.kv_heads + s.hk;
+      ks = page >= 0 ? p.ks[slot] : 1.f, vs = page >= 0 ? p.vs[slot] : 1.f;
+    };
+    int page = page_at(i_first), page2 = page_at(i_first + 2);
+    load_scales(page);
     // queries as the second operand: row g of each 8 rows, two halves of f16 per step
     uint32_t qb[NT][kSteps][2];
     float qc[NT][2];
@@ -378,17 +376,21 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttn
       m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
     }
 
-    for (int i = 0; i < s.count; ++i, ++it) {
-      if ((it & 1) != pair) continue;
-      const int st = it % kStages;
+    for (int i = i_first; i < s.count; i += 2) {
+      const int st = (it + i) % kStages;
+      const int base = i * kBlockTokens + 32 * half;  // relative to key0
+      const bool use = page >= 0 && base < any_hi && base + 32 > any_lo;
+      const float k_scale = ks, v_scale = fmaxf(vs, kScaleMin);
+      page = page2;
+      load_scales(page);
+      page2 = page_at(i + 4);
       if (ok) {
-        ok = mbar_wait(smem_u32(full + st), (it / kStages) & 1, p.budget, &abort_flag);
+        ok = mbar_wait(smem_u32(full + st), ((it + i) / kStages) & 1, p.budget, &abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) *static_cast<volatile int *>(&abort_flag) = 1;
       }
-      const int base = i * kBlockTokens + 32 * half;  // relative to key0
-      const float4 sc4 = scales[st];
-      if (ok && sc4.w != 0.f && base < any_hi && base + 32 > any_lo) {
+      if (ok && use) {
+        const float lvs = log2f(v_scale), ivs = 1.f / v_scale;
         const uint32_t kb = smem_u32(smem + st * 2 * kBytes), vb = kb + kBytes;
         // scores: row g (g + 8) of tile j is key 8 (g / 2) + 4 j + g % 2 (+ 2)
         float sc[NT][2][4];
@@ -430,11 +432,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttn
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float c = fmaxf(qc[n][x] * sc4.x, 1e-37f);  // above 0: masked scores stay -inf
+            const float c = fmaxf(qc[n][x] * k_scale, 1e-37f);  // above 0: masked scores stay -inf
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              sc[n][j][x] = fmaf(sc[n][j][x], c, sc4.y);
-              sc[n][j][x + 2] = fmaf(sc[n][j][x + 2], c, sc4.y);
+              sc[n][j][x] = fmaf(sc[n][j][x], c, lvs);
+              sc[n][j][x + 2] = fmaf(sc[n][j][x + 2], c, lvs);
             }
             const float top = fmaxf(fmaxf(sc[n][0][x], sc[n][0][x + 2]),
                                     fmaxf(sc[n][1][x], sc[n][1][x + 2]));
@@ -475,7 +477,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttn
             pb[n][j][1] = transpose8(f16x2(w[2], w[3]));
           }
 #pragma unroll
-          for (int x = 0; x < 2; ++x) l[n][x] = fmaf(sum[x], sc4.z, l[n][x]);
+          for (int x = 0; x < 2; ++x) l[n][x] = fmaf(sum[x], ivs, l[n][x]);
         }
         // codes of keys that no row sees count as zero, whatever they hold
         uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
@@ -510,6 +512,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttn
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(empty + st));
     }
+    it += s.count;
 
     // join the warps: each scales its rows to the common maximum
 #pragma unroll
@@ -566,74 +569,87 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttn
   }
 }
 
-// Joins the parts of a tile's row, one warp per row.  ROWS = 8 NT: the row kernel's shares;
-// ROWS = 16: the prompt kernel's splits, [tile of 16 rows][split][16].
+// Joins the parts of a tile's row, one CTA of D threads per row, a channel each.  SHARES: the row
+// kernel's parts (ROWS = 8 NT); else the prompt kernel's, [tile of ROWS rows][split][ROWS].
 template <typename T, int D, int ROWS, bool SHARES>
-__global__ void __launch_bounds__(128) attn_join_kernel(const LmAttnArgs p) {
-  __shared__ long long red[4];
-  pdl_wait();
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int b = blockIdx.z, hk = blockIdx.y;
-  const int row = blockIdx.x * 4 + warp;
+__global__ void __launch_bounds__(D) attn_join_kernel(const LmAttnArgs p) {
+  constexpr int kWarps = D / 32;
+  __shared__ int counts[2][kWarps];
+  __shared__ float red[2][kWarps], factor[D];
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int b = blockIdx.z, hk = blockIdx.y, row = blockIdx.x;
+  // Lengths and counts were complete before the kernel that this one follows started its work, and
+  // it writes neither, so they are read before waiting for it.
   const SeqSpan span = seq_span(p.cu, b, p.n_seq, p.n_tokens, p.max_q);
-  long long c0 = 0, c1 = 0;
+  int c0 = 0, c1 = 0;
   if (SHARES) {
     // the work before this sequence and in all, as attn_rows_kernel counts it
-    long long before = 0, total = 0;
-    for (int i = threadIdx.x; i < p.n_seq; i += 128) {
-      const long long u = seq_work<ROWS>(p, i).units;
-      total += u;
-      if (i < b) before += u;
+    int both[2] = {0, 0};
+    for (int i = tid; i < p.n_seq; i += D) {
+      const int u = seq_work<ROWS>(p, i).units;
+      both[1] += u;
+      if (i < b) both[0] += u;
     }
-    long long both[2] = {before, total};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
 #pragma unroll
       for (int o = 16; o; o /= 2) both[k] += __shfl_xor_sync(0xffffffffu, both[k], o);
-      __syncthreads();
-      if (lane == 0) red[warp] = both[k];
-      __syncthreads();
-      both[k] = red[0] + red[1] + red[2] + red[3];
+      if (lane == 0) counts[k][warp] = both[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      both[k] = 0;
+      for (int w = 0; w < kWarps; ++w) both[k] += counts[k][w];
     }
     const SeqWork w = seq_work<ROWS>(p, b);
     const int per = max(w.blocks, 1);
-    const long long q = share_of(both[1], p.ctas);
-    const long long at = both[0] + (static_cast<long long>(hk) * w.tiles + row / ROWS) * per;
+    const int q = share_of(both[1], p.ctas);
+    const int at = both[0] + (hk * w.tiles + row / ROWS) * per;
     c0 = at / q, c1 = (at + per - 1) / q;
   }
+  pdl_wait();
   if (row >= span.count * p.group) return;
   if (SHARES && c0 == c1) return;  // one CTA had the whole tile
   const long long tile =
       (static_cast<long long>(b) * p.kv_heads + hk) * p.row_tiles + row / ROWS;
-  const int parts = SHARES ? static_cast<int>(c1 - c0 + 1) : p.splits;
+  const int parts = SHARES ? c1 - c0 + 1 : p.splits;
   auto slot_of = [&](int s) {
-    const long long slot = SHARES ? (s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) : tile * p.splits + s;
+    const long long slot = SHARES ? (s == 0 ? 2ll * c0 + 1 : 2ll * (c0 + s)) : tile * p.splits + s;
     return slot * ROWS + row % ROWS;
   };
   float top = -INFINITY;
-  for (int s = lane; s < parts; s += 32) top = fmaxf(top, p.part_ml[slot_of(s)].x);
+  for (int s = tid; s < parts; s += D) top = fmaxf(top, p.part_ml[slot_of(s)].x);
 #pragma unroll
   for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float sum = 0.f, v[D / 32];
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) v[i] = 0.f;
-  for (int s = 0; s < parts; ++s) {
-    const long long at = slot_of(s);
-    const float2 x = p.part_ml[at];
-    if (x.x == -INFINITY) {  // nothing visible in this part, or NaN alone
-      sum += x.y;
-      continue;
+  if (lane == 0) red[0][warp] = top;
+  __syncthreads();
+  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, red[0][w]);
+  float sum = 0.f, v = 0.f;
+  for (int s0 = 0; s0 < parts; s0 += D) {  // factors of up to D parts, then their sum
+    float f = 0.f;
+    if (s0 + tid < parts) {
+      const float2 x = p.part_ml[slot_of(s0 + tid)];
+      // a part that saw no key has a sum of 0, or NaN where it met NaN alone
+      f = x.x == -INFINITY ? 0.f : ex2(x.x - top);
+      sum += x.x == -INFINITY ? x.y : x.y * f;
     }
-    const float f = ex2(x.x - top);
-    sum += x.y * f;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) v[i] += f * p.part_o[at * D + lane + 32 * i];
+    __syncthreads();
+    factor[tid] = f;
+    __syncthreads();
+    const int n = min(D, parts - s0);
+#pragma unroll 8
+    for (int s = 0; s < n; ++s) v = fmaf(factor[s], p.part_o[slot_of(s0 + s) * D + tid], v);
   }
-  const int tok = row / p.group, h = hk * p.group + row % p.group;
-  T *dst = static_cast<T *>(p.out) + (span.first + tok) * p.ldo + h * p.hso;
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i)
-    dst[lane + 32 * i] = from_f32<T>(sum == 0.f ? 0.f : v[i] / sum);
+  for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) red[1][warp] = sum;
+  __syncthreads();
+  sum = 0.f;
+  for (int w = 0; w < kWarps; ++w) sum += red[1][w];
+  const int tok = row / p.group, h = hk * p.group + row % p.group;
+  static_cast<T *>(p.out)[(span.first + tok) * p.ldo + h * p.hso + tid] =
+      from_f32<T>(sum == 0.f ? 0.f : v / sum);
 }
 
 }  // namespace voc

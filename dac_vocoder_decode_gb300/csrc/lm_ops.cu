@@ -470,7 +470,7 @@ AttnPlan plan_attention(int sms, int n_seq, int max_q, int heads, int kv_heads, 
     p.row_tiles = static_cast<int>((rows + p.tile - 1) / p.tile);
     const long long blocks = keys / voc::kBlockTokens + 1;
     const long long units = heads_all * p.row_tiles * blocks;
-    if (n_seq <= voc::kShareSeqs && blocks > 2 * voc::kShareMin) {
+    if (n_seq <= voc::kShareSeqs && blocks > 2 * voc::kShareMin && units < (1ll << 30)) {
       p.ctas = static_cast<int>(
           std::min<long long>(2 * sms, (units + voc::kShareMin - 1) / voc::kShareMin));
       p.slots = 2ull * p.ctas * p.tile;
@@ -487,7 +487,7 @@ cudaError_t launch_rows_attention(const voc::LmAttnArgs &a, voc_stream_t stream)
                          voc::attn_smem<D, NT>(), 1, stream, a);
   if (e != cudaSuccess || !a.ctas) return e;
   return launch(voc::attn_join_kernel<T, D, 8 * NT, true>,
-                dim3((a.group * a.max_q + 3) / 4, a.kv_heads, a.n_seq), dim3(128), 0, 1, stream, a);
+                dim3(a.group * a.max_q, a.kv_heads, a.n_seq), dim3(D), 0, 1, stream, a);
 }
 
 template <typename T, int D>
@@ -502,7 +502,7 @@ cudaError_t launch_attention(const voc::LmAttnArgs &a, const AttnPlan &plan, voc
              dim3(voc::kPrThreads), voc::PromptSmem<D>::kBytes, 1, stream, a);
   if (e != cudaSuccess || a.splits == 1) return e;
   return launch(voc::attn_join_kernel<T, D, voc::kPartRows, false>,
-                dim3((rows + 3) / 4, a.kv_heads, a.n_seq), dim3(128), 0, 1, stream, a);
+                dim3(rows, a.kv_heads, a.n_seq), dim3(D), 0, 1, stream, a);
 }
 
 }  // namespace
@@ -541,8 +541,11 @@ VOC_API voc_status vocoder_lm_attention(
   Device *dev;
   if (voc_status st = device(&dev); st != VOC_OK) return st;
   if (n_tokens == 0 || max_q == 0) return finish(*dev, stream, flags);
-  const AttnPlan plan =
+  AttnPlan plan =
       plan_attention(dev->sms, n_seq, max_q, heads, kv_heads, head_dim, max_kv, window);
+  // lengths are on the device and may exceed max_kv: what the page table can hold bounds them
+  if (static_cast<double>(n_seq) * kv_heads * plan.row_tiles * (table_cols + 1.0) >= 0x1p30)
+    plan.ctas = 0;
   if (plan.ws_bytes && (!ws || ws_bytes < plan.ws_bytes))
     return fail(VOC_WORKSPACE_TOO_SMALL, "attention: workspace below vocoder_lm_attention_ws_bytes");
   voc::LmAttnArgs a{};
