@@ -609,6 +609,7 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const LmAttnArgs p) {
     c0 = at / q, c1 = (at + per - 1) / q;
   }
   pdl_wait();
+  pdl_launch_dependents();
   if (row >= span.count * p.group) return;
   if (SHARES && c0 == c1) return;  // one CTA had the whole tile
   const long long tile =

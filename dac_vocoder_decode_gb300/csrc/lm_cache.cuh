@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(AppendShape<D>::kThreads) append_kernel(const 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int t4 = (warp % 2) * 32 + lane / 4 * 4, ch = (warp / 2) * 32 + lane % 4 * 8;
   pdl_wait();
+  pdl_launch_dependents();
   const int b = blockIdx.z, head = blockIdx.y;
   const SeqSpan span = seq_span(p.cu, b, p.n_seq, p.n_tokens, p.max_q);
   const long long len = p.lens[b];

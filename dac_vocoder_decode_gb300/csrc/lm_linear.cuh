@@ -68,6 +68,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   if (warp == 4) {
     if (lane == 0) {
       pdl_wait();
+      pdl_launch_dependents();
       int issued = c0;
       for (int c = c0; c < c1; ++c) {
         const int i = c - c0, st = i % p.stages;
@@ -123,6 +124,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   float *part = reinterpret_cast<float *>(ring);  // [token][128], split > 1
   if (warp < 4) {
     pdl_wait();
+    pdl_launch_dependents();
     const float ws = feat < p.N ? p.ws[feat] : 0.f;
     const float bias = p.bias && feat < p.N ? p.bias[feat] : 0.f;
     for (int t0 = 0; t0 < tokens; t0 += 16) {
@@ -242,6 +244,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) __cluster_dims__(2, 1, 1)
   if (warp == 4) {
     if (lane == 0) {
       pdl_wait();
+      pdl_launch_dependents();
       const uint32_t full0 = mapa_shared(smem_u32(full), 0u);
       int it = 0;
       bool ok = true;
@@ -307,6 +310,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) __cluster_dims__(2, 1, 1)
     // The accumulator's lanes are token rows.  A warp turns 32 rows x 128 bytes around in shared
     // memory, so that its stores cover whole lines of 4 rows instead of a sector of 32 rows.
     pdl_wait();
+    pdl_launch_dependents();
     constexpr int kCols = 128 / static_cast<int>(sizeof(T));  // columns of a staged piece
     constexpr int kPer = 16 / static_cast<int>(sizeof(T));
     T *out = static_cast<T *>(p.out);

@@ -86,6 +86,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
     fence_barrier_init();
   }
   pdl_wait();
+  pdl_launch_dependents();
   // the latest rows see the most keys: they start first
   const int tile_max = static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x);
   const int r0 = tile_max * kPrRows;

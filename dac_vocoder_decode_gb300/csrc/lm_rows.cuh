@@ -63,6 +63,7 @@ template <typename T, int MODE>
 __global__ void __launch_bounds__(256) rows_any_kernel(const LmRowsArgs p) {
   __shared__ float red[32];
   pdl_wait();
+  pdl_launch_dependents();
   const long long row = blockIdx.x;
   const T *x = static_cast<const T *>(p.x) + row * p.ldx;
   const T *r = p.res ? static_cast<const T *>(p.res) + row * p.ldr : nullptr;
@@ -172,6 +173,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LmRowsArgs p, c
   constexpr int N = Vec::N, kChunks = kRowValues / N;
   __shared__ float red[kRowThreads / 32];
   pdl_wait();
+  pdl_launch_dependents();
   const int lane = threadIdx.x % tpr;
   const long long row =
       static_cast<long long>(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
