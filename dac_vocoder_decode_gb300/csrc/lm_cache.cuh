@@ -86,7 +86,8 @@ struct AppendShape {
 // its stores of K rows and of V rows (4 tokens of a channel are one word) all fill 32-byte sectors,
 // without a pass through shared memory.
 template <typename T, int D>
-__global__ void __launch_bounds__(AppendShape<D>::kThreads) append_kernel(const LmAppendArgs p) {
+__global__ void __launch_bounds__(AppendShape<D>::kThreads, 1024 / AppendShape<D>::kThreads)
+    append_kernel(const LmAppendArgs p) {
   constexpr int kThreads = AppendShape<D>::kThreads, kWarps = kThreads / 32;
   __shared__ uint32_t red[2][kWarps];
   __shared__ uint32_t bad[2];  // tokens of the block with a NaN
@@ -102,14 +103,10 @@ __global__ void __launch_bounds__(AppendShape<D>::kThreads) append_kernel(const 
   const long long blk = start / kBlockTokens + blockIdx.x;
   const long long base = blk * kBlockTokens;
   if (span.count <= 0 || base >= len || blk >= p.table_cols) return;
-  const int page = p.table[b * p.ldt + blk];
-  if (page < 0 || page >= p.n_pages) return;
+  const int page = p.table[b * p.ldt + blk];  // used only after the tokens' loads are under way
   const int lo = static_cast<int>(start > base ? start - base : 0);
   const int hi = static_cast<int>(len - base < kBlockTokens ? len - base : kBlockTokens);
   const bool fresh = lo == 0;
-  const long long slot = static_cast<long long>(page) * p.heads + head;
-  const float old[2] = {fresh ? 0.f : p.ks[slot], fresh ? 0.f : p.vs[slot]};
-
   uint4 raw[2][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -122,6 +119,9 @@ __global__ void __launch_bounds__(AppendShape<D>::kThreads) append_kernel(const 
                                                    head * p.hsv + ch);
     }
   }
+  if (page < 0 || page >= p.n_pages) return;
+  const long long slot = static_cast<long long>(page) * p.heads + head;
+  const float old[2] = {fresh ? 0.f : p.ks[slot], fresh ? 0.f : p.vs[slot]};
   uint32_t m[2] = {0, 0};  // largest |value| of k and v, two at a time in the words' halves
 #pragma unroll
   for (int t = 0; t < 2; ++t)
@@ -212,19 +212,26 @@ __global__ void __launch_bounds__(AppendShape<D>::kThreads) append_kernel(const 
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (t4 + i >= lo && t4 + i < hi) mine |= 0xffu << 8 * i;
-    float f[4][8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) Vec16<T>::unpack(raw[1][i], f[i]);
+    for (int j = 0; j < 4; ++j) {
+      float f[4][2];  // channels 2j and 2j + 1 of the four tokens
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      uint32_t *dst = reinterpret_cast<uint32_t *>(vb + (ch + j) * kBlockTokens + t4);
-      uint32_t w = e4m3x4(f[0][j] * inv[1], f[1][j] * inv[1], f[2][j] * inv[1], f[3][j] * inv[1]);
-      if (!all) {
-        uint32_t o = *dst;
-        if (move[1] != 1.f) o = move_codes(o, move[1]);
-        w = (w & mine) | (o & ~mine);
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w[4] = {raw[1][i].x, raw[1][i].y, raw[1][i].z, raw[1][i].w};
+        unpack2<T>(w[j], f[i][0], f[i][1]);
       }
-      *dst = w;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t *dst = reinterpret_cast<uint32_t *>(vb + (ch + 2 * j + h) * kBlockTokens + t4);
+        uint32_t w =
+            e4m3x4(f[0][h] * inv[1], f[1][h] * inv[1], f[2][h] * inv[1], f[3][h] * inv[1]);
+        if (!all) {
+          uint32_t o = *dst;
+          if (move[1] != 1.f) o = move_codes(o, move[1]);
+          w = (w & mine) | (o & ~mine);
+        }
+        *dst = w;
+      }
     }
   }
 }

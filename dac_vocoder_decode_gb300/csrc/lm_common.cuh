@@ -97,6 +97,37 @@ struct Vec16<__nv_bfloat16> {
   }
 };
 
+// A 32-bit word of two 16-bit values <-> floats.
+template <typename T>
+__device__ __forceinline__ void unpack2(uint32_t w, float &a, float &b);
+template <>
+__device__ __forceinline__ void unpack2<__half>(uint32_t w, float &a, float &b) {
+  __half2 h;
+  memcpy(&h, &w, 4);
+  const float2 v = __half22float2(h);
+  a = v.x, b = v.y;
+}
+template <>
+__device__ __forceinline__ void unpack2<__nv_bfloat16>(uint32_t w, float &a, float &b) {
+  a = __uint_as_float(w << 16), b = __uint_as_float(w & 0xffff0000u);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  uint32_t w;
+  memcpy(&w, &h, 4);
+  return w;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  uint32_t w;
+  memcpy(&w, &h, 4);
+  return w;
+}
+
 // Two floats to two e4m3 codes, `lo` in the low byte: round to nearest even, magnitudes over 448
 // (infinities too) to 448, NaN to 0x7f.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -124,6 +155,13 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint16_t v) {
 // |v| as an integer: its maximum orders magnitudes like the float's and keeps a NaN, which a
 // floating maximum would drop.
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// max(m, |v|) that keeps a NaN.
+__device__ __forceinline__ float max_abs(float m, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+  return r;
+}
 
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float pow2(int e) {

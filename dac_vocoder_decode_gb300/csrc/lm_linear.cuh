@@ -30,7 +30,7 @@ constexpr int kLinK = 128;           // bytes of K per stage: one 128-byte swizz
 // lanes are output channels.  K is split over the CTAs of a cluster, which add their parts up
 // through distributed shared memory in a fixed order.
 template <typename T>
-__global__ void __launch_bounds__(kLinThreads, 1)
+__global__ void __launch_bounds__(kLinThreads, 2)
     linear_few_kernel(const __grid_constant__ CUtensorMap xmap,
                       const __grid_constant__ CUtensorMap wmap, const LmLinearArgs p) {
   extern __shared__ uint8_t smem_raw[];

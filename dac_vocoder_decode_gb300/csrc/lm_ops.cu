@@ -168,13 +168,25 @@ int row_threads(int sms, long long rows, int d, int chunk) {
   return t;
 }
 
+template <typename T, int MODE, int VB, int CH>
+cudaError_t launch_rows_ch(int tpr, const voc::LmRowsArgs &a, voc_stream_t stream) {
+  const int threads = std::max(128, tpr);
+  const long long per = threads / tpr;
+  return launch(voc::rows_kernel<T, MODE, VB, CH>,
+                dim3(static_cast<unsigned>((a.rows + per - 1) / per)), dim3(threads), 0, 1, stream,
+                a, tpr);
+}
+
+// As many vectors per thread as the row needs: in quarters of kRowValues values.
 template <typename T, int MODE, int VB>
 cudaError_t launch_rows_vec(int sms, const voc::LmRowsArgs &a, voc_stream_t stream) {
-  constexpr int n = VB / static_cast<int>(sizeof(T));
-  const int tpr = row_threads(sms, a.rows, a.d, n), threads = std::max(128, tpr);
-  const long long per = threads / tpr;
-  return launch(voc::rows_kernel<T, MODE, VB>, dim3(static_cast<unsigned>((a.rows + per - 1) / per)),
-                dim3(threads), 0, 1, stream, a, tpr);
+  constexpr int n = VB / static_cast<int>(sizeof(T)), most = voc::kRowValues / n;
+  const int tpr = row_threads(sms, a.rows, a.d, n);
+  const int need = (a.d + n * tpr - 1) / (n * tpr);
+  if (4 * need <= most) return launch_rows_ch<T, MODE, VB, most / 4>(tpr, a, stream);
+  if (2 * need <= most) return launch_rows_ch<T, MODE, VB, most / 2>(tpr, a, stream);
+  if (4 * need <= 3 * most) return launch_rows_ch<T, MODE, VB, 3 * most / 4>(tpr, a, stream);
+  return launch_rows_ch<T, MODE, VB, most>(tpr, a, stream);
 }
 
 // The widest access that the width, the strides and the buffers allow.
@@ -287,9 +299,9 @@ cudaError_t launch_many(int sms, const CUtensorMap &xm, const CUtensorMap &wm,
 
 template <typename T>
 cudaError_t launch_few(const CUtensorMap &xm, const CUtensorMap &wm, const voc::LmLinearArgs &a,
-                       int split, voc_stream_t stream) {
+                       int split, size_t smem, voc_stream_t stream) {
   const dim3 grid((a.N + voc::kLinRows - 1) / voc::kLinRows, (a.M + a.nt - 1) / a.nt, split);
-  return launch(voc::linear_few_kernel<T>, grid, dim3(voc::kLinThreads), kLinSmem, split, stream,
+  return launch(voc::linear_few_kernel<T>, grid, dim3(voc::kLinThreads), smem, split, stream,
                 xm, wm, a);
 }
 
@@ -343,19 +355,22 @@ VOC_API voc_status vocoder_lm_linear_fp8(const void *x8, long long ldx, const fl
   if ((M + a.nt - 1) / a.nt > 65535) return fail(VOC_UNSUPPORTED, "linear: too many rows");
   a.tmem_cols = 32;
   while (a.tmem_cols < a.nt) a.tmem_cols *= 2;
+  // two CTAs per SM where their rings are deep enough for it, and K split over up to 8 CTAs until
+  // there is one for every place
   const int stage = (voc::kLinRows + a.nt) * voc::kLinK;
-  a.stages = std::min<int>(12, (kLinSmem - 1024) / stage);
   const int tiles = ((N + voc::kLinRows - 1) / voc::kLinRows) * ((M + a.nt - 1) / a.nt);
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= dev->sms && split * 2 <= a.chunks) split *= 2;
+  const int per_sm = a.nt <= 64 ? 2 : 1;
+  const size_t smem = kLinSmem / per_sm - (per_sm - 1) * 2048;
+  a.stages = std::min<int>(12, static_cast<int>((smem - 1024) / stage));
+  const int split = std::max(1, std::min({8, per_sm * dev->sms / tiles, a.chunks / 2}));
   if (voc_status st = encode_rows(&xm, x8, M, K, ldx, a.nt); st != VOC_OK) return st;
   if (voc_status st = encode_rows(&wm, w8, N, K, ldw, voc::kLinRows); st != VOC_OK) return st;
   if (out_dtype == VOC_LM_F32)
-    e = launch_few<float>(xm, wm, a, split, stream);
+    e = launch_few<float>(xm, wm, a, split, smem, stream);
   else if (out_dtype == VOC_LM_F16)
-    e = launch_few<__half>(xm, wm, a, split, stream);
+    e = launch_few<__half>(xm, wm, a, split, smem, stream);
   else
-    e = launch_few<__nv_bfloat16>(xm, wm, a, split, stream);
+    e = launch_few<__nv_bfloat16>(xm, wm, a, split, smem, stream);
   if (e != cudaSuccess) return cuda_fail(e, "launch linear");
   return finish(*dev, stream, flags);
 }

@@ -49,7 +49,15 @@ __device__ __forceinline__ float rms_factor(float sumsq, int d, float eps, float
   return v > 0.f ? 1.f / sqrtf(v) : (v == 0.f ? 0.f : v);  // a row of zeros without eps: zeros
 }
 
-__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.f + expf(-g)) * u; }
+// The exponential's and the quotient's approximations are good to a few 2^-23, far inside half an
+// e4m3 step; e^-g that overflows gives the limit, 0.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  return __fdividef(g, 1.f + __expf(-g)) * u;
+}
+
+// Whether a row's sum of squares lost nothing: no overflow, and squares that vanished count for less
+// than 2^-24 of it.
+__device__ __forceinline__ bool rms_sum_holds(float ss) { return ss >= 0x1p-60f && ss < INFINITY; }
 
 // scale and 1/scale of a row whose largest |n| has the bits `amax` (NaN kept).
 __device__ __forceinline__ float2 row_scale(uint32_t amax) {
@@ -115,62 +123,99 @@ __global__ void __launch_bounds__(256) rows_any_kernel(const LmRowsArgs p) {
 template <typename T, int VB>
 struct RowVec {
   static constexpr int N = VB / static_cast<int>(sizeof(T));
-  using Raw = typename std::conditional<
-      VB == 16, uint4,
-      typename std::conditional<VB == 8, uint2,
-                                typename std::conditional<VB == 4, uint32_t,
-                                                          uint16_t>::type>::type>::type;
-  union U {
-    Raw raw;
-    T v[N];
-    __device__ U() {}
-  };
-  static __device__ __forceinline__ void load(const T *p, float (&f)[N]) {
-    U u;
-    u.raw = *reinterpret_cast<const Raw *>(p);
-#pragma unroll
-    for (int j = 0; j < N; ++j) f[j] = to_f32(u.v[j]);
+  static constexpr int kWords = VB >= 4 ? VB / 4 : 1;
+  static __device__ __forceinline__ void load_raw(const T *p, uint32_t (&w)[kWords]) {
+    if constexpr (VB == 16) {
+      const uint4 u = *reinterpret_cast<const uint4 *>(p);
+      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    } else if constexpr (VB == 8) {
+      const uint2 u = *reinterpret_cast<const uint2 *>(p);
+      w[0] = u.x, w[1] = u.y;
+    } else if constexpr (VB == 4) {
+      w[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else {
+      w[0] = *reinterpret_cast<const uint16_t *>(p);
+    }
   }
-  static __device__ __forceinline__ void store(T *p, const float *f) {
-    U u;
+  static __device__ __forceinline__ void unpack(const uint32_t (&w)[kWords], float (&f)[N]) {
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) u.v[j] = from_f32<T>(f[j]);
-    *reinterpret_cast<Raw *>(p) = u.raw;
+      for (int j = 0; j < N; ++j) f[j] = __uint_as_float(w[j]);
+    } else if constexpr (N == 1) {
+      float unused;
+      unpack2<T>(w[0], f[0], unused);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) unpack2<T>(w[j], f[2 * j], f[2 * j + 1]);
+    }
+  }
+  static __device__ __forceinline__ void load(const T *p, float (&f)[N]) {
+    uint32_t w[kWords];
+    load_raw(p, w);
+    unpack(w, f);
+  }
+  static __device__ __forceinline__ void store(T *p, const float (&f)[N]) {
+    if constexpr (N == 1) {
+      *p = from_f32<T>(f[0]);
+    } else {
+      uint32_t w[kWords];
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) {
+        if constexpr (sizeof(T) == 4)
+          w[j] = __float_as_uint(f[j]);
+        else
+          w[j] = pack2<T>(f[2 * j], f[2 * j + 1]);
+      }
+      if constexpr (VB == 16)
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+      else if constexpr (VB == 8)
+        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+      else
+        *reinterpret_cast<uint32_t *>(p) = w[0];
+    }
   }
 };
 
 constexpr int kRowValues = 32;    // values of a row that a thread keeps in registers
 constexpr int kRowThreads = 512;  // most threads of a row: rows of up to 16384 values
 
-// Sum or maximum over a row's `tpr` threads (a power of two from 32 on); `red` has a float per
-// warp.  The order is fixed.
-template <bool MAX>
-__device__ __forceinline__ uint32_t row_reduce(uint32_t v, int tpr, float *red) {
+// Sum, or maximum of magnitudes (NaN kept), over a row's `tpr` threads (a power of two from 32 on);
+// `red` has a float per warp.  The order is fixed.
+__device__ __forceinline__ float row_sum(float v, int tpr, float *red) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const uint32_t w = __shfl_xor_sync(0xffffffffu, v, o);
-    v = MAX ? max(v, w) : __float_as_uint(__uint_as_float(v) + __uint_as_float(w));
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (tpr > 32) {
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
+    __syncthreads();
+    const int base = threadIdx.x / tpr * (tpr / 32);
+    v = red[base];
+    for (int i = 1; i < tpr / 32; ++i) v += red[base + i];
   }
+  return v;
+}
+__device__ __forceinline__ uint32_t row_max(float m, int tpr, float *red) {
+  uint32_t v = __reduce_max_sync(0xffffffffu, abs_bits(m));
   if (tpr > 32) {
     __syncthreads();
     if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = __uint_as_float(v);
     __syncthreads();
     const int base = threadIdx.x / tpr * (tpr / 32);
     v = __float_as_uint(red[base]);
-    for (int i = 1; i < tpr / 32; ++i) {
-      const uint32_t w = __float_as_uint(red[base + i]);
-      v = MAX ? max(v, w) : __float_as_uint(__uint_as_float(v) + __uint_as_float(w));
-    }
+    for (int i = 1; i < tpr / 32; ++i) v = max(v, __float_as_uint(red[base + i]));
   }
   return v;
 }
 
-// Rows of up to 16384 values, each read once and kept in registers by its `tpr` threads.  VB is the
-// widest access that the row's buffers and strides allow.
-template <typename T, int MODE, int VB>
+// Rows of up to 16384 values, each read once and kept in registers by its `tpr` threads, CH
+// vectors of VB bytes each.  VB is the widest access that the row's buffers and strides allow.
+// With d values a row moves 7 d bytes (16-bit, residual), and the kernel has to spend few
+// instructions on a value to keep up with that: conversions two at a time, and magnitudes before
+// the norm are looked at only where the sum of squares says that squares overflowed or vanished.
+template <typename T, int MODE, int VB, int CH>
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LmRowsArgs p, const int tpr) {
   using Vec = RowVec<T, VB>;
-  constexpr int N = Vec::N, kChunks = kRowValues / N;
+  constexpr int N = Vec::N;
   __shared__ float red[kRowThreads / 32];
   pdl_wait();
   pdl_launch_dependents();
@@ -180,83 +225,99 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LmRowsArgs p, c
   const bool live = row < p.rows;  // spare threads of the last block keep to the barriers
   const int chunks = live ? p.d / N : 0;
   const T *x = static_cast<const T *>(p.x) + row * p.ldx;
-  const T *r = static_cast<const T *>(p.res) + row * p.ldr;
-  const T *w = static_cast<const T *>(p.w);
-  float h[kChunks][N];
-  uint32_t m = 0;
-  float ss = 0.f;
+  float h[CH][N];
+  if (MODE == kRowsGated || p.res) {
+    const T *r = MODE == kRowsGated ? x + p.d : static_cast<const T *>(p.res) + row * p.ldr;
+    uint32_t a[CH][Vec::kWords], b[CH][Vec::kWords];
 #pragma unroll
-  for (int i = 0; i < kChunks; ++i) {
-    const int c = lane + i * tpr;
-    if (c < chunks) {
-      Vec::load(x + c * N, h[i]);
-      if (MODE == kRowsGated) {
-        float u[N];
-        Vec::load(x + p.d + c * N, u);
-#pragma unroll
-        for (int j = 0; j < N; ++j) h[i][j] = silu_mul(h[i][j], u[j]);
-      } else if (p.res) {
-        float u[N];
-        Vec::load(r + c * N, u);
-#pragma unroll
-        for (int j = 0; j < N; ++j) h[i][j] += u[j];
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < N; ++j) h[i][j] = 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      m = max(m, abs_bits(h[i][j]));
-      if (MODE == kRowsRms) ss = fmaf(h[i][j], h[i][j], ss);
-    }
-  }
-  if (p.sum) {
-    T *s = static_cast<T *>(p.sum) + row * p.lds;
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
+    for (int i = 0; i < CH; ++i) {
       const int c = lane + i * tpr;
-      if (c < chunks) Vec::store(s + c * N, h[i]);
+#pragma unroll
+      for (int j = 0; j < Vec::kWords; ++j) a[i][j] = b[i][j] = 0;
+      if (c < chunks) {
+        Vec::load_raw(x + c * N, a[i]);
+        Vec::load_raw(r + c * N, b[i]);
+      }
     }
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      float u[N];
+      Vec::unpack(a[i], h[i]);
+      Vec::unpack(b[i], u);
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        h[i][j] = MODE == kRowsGated ? silu_mul(h[i][j], u[j]) : h[i][j] + u[j];
+    }
+    if (MODE != kRowsGated && p.sum) {
+      T *s = static_cast<T *>(p.sum) + row * p.lds;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int c = lane + i * tpr;
+        if (c < chunks) Vec::store(s + c * N, h[i]);
+      }
+    }
+  } else {
+    uint32_t a[CH][Vec::kWords];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = lane + i * tpr;
+#pragma unroll
+      for (int j = 0; j < Vec::kWords; ++j) a[i][j] = 0;
+      if (c < chunks) Vec::load_raw(x + c * N, a[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < CH; ++i) Vec::unpack(a[i], h[i]);
   }
+  float rs = 1.f;
   if (MODE == kRowsRms) {
-    ss = __uint_as_float(row_reduce<false>(__float_as_uint(ss), tpr, red));
-    m = row_reduce<true>(m, tpr, red);
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int j = 0; j < N; ++j) ss = fmaf(h[i][j], h[i][j], ss);
+    ss = row_sum(ss, tpr, red);
     float pre = 1.f;
-    if (tpr > 32 ? __syncthreads_or(rms_needs_scaling(m)) : rms_needs_scaling(m)) {
-      if (rms_needs_scaling(m)) pre = rms_prescale(m);
+    const bool holds = rms_sum_holds(ss);
+    if (tpr > 32 ? __syncthreads_or(!holds) : !holds) {
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+#pragma unroll
+        for (int j = 0; j < N; ++j) m = max_abs(m, h[i][j]);
+      const uint32_t top = row_max(m, tpr, red);
+      if (!holds && rms_needs_scaling(top)) pre = rms_prescale(top);
       float again = 0.f;
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i)
+      for (int i = 0; i < CH; ++i)
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           h[i][j] *= pre;
           again = fmaf(h[i][j], h[i][j], again);
         }
-      ss = __uint_as_float(row_reduce<false>(__float_as_uint(again), tpr, red));
+      ss = row_sum(again, tpr, red);
     }
-    const float rs = rms_factor(ss, p.d, p.eps, pre);
-    m = 0;
+    rs = rms_factor(ss, p.d, p.eps, pre);
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
+    for (int i = 0; i < CH; ++i) {
       const int c = lane + i * tpr;
       if (c < chunks) {
         float u[N];
-        Vec::load(w + c * N, u);
+        Vec::load(static_cast<const T *>(p.w) + c * N, u);
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          h[i][j] = h[i][j] * rs * u[j];
-          m = max(m, abs_bits(h[i][j]));
-        }
+        for (int j = 0; j < N; ++j) h[i][j] = h[i][j] * rs * u[j];
       }
     }
   }
-  m = row_reduce<true>(m, tpr, red);
-  const float2 sc = row_scale(m);
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < CH; ++i)
+#pragma unroll
+    for (int j = 0; j < N; ++j) m = max_abs(m, h[i][j]);
+  const float2 sc = row_scale(row_max(m, tpr, red));
   if (live && lane == 0) p.scale[row] = sc.x;
   uint8_t *out = p.out + row * p.ldo;
 #pragma unroll
-  for (int i = 0; i < kChunks; ++i) {
+  for (int i = 0; i < CH; ++i) {
     const int c = lane + i * tpr;
     if (c < chunks) {
       if constexpr (N == 1) {
