@@ -118,54 +118,86 @@ __global__ void __launch_bounds__(kLinThreads, 2)
   __syncwarp();
   tc_fence_after();
 
-  T *out = static_cast<T *>(p.out);
+  // The accumulator's lanes are channels: it goes through shared memory as [token][128] so that a
+  // warp writes a token's 128 channels in a row.  CTA `rank` adds up every split-th token.
   const int tokens = min(p.nt, p.M - m0);
-  const int feat = n0 + warp * 32 + lane;
-  float *part = reinterpret_cast<float *>(ring);  // [token][128], split > 1
+  float *part = reinterpret_cast<float *>(ring);
   if (warp < 4) {
-    pdl_wait();
-    pdl_launch_dependents();
-    const float ws = feat < p.N ? p.ws[feat] : 0.f;
-    const float bias = p.bias && feat < p.N ? p.bias[feat] : 0.f;
     for (int t0 = 0; t0 < tokens; t0 += 16) {
       uint32_t r[16];
       tmem_ld16_issue(tmem + (static_cast<uint32_t>(warp * 32) << 16) + t0, r);
       tmem_ld16_wait(r);
-      if (split > 1) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          part[(t0 + j) * kLinRows + warp * 32 + lane] = __uint_as_float(r[j]);
-      } else if (feat < p.N) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (t0 + j < tokens) {
-            const long long row = m0 + t0 + j;
-            out[row * p.ldo + feat] = from_f32<T>(__uint_as_float(r[j]) * p.xs[row] * ws + bias);
-          }
-      }
+      for (int j = 0; j < 16; ++j)
+        part[(t0 + j) * kLinRows + warp * 32 + lane] = __uint_as_float(r[j]);
     }
-    if (split > 1) {
-      __syncwarp();
-      cluster_sync();
-      if (feat < p.N)
-        for (int t = rank; t < tokens; t += split) {
-          float v = 0.f;
-          const uint32_t at = smem_u32(part + t * kLinRows + warp * 32 + lane);
-          for (int s = 0; s < split; ++s) v += ld_cluster_f32(mapa_shared(at, s));
-          const long long row = m0 + t;
-          out[row * p.ldo + feat] = from_f32<T>(v * p.xs[row] * ws + bias);
-        }
-      __syncwarp();
-      cluster_sync();  // nobody leaves while its part is being read
-    }
-  } else if (split > 1) {
-    __syncwarp();
-    cluster_sync();
-    cluster_sync();
   }
   tc_fence_before();
-  __syncthreads();
-  if (warp == 5) tmem_dealloc(tmem, p.tmem_cols);
+  __syncwarp();
+  if (split > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, p.tmem_cols);
+  }
+  pdl_wait();
+  T *out = static_cast<T *>(p.out);
+  const int n = n0 + 4 * lane;  // this lane's four channels
+  float ws[4], bias[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    ws[j] = n + j < p.N ? p.ws[n + j] : 0.f;
+    bias[j] = p.bias && n + j < p.N ? p.bias[n + j] : 0.f;
+  }
+  // the reads of 4 tokens are in flight together
+  constexpr int kWarps = kLinThreads / 32, kTogether = 4;
+  for (int t0 = rank + split * warp; t0 < tokens; t0 += kTogether * kWarps * split) {
+    float4 v[kTogether];
+    float xs[kTogether];
+#pragma unroll
+    for (int j = 0; j < kTogether; ++j) {
+      const int t = t0 + j * kWarps * split;
+      v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      xs[j] = t < tokens ? p.xs[m0 + t] : 0.f;
+    }
+    for (int s = 0; s < split; ++s) {
+      const uint32_t from = mapa_shared(smem_u32(part + 4 * lane), s);
+      float4 r[kTogether];
+#pragma unroll
+      for (int j = 0; j < kTogether; ++j) {
+        const int t = t0 + j * kWarps * split;
+        r[j] = t < tokens ? ld_cluster_f32x4(from + t * (kLinRows * 4))
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int j = 0; j < kTogether; ++j)
+        v[j].x += r[j].x, v[j].y += r[j].y, v[j].z += r[j].z, v[j].w += r[j].w;
+    }
+#pragma unroll
+    for (int j = 0; j < kTogether; ++j) {
+      const int t = t0 + j * kWarps * split;
+      if (t >= tokens) continue;
+      T *dst = out + static_cast<long long>(m0 + t) * p.ldo + n;
+      const float f[4] = {fmaf(v[j].x * xs[j], ws[0], bias[0]), fmaf(v[j].y * xs[j], ws[1], bias[1]),
+                          fmaf(v[j].z * xs[j], ws[2], bias[2]), fmaf(v[j].w * xs[j], ws[3], bias[3])};
+      if (n + 4 <= p.N && reinterpret_cast<uintptr_t>(dst) % (4 * sizeof(T)) == 0) {
+        if constexpr (sizeof(T) == 4)
+          *reinterpret_cast<float4 *>(dst) = make_float4(f[0], f[1], f[2], f[3]);
+        else
+          *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (n + k < p.N) dst[k] = from_f32<T>(f[k]);
+      }
+    }
+  }
+  if (split > 1) {
+    __syncwarp();
+    cluster_sync();  // nobody leaves while its part is being read
+  }
 }
 
 // Many tokens: 256 tokens x 256 channels by a pair of CTAs that share one MMA (cta_group::2).  Each

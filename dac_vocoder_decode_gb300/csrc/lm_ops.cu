@@ -284,8 +284,15 @@ voc_status encode_rows(CUtensorMap *map, const void *base, long long rows, long 
   return VOC_OK;
 }
 
-// From this many tokens a product runs on 256 x 256 tiles of CTA pairs.
-constexpr int kManyTokens = 512;
+// Whether a product runs on 256 x 256 tiles of CTA pairs: above 128 tokens and with 32 such tiles or
+// more.  Measured (us, pairs / split K) at N x K = 12288 x 4096: 128 tokens 16.4 / 16.6, 256 tokens
+// 16.9 / 23.1; at 2048 x 8192: 400 tokens (16 tiles) 22.6 / 14.0; at 4096 x 4096: 400 tokens (32
+// tiles) 14.4 / 13.7.
+bool many_tokens(int M, int N) {
+  const long long jobs = static_cast<long long>((M + voc::kManyTile - 1) / voc::kManyTile) *
+                         ((N + voc::kManyTile - 1) / voc::kManyTile);
+  return M > 128 && jobs >= 32;
+}
 
 template <typename T>
 cudaError_t launch_many(int sms, const CUtensorMap &xm, const CUtensorMap &wm,
@@ -339,7 +346,7 @@ VOC_API voc_status vocoder_lm_linear_fp8(const void *x8, long long ldx, const fl
   a.chunks = (K + voc::kLinK - 1) / voc::kLinK;
   CUtensorMap xm, wm;
   cudaError_t e;
-  if (M >= kManyTokens) {
+  if (many_tokens(M, N)) {
     if (voc_status st = encode_rows(&xm, x8, M, K, ldx, 128); st != VOC_OK) return st;
     if (voc_status st = encode_rows(&wm, w8, N, K, ldw, 128); st != VOC_OK) return st;
     if (out_dtype == VOC_LM_F32)
@@ -351,7 +358,8 @@ VOC_API voc_status vocoder_lm_linear_fp8(const void *x8, long long ldx, const fl
     if (e != cudaSuccess) return cuda_fail(e, "launch linear");
     return finish(*dev, stream, flags);
   }
-  a.nt = std::min(256, (M + 15) / 16 * 16);
+  const int m_tiles = (M + 255) / 256;
+  a.nt = ((M + m_tiles - 1) / m_tiles + 15) / 16 * 16;  // equal tiles of up to 256 tokens
   if ((M + a.nt - 1) / a.nt > 65535) return fail(VOC_UNSUPPORTED, "linear: too many rows");
   a.tmem_cols = 32;
   while (a.tmem_cols < a.nt) a.tmem_cols *= 2;
