@@ -207,15 +207,24 @@ __global__ void __launch_bounds__(kLinThreads, 2)
 constexpr int kManyTile = 256;
 constexpr int kManyStage = 2 * 128 * kLinK;  // bytes of a stage in each CTA
 constexpr int kManyStages = 6;
-constexpr int kManyOut = 4 * 32 * 128;       // output staging: 32 rows of 128 bytes for each warp
+constexpr int kManyOut = 8 * 32 * 64;        // output staging: 32 rows of 64 bytes for each warp
 constexpr size_t kManySmem = static_cast<size_t>(kManyStages) * kManyStage + kManyOut + 1024;
 
-// 16 bytes of an output row, as far as the row goes (`left` values).
+// 16 bytes of an output row, as far as the row goes (`left` values), in the widest stores that its
+// place allows.
 template <typename T>
 __device__ __forceinline__ void store_out16(T *dst, const uint4 &v, int left) {
   constexpr int kPer = 16 / static_cast<int>(sizeof(T));
-  if (left >= kPer && (reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
+  const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst)) & 15;
+  if (left >= kPer && at == 0) {
     *reinterpret_cast<uint4 *>(dst) = v;
+  } else if (left >= kPer && at == 8) {
+    reinterpret_cast<uint2 *>(dst)[0] = make_uint2(v.x, v.y);
+    reinterpret_cast<uint2 *>(dst)[1] = make_uint2(v.z, v.w);
+  } else if (left >= kPer && at % 4 == 0) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t *>(dst)[i] = w[i];
   } else {
     T e[kPer];
     memcpy(e, &v, 16);
@@ -225,8 +234,11 @@ __device__ __forceinline__ void store_out16(T *dst, const uint4 &v, int left) {
   }
 }
 
+constexpr int kManyEpi = 8;                          // epilogue warps, two for each 32 token rows
+constexpr int kManyThreads = 32 * (kManyEpi + 2);    // and a copy warp and an MMA warp
+
 template <typename T>
-__global__ void __launch_bounds__(kLinThreads, 1) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(kManyThreads, 1) __cluster_dims__(2, 1, 1)
     linear_many_kernel(const __grid_constant__ CUtensorMap xmap,
                        const __grid_constant__ CUtensorMap wmap, const LmLinearArgs p) {
   extern __shared__ uint8_t smem_raw[];
@@ -257,14 +269,14 @@ __global__ void __launch_bounds__(kLinThreads, 1) __cluster_dims__(2, 1, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(acc_full + i), 1);
-      mbar_init(smem_u32(acc_empty + i), 2 * 4);  // the epilogue warps of both CTAs
+      mbar_init(smem_u32(acc_empty + i), 2 * kManyEpi);  // the epilogue warps of both CTAs
     }
     mbar_init(smem_u32(&drain), 1);
     mbar_init(smem_u32(&unused), 1);
     abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 5) {
+  if (warp == kManyEpi + 1) {
     tmem_alloc_pair(smem_u32(&tmem_slot), 512);
     tmem_relinquish_pair();
   }
@@ -273,7 +285,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) __cluster_dims__(2, 1, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
-  if (warp == 4) {
+  if (warp == kManyEpi) {
     if (lane == 0) {
       pdl_wait();
       pdl_launch_dependents();
@@ -302,7 +314,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) __cluster_dims__(2, 1, 1)
         mbar_wait(smem_u32(&unused), 0, p.budget, &never);
       }
     }
-  } else if (warp == 5 && rank == 0) {
+  } else if (warp == kManyEpi + 1 && rank == 0) {
     constexpr uint32_t kId = idesc_e4m3_f32(256, kManyTile);
     auto wait = [&](uint64_t *bar, int parity) {
       const bool got = mbar_wait_cluster(smem_u32(bar), parity, p.budget, abort);
@@ -338,44 +350,49 @@ __global__ void __launch_bounds__(kLinThreads, 1) __cluster_dims__(2, 1, 1)
     mma_commit_pair_warp(smem_u32(&drain), 1);
     mbar_wait_cluster(smem_u32(&drain), 0, 4 * p.budget, &never);
     __syncwarp();
-  } else if (warp < 4) {
-    // The accumulator's lanes are token rows.  A warp turns 32 rows x 128 bytes around in shared
-    // memory, so that its stores cover whole lines of 4 rows instead of a sector of 32 rows.
+  } else if (warp < kManyEpi) {
+    // The accumulator's lanes are token rows.  A warp takes 32 rows of half of the columns and turns
+    // pieces of 32 rows x 64 bytes around in shared memory, so that its stores fill whole sectors.
     pdl_wait();
     pdl_launch_dependents();
-    constexpr int kCols = 128 / static_cast<int>(sizeof(T));  // columns of a staged piece
+    constexpr int kCols = 64 / static_cast<int>(sizeof(T));  // columns of a staged piece
     constexpr int kPer = 16 / static_cast<int>(sizeof(T));
+    const int quad = warp % 4, c_first = warp / 4 * (kManyTile / 2);
     T *out = static_cast<T *>(p.out);
     const uint32_t empty0 = mapa_shared(smem_u32(acc_empty), 0u);
-    const uint32_t stage = smem_u32(ring) + kManyStages * kManyStage + warp * (32 * 128);
+    const uint32_t stage = smem_u32(ring) + kManyStages * kManyStage + warp * (32 * 64);
     int k = 0;
     for (long long job = job0; job < jobs; job += step, ++k) {
       const int acc = k & 1;
       const int row0 = static_cast<int>(job / n_tiles) * kManyTile + 128 * static_cast<int>(rank) +
-                       warp * 32;
+                       quad * 32;
       const int n0 = static_cast<int>(job % n_tiles) * kManyTile;
       const int cols = min(kManyTile, p.N - n0);
-      for (int c = threadIdx.x; c < kManyTile; c += 128) {
+      for (int c = threadIdx.x; c < kManyTile; c += 32 * kManyEpi) {
         col_scale[acc][c] = c < cols ? p.ws[n0 + c] : 0.f;
         col_bias[acc][c] = p.bias && c < cols ? p.bias[n0 + c] : 0.f;
       }
       const float xs = row0 + lane < p.M ? p.xs[row0 + lane] : 0.f;
-      asm volatile("bar.sync 1, 128;" ::: "memory");  // the epilogue warps
+      asm volatile("bar.sync 1, 256;" ::: "memory");  // the epilogue warps
       const bool got = mbar_wait_cluster(smem_u32(acc_full + acc), (k / 2) & 1, 4 * p.budget, abort);
       if (!__all_sync(0xffffffffu, got)) {
         if (lane == 0) raise();
         break;
       }
       tc_fence_after();
-      for (int c0 = 0; c0 < cols; c0 += kCols) {
+      const int c_end = min(cols, c_first + kManyTile / 2);
+      for (int c0 = c_first; c0 < c_end; c0 += kCols) {
         uint32_t r[kCols];
-#pragma unroll
-        for (int i = 0; i < kCols / 32; ++i)
-          tmem_ld32_issue(tmem + (static_cast<uint32_t>(warp * 32) << 16) + acc * kManyTile + c0 +
-                              32 * i, r + 32 * i);
-        tmem_ld_wait_all();
-#pragma unroll
-        for (int i = 0; i < kCols / 32; ++i) tmem_ld32_after_wait(r + 32 * i);
+        const uint32_t from =
+            tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * kManyTile + c0;
+        if constexpr (kCols == 32) {
+          tmem_ld32_issue(from, r);
+          tmem_ld_wait_all();
+          tmem_ld32_after_wait(r);
+        } else {
+          tmem_ld16_issue(from, r);
+          tmem_ld16_wait(r);
+        }
         __syncwarp();  // the previous piece has been read
 #pragma unroll
         for (int i = 0; i < kCols; i += kPer) {
@@ -391,13 +408,13 @@ __global__ void __launch_bounds__(kLinThreads, 1) __cluster_dims__(2, 1, 1)
           }
           uint4 v;
           memcpy(&v, e, 16);
-          sts128(stage + lane * 128 + (((i / kPer) ^ (lane & 7)) << 4), v);
+          sts128(stage + lane * 64 + (((i / kPer) ^ (lane >> 1 & 3)) << 4), v);
         }
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int rr = 4 * i + lane / 8, u = lane % 8, c = c0 + u * kPer;
-          const uint4 v = lds128(stage + rr * 128 + ((u ^ (rr & 7)) << 4));
+        for (int i = 0; i < 4; ++i) {
+          const int rr = 8 * i + lane / 4, u = lane % 4, c = c0 + u * kPer;
+          const uint4 v = lds128(stage + rr * 64 + ((u ^ (rr >> 1 & 3)) << 4));
           if (row0 + rr < p.M && c < cols)
             store_out16(out + static_cast<long long>(row0 + rr) * p.ldo + n0 + c, v, cols - c);
         }
@@ -410,7 +427,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) __cluster_dims__(2, 1, 1)
   __syncwarp();
   tc_fence_before();
   cluster_sync();  // neither CTA leaves while the other may reach its barriers
-  if (warp == 5) {
+  if (warp == kManyEpi + 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }

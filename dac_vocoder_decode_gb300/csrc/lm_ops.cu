@@ -65,6 +65,7 @@ struct Device {
   cudaError_t err = cudaSuccess;
   int sms = 0;
   int *timeout = nullptr;
+  int clusters[9] = {};  // clusters of 1..8 CTAs of the split-K product that run at once
 };
 Device g_devices[kMaxDevices];
 
@@ -74,7 +75,25 @@ void allow_smem(cudaError_t &e, K kernel, size_t bytes) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(bytes));
 }
-constexpr size_t kLinSmem = 220 * 1024;
+constexpr size_t kLinSmem = 220 * 1024;       // one CTA of the split-K product on an SM
+constexpr size_t kLinSmemTwo = 108 * 1024;    // two
+
+// Clusters of `size` CTAs (along z) of `kernel` that run at once.
+template <typename K>
+cudaError_t count_clusters(int *out, K kernel, int threads, size_t smem, int size) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1, 1, size);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = size;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaOccupancyMaxActiveClusters(out, kernel, &cfg);
+}
 
 // The current device, set up on first use (shared-memory limits of the kernels, SM count).
 voc_status device(Device **out) {
@@ -108,6 +127,9 @@ voc_status device(Device **out) {
     allow_smem(er, linear_few_kernel<float>, kLinSmem);
     allow_smem(er, linear_few_kernel<__half>, kLinSmem);
     allow_smem(er, linear_few_kernel<__nv_bfloat16>, kLinSmem);
+    for (int size = 1; size <= 8 && er == cudaSuccess; ++size)
+      er = count_clusters(&dev.clusters[size], linear_few_kernel<__nv_bfloat16>, kLinThreads,
+                          kLinSmem, size);
   });
   if (dev.err != cudaSuccess) return cuda_fail(dev.err, "lm: device set-up");
   *out = &dev;
@@ -300,7 +322,7 @@ cudaError_t launch_many(int sms, const CUtensorMap &xm, const CUtensorMap &wm,
   const long long jobs = static_cast<long long>((a.M + voc::kManyTile - 1) / voc::kManyTile) *
                          ((a.N + voc::kManyTile - 1) / voc::kManyTile);
   const unsigned pairs = static_cast<unsigned>(std::min<long long>(sms / 2, jobs));
-  return launch(voc::linear_many_kernel<T>, dim3(2 * pairs), dim3(voc::kLinThreads),
+  return launch(voc::linear_many_kernel<T>, dim3(2 * pairs), dim3(voc::kManyThreads),
                 voc::kManySmem, 1, stream, xm, wm, a);
 }
 
@@ -363,14 +385,19 @@ VOC_API voc_status vocoder_lm_linear_fp8(const void *x8, long long ldx, const fl
   if ((M + a.nt - 1) / a.nt > 65535) return fail(VOC_UNSUPPORTED, "linear: too many rows");
   a.tmem_cols = 32;
   while (a.tmem_cols < a.nt) a.tmem_cols *= 2;
-  // two CTAs per SM where their rings are deep enough for it, and K split over up to 8 CTAs until
-  // there is one for every place
+  // Up to 64 tokens leave room for two CTAs on an SM.  K is split over up to 8 CTAs as long as all
+  // clusters run at once, and each keeps 4 stages of K once every SM has a CTA.  Measured at 33 tokens,
+  // N x K = 12288 x 4096 (96 tiles): split 1 14.7, 2 12.5, 3 12.8 (does not fit), 4 17.2 us; 8 tokens,
+  // 2048 x 8192 (16 tiles): split 1 21.9, 4 7.9, 8 5.9 us.
   const int stage = (voc::kLinRows + a.nt) * voc::kLinK;
   const int tiles = ((N + voc::kLinRows - 1) / voc::kLinRows) * ((M + a.nt - 1) / a.nt);
   const int per_sm = a.nt <= 64 ? 2 : 1;
-  const size_t smem = kLinSmem / per_sm - (per_sm - 1) * 2048;
+  const size_t smem = per_sm == 2 ? kLinSmemTwo : kLinSmem;
   a.stages = std::min<int>(12, static_cast<int>((smem - 1024) / stage));
-  const int split = std::max(1, std::min({8, per_sm * dev->sms / tiles, a.chunks / 2}));
+  int split = std::max(1, std::min(8, a.chunks / 2));
+  while (split > 1 && (per_sm * dev->clusters[split] < tiles ||
+                       (tiles * split > dev->sms && a.chunks / split < 4)))
+    --split;
   if (voc_status st = encode_rows(&xm, x8, M, K, ldx, a.nt); st != VOC_OK) return st;
   if (voc_status st = encode_rows(&wm, w8, N, K, ldw, voc::kLinRows); st != VOC_OK) return st;
   if (out_dtype == VOC_LM_F32)
