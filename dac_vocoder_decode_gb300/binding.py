@@ -758,9 +758,12 @@ class Encoder:
 # ------------------------------------------------------------------ 8-bit operators
 # One call of these is a few microseconds of host time beside kernels of the same length, so the
 # checks below stay with what is cheap to ask of a tensor; the library checks the rest.
+# The regular calls go through lm_torch.so (csrc/lm_torch.cpp), which marshals them in a fraction of
+# that; it hands back None where something is unusual or wrong, and the code here takes over.
 class _LM:
     """What the wrappers need of torch and the library, looked up with the first call."""
     ready = False
+    fast = None
 
 
 def _lm_setup():
@@ -776,6 +779,17 @@ def _lm_setup():
     # the current stream as an integer, without building a Stream object where torch allows it
     _LM.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                              lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    if os.path.exists(_build.TORCH_LIB):
+        import importlib.machinery
+        import importlib.util
+        loader = importlib.machinery.ExtensionFileLoader("lm_torch", _build.TORCH_LIB)
+        fast = importlib.util.module_from_spec(
+            importlib.util.spec_from_file_location("lm_torch", _build.TORCH_LIB, loader=loader))
+        loader.exec_module(fast)
+        fast.init(*(ctypes.cast(f, ctypes.c_void_p).value
+                    for f in (_LM.rows, _LM.linear, _LM.append, _LM.attention,
+                              _LM.attention_ws)))
+        _LM.fast = fast
     _LM.ready = True
 
 
@@ -831,6 +845,12 @@ def rows_fp8(x, mode: int = VOC_LM_RMS, weight=None, residual=None, eps: float =
     [rows], sum = x + residual in x's type, or None without a residual."""
     if not _LM.ready:
         _lm_setup()
+    if stream is None and _LM.fast is not None:
+        res = _LM.fast.rows(x, mode, weight, residual, eps, sum_out, out, scale, flags)
+        if res.__class__ is tuple:
+            return res
+        if res is not None:
+            _check(res)
     dtype, shape = x.dtype, x.shape
     code = _LM.types.get(dtype)
     if code is None or len(shape) != 2:
@@ -885,6 +905,14 @@ def linear_fp8(x, x_scale, w, w_scale, bias=None, out_dtype=None, out=None, stre
     vocoder_lm_linear_fp8 in include/vocoder.h)."""
     if not _LM.ready:
         _lm_setup()
+    if stream is None and _LM.fast is not None:
+        code = -1 if out_dtype is None else _LM.types.get(out_dtype)
+        if code is not None:
+            res = _LM.fast.linear(x, x_scale, w, w_scale, bias, code, out, flags)
+            if res.__class__ is int:
+                _check(res)
+            elif res is not None:
+                return res
     if x.dim() != 2 or w.dim() != 2:
         raise _bad("x and w must be 2-d float8_e4m3fn tensors")
     f32 = _LM.f32
@@ -925,12 +953,23 @@ class KVCacheFP8:
     """A pool of 64-token blocks of e4m3 keys and values: k [pages, kv_heads, 64, d] and v [pages,
     kv_heads, d, 64] float8_e4m3fn, k_scale and v_scale fp32 [pages, kv_heads] (see the cache in
     include/vocoder.h)."""
-    __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "kv_heads", "head_dim", "device_index",
-                 "_args")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "_args")
 
     def __init__(self, k, v, k_scale, v_scale):
         if not _LM.ready:
             _lm_setup()
+        # addresses, pages, key heads, head_dim, device
+        args = _LM.fast.cache(k, v, k_scale, v_scale) if _LM.fast is not None else None
+        self._args = self._checked(k, v, k_scale, v_scale) if args is None else args
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+
+    pages = property(lambda self: self._args[4])
+    kv_heads = property(lambda self: self._args[5])
+    head_dim = property(lambda self: self._args[6])
+    device_index = property(lambda self: self._args[7])
+
+    @staticmethod
+    def _checked(k, v, k_scale, v_scale):
         shape = k.shape
         if len(shape) != 4 or shape[2] != VOC_LM_BLOCK:
             raise _bad("k must be [pages, kv_heads, 64, head_dim]")
@@ -944,10 +983,8 @@ class KVCacheFP8:
             if t.dtype != dtype or not t.is_contiguous() or t.get_device() != dev:
                 raise _bad("the cache is contiguous float8_e4m3fn codes and fp32 scales on one "
                            "device")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.pages, self.kv_heads, self.head_dim, self.device_index = pages, heads, d, dev
-        self._args = (k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages,
-                      heads, d)
+        return (k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, heads,
+                d, dev)
 
     @classmethod
     def empty(cls, pages: int, kv_heads: int, head_dim: int, device="cuda"):
@@ -981,6 +1018,12 @@ def kv_append_fp8(cache: KVCacheFP8, k, v, page_table, kv_lens, cu_q=None, max_q
     vocoder_lm_kv_append in include/vocoder.h).  page_table int32 [sequences, blocks], kv_lens
     int32 [sequences] with the new tokens counted, cu_q int32 [sequences + 1] or None when every
     sequence has max_q new tokens."""
+    if stream is None and _LM.fast is not None:
+        res = _LM.fast.append(cache._args, k, v, page_table, kv_lens, cu_q, max_q, flags)
+        if res is not None:
+            if res:
+                _check(res)
+            return
     dev, batch = _batch_args(cache, k, page_table, kv_lens, cu_q)
     shape, ks, vs = k.shape, k.stride(), v.stride()
     code = _LM.types.get(k.dtype)
@@ -988,7 +1031,7 @@ def kv_append_fp8(cache: KVCacheFP8, k, v, page_table, kv_lens, cu_q=None, max_q
             v.shape != shape or code is None or v.dtype != k.dtype or ks[2] != 1 or \
             vs[2] != 1 or v.get_device() != dev:
         raise _bad("k and v must be [tokens, kv_heads, head_dim] of one type, head_dim contiguous")
-    st = _LM.append(*cache._args, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], code,
+    st = _LM.append(*cache._args[:7], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], code,
                     *batch, shape[0], max_q, _lm_stream(dev, stream, ()), flags)
     if st:
         _check(st)
@@ -1002,6 +1045,14 @@ def attention_fp8(q, cache: KVCacheFP8, page_table, kv_lens, cu_q=None, max_q: i
     vocoder_lm_attention in include/vocoder.h; the batch as in kv_append_fp8).  max_kv: at least
     the largest kv_len (default: what the page table can hold); softmax_scale defaults to
     1/sqrt(head_dim); ws: uint8 workspace of vocoder_lm_attention_ws_bytes (a new one if None)."""
+    if stream is None and _LM.fast is not None:
+        res = _LM.fast.attention(q, cache._args, page_table, kv_lens, cu_q, max_q,
+                                 -1 if max_kv is None else max_kv, softmax_scale, causal, window,
+                                 out, ws, flags)
+        if res.__class__ is int:
+            _check(res)
+        elif res is not None:
+            return res
     dev, batch = _batch_args(cache, q, page_table, kv_lens, cu_q)
     shape, qs, dtype = q.shape, q.stride(), q.dtype
     code = _LM.types.get(dtype)
@@ -1026,7 +1077,7 @@ def attention_fp8(q, cache: KVCacheFP8, page_table, kv_lens, cu_q=None, max_q: i
             ws = made_ws = _LM.empty((need,), dtype=_LM.torch.uint8, device=q.device)
     elif ws.dtype != _LM.torch.uint8 or not ws.is_contiguous() or ws.get_device() != dev:
         raise _bad("ws must be contiguous uint8 on q's device")
-    st = _LM.attention(q.data_ptr(), qs[0], qs[1], code, heads, *cache._args, *batch, tokens,
+    st = _LM.attention(q.data_ptr(), qs[0], qs[1], code, heads, *cache._args[:7], *batch, tokens,
                        max_q, max_kv, softmax_scale, causal, window, out.data_ptr(), os_[0],
                        os_[1], None if ws is None else ws.data_ptr(),
                        0 if ws is None else ws.numel(),
