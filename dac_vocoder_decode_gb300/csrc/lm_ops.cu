@@ -498,7 +498,7 @@ struct AttnPlan {
 
 // Row kernel: two CTAs per SM in equal shares, unless no tile has more than two of the smallest
 // shares' blocks (then a tile is a CTA's) or there are too many sequences to count through.  Prompt
-// kernel: keys are split while there are fewer tiles than SMs, into parts of 4 key tiles or more.
+// kernel: keys are split while there are fewer tiles than SMs, into parts of 8 blocks or more.
 AttnPlan plan_attention(int sms, int n_seq, int max_q, int heads, int kv_heads, int head_dim,
                         int max_kv, int window) {
   AttnPlan p;
@@ -510,9 +510,9 @@ AttnPlan plan_attention(int sms, int n_seq, int max_q, int heads, int kv_heads, 
   if (p.prompt) {
     p.row_tiles = static_cast<int>((rows + voc::kPartRows - 1) / voc::kPartRows);
     const long long tiles = heads_all * ((rows + voc::kPrRows - 1) / voc::kPrRows);
-    const long long steps = keys / voc::kPrKeys + 1;
+    const long long steps = keys / voc::kBlockTokens + 1;
     const long long splits = tiles >= sms ? 1 : sms / tiles;
-    p.splits = static_cast<int>(std::max(1ll, std::min({splits, steps / 4, 65535ll / n_seq})));
+    p.splits = static_cast<int>(std::max(1ll, std::min({splits, steps / 8, 65535ll / n_seq})));
     if (p.splits > 1)
       p.slots = static_cast<size_t>(heads_all) * p.row_tiles * p.splits * voc::kPartRows;
   } else {

@@ -2,18 +2,23 @@
 // the 5th-generation tensor cores.
 //
 // A CTA takes 256 rows (queries that share a key head) as two tiles of 128 and walks over its keys
-// in tiles of 128 (two cache blocks):
+// one cache block of 64 at a time:
 //   warps 0..3, 4..7   one thread per row of the first / second row tile: softmax of the scores
 //   warps 8..11        convert K and V codes to f16 (exact) in shared memory
-//   warp 12            issues the products: S = Q K^T from shared memory, O += P V with P in
-//                      tensor memory, in the place of the scores it was made from
-// The two row tiles take turns: while one's scores go through its softmax, the tensor cores work
-// on the other's products.  Both operands are 16-bit: the codes are exact in f16 and the weights
-// keep 11 bits, where an e4m3 product would round queries and weights to 4.
+//   warps 12, 13       issue the products of the first / second row tile: S = Q K^T, O += P V
+//   warp 14            fetches the blocks' scales
+// The softmax threads take a tile's scores into registers and give them free at once, and P has a
+// place of its own, so a row tile's next scores are computed while its softmax is at work: neither
+// waits for the other in turn.  First operands come from tensor memory where it has room for them (at
+// 128 channels it is full with 2 x (128 O + 64 S + 32 P) + 64 Q columns: the second tile's Q stays in
+// shared memory), since a 128-row operand in shared memory costs each step 4 KB of its bandwidth
+// beside the conversions' stores.
+// Operands are 16-bit: the codes are exact in f16 and the weights keep 11 bits, where an e4m3
+// product would round queries and weights to 4.
 //
-// The running maximum that the weights are taken against (see lm_attention.cuh) is raised only
-// when a row's new maximum is more than 8 above it, so the accumulator is rarely rescaled; weights
-// are kept times 2^7 and stay below 2^15, inside f16.
+// The weights of a tile are taken against the maximum of the tiles before it, in one pass over the
+// scores; only where one comes out 2^8 or more too large (weights are kept times 2^7, so 2^15 in f16)
+// are the row's maximum raised, the accumulator rescaled and the tile's weights taken again.
 #pragma once
 #include "lm_attention.cuh"
 
@@ -21,7 +26,7 @@ namespace voc {
 
 constexpr int kPrThreads = 512;
 constexpr int kPrRows = 256;       // rows of a CTA
-constexpr int kPrKeys = 128;       // keys of a tile
+constexpr int kPrStages = 4;       // key tiles in shared memory
 constexpr int kPartRows = 16;      // rows of a tile of partial outputs
 // Registers: 256 softmax threads, 128 converting, 128 others: 256 x 184 + 128 x 104 + 128 x 40 =
 // 65536, the block's registers at launch (512 x 128).
@@ -30,11 +35,11 @@ static_assert(256 * kPrSoftRegs + 128 * kPrConvRegs + 128 * kPrRestRegs <= 512 *
 
 template <int D>
 struct PromptSmem {
-  static constexpr int kSlab = 128 * 128;               // 128 rows of 64 f16 values
-  static constexpr int kQ = D / 64 * kSlab;             // one row tile
+  static constexpr int kSlab = kBlockTokens * 128;      // 64 keys of 64 f16 values
   static constexpr int kK = D / 64 * kSlab;             // one key tile
-  static constexpr int kV = 2 * D * 128;                // two blocks of D rows of 64 keys
-  static constexpr size_t kBytes = 2 * kQ + 2 * kK + 2 * kV + 1024;
+  static constexpr int kV = D * 128;                    // D rows of 64 keys
+  static constexpr int kQ = D == 64 ? 0 : 2 * 128 * 128;  // the second row tile's queries
+  static constexpr size_t kBytes = kPrStages * (kK + kV) + kQ + 1024;
 };
 
 // The 16-byte unit `u` of a 128-byte row `r` in the 128-byte swizzle.
@@ -59,9 +64,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base_ptr = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const uint32_t sq = smem_u32(base_ptr), sk = sq + 2 * S::kQ, sv = sk + 2 * S::kK;
-  __shared__ __align__(8) uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2],
-      p_full[2], o_full;
+  const uint32_t sk = smem_u32(base_ptr), sv = sk + kPrStages * S::kK, sq = sv + kPrStages * S::kV;
+  __shared__ __align__(8) uint64_t q_full, k_full[kPrStages], k_empty[kPrStages],
+      v_full[kPrStages], v_empty[kPrStages], s_full[2], s_empty[2], p_full[2], p_empty[2],
+      sc_full[2], sc_empty[2], o_full[2];
+  __shared__ float4 scales[2][32];  // key scale, log2 and reciprocal of the value scale, by tile
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, wg = warp / 4;
@@ -71,26 +78,34 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
   const int b = blockIdx.z / p.splits, split = blockIdx.z % p.splits, hk = blockIdx.y;
   const SeqSpan span = seq_span(p.cu, b, p.n_seq, p.n_tokens, p.max_q);
   const int rows = span.count * p.group;
-  if (tid == 0) {
-    mbar_init(smem_u32(&q_full), 256);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(k_full + i), 128);
-      mbar_init(smem_u32(v_full + i), 128);
-      mbar_init(smem_u32(k_empty + i), 1);
-      mbar_init(smem_u32(v_empty + i), 1);
-      mbar_init(smem_u32(s_full + i), 1);
-      mbar_init(smem_u32(p_full + i), 128);
-    }
-    mbar_init(smem_u32(&o_full), 1);
-    abort_flag = 0;
-    fence_barrier_init();
-  }
   pdl_wait();
   pdl_launch_dependents();
   // the latest rows see the most keys: they start first
   const int tile_max = static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x);
   const int r0 = tile_max * kPrRows;
-  if (r0 >= span.count * p.group) return;  // the whole block, before any barrier or allocation
+  if (r0 >= rows) return;  // the whole block, before any barrier or allocation
+  const int r_last = min(rows, r0 + kPrRows) - 1;
+  const bool two = r_last - r0 >= 128;  // the second row tile has rows
+  if (tid == 0) {
+    mbar_init(smem_u32(&q_full), 256);
+    for (int i = 0; i < kPrStages; ++i) {
+      mbar_init(smem_u32(k_full + i), 128);
+      mbar_init(smem_u32(v_full + i), 128);
+      mbar_init(smem_u32(k_empty + i), two ? 2 : 1);
+      mbar_init(smem_u32(v_empty + i), two ? 2 : 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(s_full + i), 1);
+      mbar_init(smem_u32(s_empty + i), 128);
+      mbar_init(smem_u32(p_full + i), 128);
+      mbar_init(smem_u32(p_empty + i), 1);
+      mbar_init(smem_u32(sc_full + i), 1);
+      mbar_init(smem_u32(sc_empty + i), two ? 8 : 4);
+      mbar_init(smem_u32(o_full + i), 1);
+    }
+    abort_flag = 0;
+    fence_barrier_init();
+  }
   if (warp == 12) {
     tmem_alloc(smem_u32(&tmem_slot), 512);
     tmem_relinquish();
@@ -98,26 +113,22 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;  // scores 0..127 and 128..255, outputs from 256
-  const int r_last = min(rows, r0 + kPrRows) - 1;
-  const bool two = r_last - r0 >= 128;  // the second row tile has rows
+  const uint32_t tmem = tmem_slot;  // columns: two outputs, two scores, two weights, queries
+  constexpr uint32_t kColS = 2 * D, kColP = kColS + 2 * kBlockTokens, kColQ = kColP + kBlockTokens;
   const long long len = max(0ll, min(static_cast<long long>(p.lens[b]),
                                      static_cast<long long>(p.table_cols) * kBlockTokens));
   const long long p0 = static_cast<long long>(p.lens[b]) - span.count;
   const long long key_lo = visible(p, p0 + r0 / p.group, len).lo;
   const long long key_hi = visible(p, p0 + r_last / p.group, len).hi;
-  const long long tile0 = key_lo / kPrKeys;
-  const long long n_all = key_hi > key_lo ? (key_hi - 1) / kPrKeys + 1 - tile0 : 0;
+  const long long tile0 = key_lo / kBlockTokens;
+  const long long n_all = key_hi > key_lo ? (key_hi - 1) / kBlockTokens + 1 - tile0 : 0;
   const long long per = (n_all + p.splits - 1) / p.splits;
   const long long first = tile0 + min(n_all, split * per);
   const int n = static_cast<int>(min(n_all, (split + 1) * per) - min(n_all, split * per));
-  const int *table = p.table + b * p.ldt;
-  // page of a block, or -1 where the CTA sees none of its keys
-  auto page_of = [&](long long blk) {
-    if (blk * kBlockTokens >= key_hi || (blk + 1) * kBlockTokens <= key_lo) return -1;
-    const int page = table[blk];
-    return page >= 0 && page < p.n_pages ? page : -1;
-  };
+  // page of key tile kt (not yet checked: a use right behind the load would wait for it)
+  const int *table = p.table + b * p.ldt + first;
+  auto page_of = [&](int kt) { return kt < n ? table[kt] : -1; };
+  auto known = [&](int page) { return page >= 0 && page < p.n_pages; };
 
   if (wg < 2) {
     regs_inc<kPrSoftRegs>();
@@ -157,134 +168,135 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
       const int e = query_exponent(a);
       const float up = pow2(e) * flip;
       qc = fabsf(p.scale_log2) * pow2(-e);
+      uint32_t h[D / 2];
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
         float f[8];
         Vec16<T>::unpack(raw[i], f);
-        uint32_t h[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = f16x2(f[2 * j] * up, f[2 * j + 1] * up);
-        sts128(sq + wg * S::kQ + i / 8 * S::kSlab + sw128(local, i % 8),
-               make_uint4(h[0], h[1], h[2], h[3]));
+        for (int j = 0; j < 4; ++j) h[4 * i + j] = f16x2(f[2 * j] * up, f[2 * j + 1] * up);
+      }
+      if (D == 64 || wg == 0) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+          tmem_st32(tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16) + kColQ + wg * (D / 2) +
+                        32 * i, h + 32 * i);
+        tmem_st_wait();
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          sts128(sq + i / 8 * (128 * 128) + sw128(local, i % 8),
+                 make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]));
+        fence_proxy_async_smem();
       }
     }
-    fence_proxy_async_smem();
+    tc_fence_before();
     mbar_arrive(smem_u32(&q_full));
 
     const uint32_t lane_base = static_cast<uint32_t>((warp % 4) * 32) << 16;
-    const uint32_t s_addr = tmem + lane_base + wg * 128, o_addr = tmem + lane_base + 256 + wg * D;
+    const uint32_t s_addr = tmem + lane_base + kColS + wg * kBlockTokens;
+    const uint32_t p_addr = tmem + lane_base + kColP + wg * (kBlockTokens / 2);
+    const uint32_t o_addr = tmem + lane_base + wg * D;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     if (wg == 0 || two) {
-      // scales of the tile's two blocks, one tile ahead of their use; pages two ahead
-      int pg[2] = {page_of(2 * first), page_of(2 * first + 1)};
-      float ks[2], vs[2];
-      auto load_scales = [&]() {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const long long slot = static_cast<long long>(pg[h]) * p.kv_heads + hk;
-          ks[h] = pg[h] >= 0 ? p.ks[slot] : 1.f;
-          vs[h] = pg[h] >= 0 ? p.vs[slot] : 0.f;
-        }
-      };
-      if (n > 0) load_scales();
-      if (n > 1) pg[0] = page_of(2 * (first + 1)), pg[1] = page_of(2 * (first + 1) + 1);
-      for (int kt = 0; kt < n; ++kt) {
-        float c[2], lvs[2], ivs[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float v = fmaxf(vs[h], kScaleMin);
-          c[h] = fmaxf(qc * ks[h], 1e-37f);  // above 0: masked scores stay -inf
-          lvs[h] = vs[h] == 0.f ? -INFINITY : log2f(v);  // no page: no weight
-          ivs[h] = vs[h] == 0.f ? 0.f : 1.f / v;
-        }
-        if (kt + 1 < n) {
-          load_scales();
-          if (kt + 2 < n) {
-            pg[0] = page_of(2 * (first + kt + 2));
-            pg[1] = page_of(2 * (first + kt + 2) + 1);
-          }
-        }
-        ok = mbar_wait(smem_u32(s_full + wg), kt & 1, p.budget, abort);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
+      auto wait = [&](uint64_t *bar, int parity) {
+        const bool got = mbar_wait(smem_u32(bar), parity, p.budget, abort);
+        if (!__all_sync(0xffffffffu, got)) {
           *abort = 1;
-          break;
+          ok = false;
         }
+        return ok;
+      };
+      for (int kt = 0; kt < n; ++kt) {
+        if (kt % 32 == 0 && !wait(sc_full + (kt / 32 & 1), kt / 64 & 1)) break;
+        const float4 block = scales[kt / 32 & 1][kt % 32];
+        const float c = fmaxf(qc * block.x, 1e-37f);  // above 0: masked scores stay -inf
+        const float lvs = block.y, ivs = block.z;
+        if (!wait(s_full + wg, kt & 1)) break;
         tc_fence_after();
-        uint32_t sc[128];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32_issue(s_addr + 32 * i, sc + 32 * i);
+        uint32_t sc[kBlockTokens];
+        tmem_ld32_issue(s_addr, sc);
+        tmem_ld32_issue(s_addr + 32, sc + 32);
         tmem_ld_wait_all();
+        tmem_ld32_after_wait(sc);
+        tmem_ld32_after_wait(sc + 32);
+        tc_fence_before();
+        mbar_arrive(smem_u32(s_empty + wg));
+        // the row's keys of this tile, where it does not see them all
+        const long long base = (first + kt) * kBlockTokens;
+        if (__any_sync(0xffffffffu, base < see.lo || base + kBlockTokens > see.hi)) {
+          const int from = static_cast<int>(max(-1ll, min(see.lo - base, 64ll)));
+          const int upto = static_cast<int>(max(-1ll, min(see.hi - base, 64ll)));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32_after_wait(sc + 32 * i);
-        const long long base = (first + kt) * kPrKeys;
-        if (__any_sync(0xffffffffu, base < see.lo || base + kPrKeys > see.hi)) {
-          const int a = static_cast<int>(max(-1ll, min(see.lo - base, 128ll)));
-          const int z = static_cast<int>(max(-1ll, min(see.hi - base, 128ll)));
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i < a || i >= z) sc[i] = 0xff800000u;
+          for (int i = 0; i < kBlockTokens; ++i)
+            if (i < from || i >= upto) sc[i] = 0xff800000u;
         }
-        float top[2];
+        uint32_t w[kBlockTokens / 2];
+        bool raise = __any_sync(0xffffffffu, m == -INFINITY);
+        while (true) {
+          if (raise) {  // a look at the maximum, and the row's weights taken against it from here on
+            float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float t0 = -INFINITY, t1 = -INFINITY;
+            for (int i = 0; i < kBlockTokens; ++i) t[i % 4] = fmaxf(t[i % 4], __uint_as_float(sc[i]));
+            const float nm = fmaf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), c, lvs);
+            float alpha = 1.f;
+            if (nm > m + kLazy || (m == -INFINITY && nm > m)) {
+              alpha = ex2(m - nm);
+              m = nm;
+            }
+            l *= alpha;
+            if (kt > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+              if (!wait(p_empty + wg, (kt - 1) & 1)) break;  // O is at rest
+              tc_fence_after();
 #pragma unroll
-          for (int i = 0; i < 64; i += 2) {
-            t0 = fmaxf(t0, __uint_as_float(sc[64 * h + i]));
-            t1 = fmaxf(t1, __uint_as_float(sc[64 * h + i + 1]));
+              for (int i = 0; i < D / 16; ++i) {
+                uint32_t o[16];
+                tmem_ld16_issue(o_addr + 16 * i, o);
+                tmem_ld16_wait(o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                tmem_st16(o_addr + 16 * i, o);
+              }
+            }
           }
-          top[h] = fmaf(fmaxf(t0, t1), c[h], lvs[h]);
-        }
-        const float nm = fmaxf(top[0], top[1]);
-        float alpha = 1.f;
-        if (nm > m + kLazy || (m == -INFINITY && nm > m)) {
-          alpha = ex2(m - nm);
-          m = nm;
-        }
-        const float off = (m == -INFINITY ? 0.f : m) - kPShift;
-        l *= alpha;
-        if (kt > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          // the products that this tile's scores were issued behind are done: O is at rest
+          const float d = lvs - ((m == -INFINITY ? 0.f : m) - kPShift);
+          const float2 cc = make_float2(c, c), dd = make_float2(d, d);
+          uint32_t big = 0;
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t o[32];
-            tmem_ld32_issue(o_addr + 32 * i, o);
-            tmem_ld_wait_all();
-            tmem_ld32_after_wait(o);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-            tmem_st32(o_addr + 32 * i, o);
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float2 cc = make_float2(c[h], c[h]);
-          const float d = lvs[h] - off;
-          const float2 dd = make_float2(d, d);
-          float2 sum = make_float2(0.f, 0.f);
-          uint32_t w[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float2 u = fma2(make_float2(__uint_as_float(sc[64 * h + 2 * i]),
-                                        __uint_as_float(sc[64 * h + 2 * i + 1])),
+          for (int i = 0; i < kBlockTokens / 2; ++i) {
+            float2 u = fma2(make_float2(__uint_as_float(sc[2 * i]), __uint_as_float(sc[2 * i + 1])),
                             cc, dd);
             u.x = ex2(u.x), u.y = ex2(u.y);
-            sum = add2(sum, u);
+            sum[i % 2] = add2(sum[i % 2], u);
             w[i] = f16x2(u.x, u.y);
+            big = __vmaxu2(big, w[i]);
           }
-          tmem_st32(s_addr + 32 * h, w);
-          l = fmaf(sum.x + sum.y, ivs[h], l);
+          // weights are positive, so their bits order them: 2^15 and above (NaN too) is too far ahead
+          const bool far = (big & 0xffffu) >= 0x7800u || (big >> 16) >= 0x7800u;
+          if (raise || !__any_sync(0xffffffffu, far)) {
+            l = fmaf((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y), ivs, l);
+            break;
+          }
+          raise = true;
         }
+        if (kt > 0 && !wait(p_empty + wg, (kt - 1) & 1)) break;  // the last weights are used up
+        tc_fence_after();
+        tmem_st32(p_addr, w);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(smem_u32(p_full + wg));
+        if (kt % 32 == 31) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(sc_empty + (kt / 32 & 1)));
+        }
       }
     }
     // outputs
     if (n > 0 && (wg == 0 || two)) {
-      const bool done = mbar_wait(smem_u32(&o_full), 0, 4 * p.budget, &never);
+      const bool done = mbar_wait(smem_u32(o_full + wg), 0, 4 * p.budget, &never);
       if (!__all_sync(0xffffffffu, done)) *abort = 1;
       tc_fence_after();
     }
@@ -335,85 +347,77 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
   } else if (wg == 2) {
     regs_dec<kPrConvRegs>();
     const int ct = tid - 256, quarter = ct % 4, row0 = ct / 4;
-    constexpr int kSlabs = D / 64;
-    uint4 kr[4 * kSlabs], vr[2 * (D / 32)];
-    int pg[2], next[2];
-    auto pages = [&](int kt, int (&to)[2]) {
-      to[0] = kt < n ? page_of(2 * (first + kt)) : -1;
-      to[1] = kt < n ? page_of(2 * (first + kt) + 1) : -1;
-    };
+    constexpr int kPerK = 2 * (D / 64), kPerV = D / 32;  // 16-code pieces of a thread
+    uint4 kr[kPerK], vr[kPerV];
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    auto load_k = [&](const int (&from)[2]) {
+    auto load_k = [&](int page) {
 #pragma unroll
-      for (int i = 0; i < 4 * kSlabs; ++i) {
-        const int row = row0 + 32 * (i % 4), slab = i / 4, page = from[i % 4 / 2];
-        kr[i] = page < 0 ? zero
-                         : *reinterpret_cast<const uint4 *>(
-                               p.kc + ((static_cast<long long>(page) * p.kv_heads + hk) *
-                                           kBlockTokens + row % kBlockTokens) * D +
-                               64 * slab + 16 * quarter);
+      for (int i = 0; i < kPerK; ++i) {
+        const int row = row0 + 32 * (i % 2), slab = i / 2;
+        kr[i] = !known(page) ? zero
+                             : *reinterpret_cast<const uint4 *>(
+                                   p.kc + ((static_cast<long long>(page) * p.kv_heads + hk) *
+                                               kBlockTokens + row) * D + 64 * slab + 16 * quarter);
       }
     };
-    auto load_v = [&](const int (&from)[2], int kt) {
+    auto load_v = [&](int page, int kt) {
 #pragma unroll
-      for (int i = 0; i < 2 * (D / 32); ++i) {
-        const int blk = i / (D / 32), row = row0 + 32 * (i % (D / 32)), page = from[blk];
-        vr[i] = page < 0 ? zero
-                         : *reinterpret_cast<const uint4 *>(
-                               p.vc + ((static_cast<long long>(page) * p.kv_heads + hk) * D + row) *
-                                          kBlockTokens + 16 * quarter);
-      }
+      for (int i = 0; i < kPerV; ++i)
+        vr[i] = !known(page) ? zero
+                             : *reinterpret_cast<const uint4 *>(
+                                   p.vc + ((static_cast<long long>(page) * p.kv_heads + hk) * D +
+                                           row0 + 32 * i) * kBlockTokens + 16 * quarter);
       // values of keys that no row of the CTA sees count as zero, whatever their codes
-      const long long base = (first + kt) * kPrKeys;
-      if (base < key_lo || base + kPrKeys > key_hi) {
+      const long long base = (first + kt) * kBlockTokens;
+      if (base < key_lo || base + kBlockTokens > key_hi) {
+        uint32_t keep[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
 #pragma unroll
-        for (int i = 0; i < 2 * (D / 32); ++i) {
-          const long long key = base + i / (D / 32) * kBlockTokens + 16 * quarter;
-          uint32_t w[4] = {vr[i].x, vr[i].y, vr[i].z, vr[i].w};
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (key + j < key_lo || key + j >= key_hi) w[j / 4] &= ~(0xffu << 8 * (j % 4));
-          vr[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int j = 0; j < 16; ++j) {
+          const long long key = base + 16 * quarter + j;
+          if (key < key_lo || key >= key_hi) keep[j / 4] &= ~(0xffu << 8 * (j % 4));
         }
+#pragma unroll
+        for (int i = 0; i < kPerV; ++i)
+          vr[i] = make_uint4(vr[i].x & keep[0], vr[i].y & keep[1], vr[i].z & keep[2],
+                             vr[i].w & keep[3]);
       }
     };
-    pages(0, pg);
-    pages(1, next);
+    int next = page_of(1);
     if (n > 0) {
-      load_k(pg);
-      load_v(pg, 0);
+      const int page = page_of(0);
+      load_k(page);
+      load_v(page, 0);
     }
     for (int kt = 0; kt < n; ++kt) {
-      const int st = kt & 1, ph = kt >> 1 & 1;
-      if (kt >= 2 && !mbar_wait(smem_u32(k_empty + st), ph ^ 1, p.budget, abort)) {
+      const int st = kt % kPrStages, ph = kt / kPrStages & 1;
+      const int after = page_of(kt + 2);
+      if (kt >= kPrStages && !mbar_wait(smem_u32(k_empty + st), ph ^ 1, p.budget, abort)) {
         *abort = 1;
         break;
       }
       const uint32_t kd = sk + st * S::kK, vd = sv + st * S::kV;
 #pragma unroll
-      for (int i = 0; i < 4 * kSlabs; ++i)
-        store_codes(kd + i / 4 * S::kSlab, row0 + 32 * (i % 4), 2 * quarter, kr[i]);
+      for (int i = 0; i < kPerK; ++i)
+        store_codes(kd + i / 2 * S::kSlab, row0 + 32 * (i % 2), 2 * quarter, kr[i]);
       fence_proxy_async_smem();
       mbar_arrive(smem_u32(k_full + st));
       if (kt + 1 < n) load_k(next);
-      if (kt >= 2 && !mbar_wait(smem_u32(v_empty + st), ph ^ 1, p.budget, abort)) {
+      if (kt >= kPrStages && !mbar_wait(smem_u32(v_empty + st), ph ^ 1, p.budget, abort)) {
         *abort = 1;
         break;
       }
 #pragma unroll
-      for (int i = 0; i < 2 * (D / 32); ++i)
-        store_codes(vd + i / (D / 32) * (D * 128), row0 + 32 * (i % (D / 32)), 2 * quarter, vr[i]);
+      for (int i = 0; i < kPerV; ++i) store_codes(vd, row0 + 32 * i, 2 * quarter, vr[i]);
       fence_proxy_async_smem();
       mbar_arrive(smem_u32(v_full + st));
-      if (kt + 1 < n) {
-        load_v(next, kt + 1);
-        pages(kt + 2, next);
-      }
+      if (kt + 1 < n) load_v(next, kt + 1);
+      next = after;
     }
   } else {
     regs_dec<kPrRestRegs>();
-    if (warp == 12) {
-      constexpr uint32_t kIdS = idesc_f16_f32(128, kPrKeys), kIdO = idesc_f16_f32(128, D);
+    const int t = warp - 12;  // the row tile whose products the warp issues
+    if (t == 0 || (t == 1 && two)) {
+      constexpr uint32_t kIdS = idesc_f16_f32(128, kBlockTokens), kIdO = idesc_f16_f32(128, D);
       bool ok = true;
       auto wait = [&](uint64_t *bar, int parity) {
         const bool landed = mbar_wait(smem_u32(bar), parity, p.budget, abort);
@@ -421,54 +425,81 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
           *abort = 1;
           ok = false;
         }
-        tc_fence_after();
         return ok;
       };
-      auto scores = [&](int t, int kt) {  // S of row tile t over key tile kt
-        const uint32_t a = sw128_desc_lo(sq + t * S::kQ), k = sw128_desc_lo(sk + (kt & 1) * S::kK);
+      auto scores = [&](int kt) {  // S over key tile kt
+        tc_fence_after();
+        const uint32_t k = sw128_desc_lo(sk + kt % kPrStages * S::kK), q = sw128_desc_lo(sq);
+        const uint32_t d = tmem + kColS + t * kBlockTokens, a = tmem + kColQ + t * (D / 2);
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
-          const uint32_t step = s / 4 * (S::kSlab >> 4) + s % 4 * 2;
-          mma_f16_warp_ss(tmem + t * 128, a + step, k + step, kSw128DescHi, kIdS, s > 0 ? 1u : 0u);
+          const uint32_t b = k + s / 4 * (S::kSlab >> 4) + s % 4 * 2;
+          if (D == 64 || t == 0)
+            mma_f16_warp_ts(d, a + 8 * s, b, kSw128DescHi, kIdS, s > 0 ? 1u : 0u);
+          else
+            mma_f16_warp_ss(d, q + s / 4 * (128 * 128 >> 4) + s % 4 * 2, b, kSw128DescHi, kIdS,
+                            s > 0 ? 1u : 0u);
         }
         mma_commit_warp(smem_u32(s_full + t));
+        mma_commit_warp(smem_u32(k_empty + kt % kPrStages));
       };
-      auto values = [&](int t, int kt) {  // O of row tile t += P V
-        const uint32_t v = sw128_desc_lo(sv + (kt & 1) * S::kV);
+      auto values = [&](int kt) {  // O += P V
+        tc_fence_after();
+        const uint32_t v = sw128_desc_lo(sv + kt % kPrStages * S::kV);
 #pragma unroll
-        for (int s = 0; s < kPrKeys / 16; ++s)
-          mma_f16_warp_ts(tmem + 256 + t * D, tmem + t * 128 + 8 * s,
-                          v + s / 4 * (D * 128 >> 4) + s % 4 * 2, kSw128DescHi, kIdO,
-                          kt > 0 || s > 0 ? 1u : 0u);
+        for (int s = 0; s < kBlockTokens / 16; ++s)
+          mma_f16_warp_ts(tmem + t * D, tmem + kColP + t * (kBlockTokens / 2) + 8 * s, v + 2 * s,
+                          kSw128DescHi, kIdO, kt > 0 || s > 0 ? 1u : 0u);
+        mma_commit_warp(smem_u32(p_empty + t));
+        mma_commit_warp(smem_u32(v_empty + kt % kPrStages));
       };
       if (n > 0 && wait(&q_full, 0) && wait(k_full, 0)) {
-        scores(0, 0);
-        if (two) scores(1, 0);
-        mma_commit_warp(smem_u32(k_empty));
-        for (int kt = 0; kt < n && ok; ++kt) {
-          const int st = kt & 1, ph = kt >> 1 & 1;
-          if (!wait(v_full + st, ph) || !wait(p_full, kt & 1)) break;
-          values(0, kt);
+        scores(0);
+        for (int kt = 0; kt < n; ++kt) {
           if (kt + 1 < n) {
-            if (!wait(k_full + (st ^ 1), (kt + 1) >> 1 & 1)) break;
-            scores(0, kt + 1);
+            if (!wait(k_full + (kt + 1) % kPrStages, (kt + 1) / kPrStages & 1) ||
+                !wait(s_empty + t, kt & 1))
+              break;
+            scores(kt + 1);
           }
-          if (two) {
-            if (!wait(p_full + 1, kt & 1)) break;
-            values(1, kt);
-          }
-          mma_commit_warp(smem_u32(v_empty + st));
-          if (kt + 1 < n) {
-            if (two) scores(1, kt + 1);
-            mma_commit_warp(smem_u32(k_empty + (st ^ 1)));
-          }
+          if (!wait(v_full + kt % kPrStages, kt / kPrStages & 1) || !wait(p_full + t, kt & 1)) break;
+          values(kt);
         }
       }
       // after a give-up too: everything issued is done before tensor memory is freed
-      mma_commit_warp(smem_u32(&o_full));
-      if (!mbar_wait(smem_u32(&o_full), 0, 4 * p.budget, &never)) *abort = 1;
+      mma_commit_warp(smem_u32(o_full + t));
+      if (!mbar_wait(smem_u32(o_full + t), 0, 4 * p.budget, &never)) *abort = 1;
       __syncwarp();
       if (*abort && lane == 0 && p.timeout) *p.timeout = 1;
+    } else if (t == 2) {
+      // scales of 32 tiles at a time, a lane each, the next 32 loaded while these are used
+      auto fetch = [&](int i0) {
+        float ks = 1.f, vs = 0.f;  // no page: no weight
+        const int page = page_of(i0 + lane);
+        if (known(page)) {
+          const long long slot = static_cast<long long>(page) * p.kv_heads + hk;
+          ks = p.ks[slot], vs = fmaxf(p.vs[slot], kScaleMin);
+        }
+        return make_float2(ks, vs);
+      };
+      float2 f = fetch(0);
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        const int half = i0 / 32 & 1;
+        const float2 next = fetch(i0 + 32);
+        if (i0 >= 64) {
+          const bool free =
+              mbar_wait(smem_u32(sc_empty + half), (i0 / 64 - 1) & 1, p.budget, abort);
+          if (!__all_sync(0xffffffffu, free)) {
+            *abort = 1;
+            break;
+          }
+        }
+        scales[half][lane] = make_float4(f.x, f.y == 0.f ? -INFINITY : log2f(f.y),
+                                         f.y == 0.f ? 0.f : 1.f / f.y, 0.f);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(sc_full + half));
+        f = next;
+      }
     }
   }
   tc_fence_before();
