@@ -5,8 +5,10 @@
 // one cache block of 64 at a time:
 //   warps 0..3, 4..7   one thread per row of the first / second row tile: softmax of the scores
 //   warps 8..11        convert K and V codes to f16 (exact) in shared memory
-//   warps 12, 13       issue the products of the first / second row tile: S = Q K^T, O += P V
-//   warp 14            fetches the blocks' scales
+//   warps 12, 13       issue the scores' products S = Q K^T of the first / second row tile
+//   warps 14, 15       issue the outputs' products O += P V of the first / second row tile
+// One warp for both products of a row tile was the slowest part: its waits, commits and issues, one
+// after the other, took longer than the products.
 // The softmax threads take a tile's scores into registers and give them free at once, and P has a
 // place of its own, so a row tile's next scores are computed while its softmax is at work: neither
 // waits for the other in turn.  First operands come from tensor memory where it has room for them (at
@@ -20,6 +22,8 @@
 // scores; only where one comes out 2^8 or more too large (weights are kept times 2^7, so 2^15 in f16)
 // are the row's maximum raised, the accumulator rescaled and the tile's weights taken again.
 #pragma once
+#include <type_traits>
+
 #include "lm_attention.cuh"
 
 namespace voc {
@@ -65,9 +69,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
   uint8_t *base_ptr = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sk = smem_u32(base_ptr), sv = sk + kPrStages * S::kK, sq = sv + kPrStages * S::kV;
-  __shared__ __align__(8) uint64_t q_full, k_full[kPrStages], k_empty[kPrStages],
-      v_full[kPrStages], v_empty[kPrStages], s_full[2], s_empty[2], p_full[2], p_empty[2],
-      sc_full[2], sc_empty[2], o_full[2];
+  // [row tile][stage]: s_full -- the scores of a key tile are there and its K stage is free again;
+  // p_empty -- its weights and its V stage are
+  __shared__ __align__(8) uint64_t q_full, k_full[kPrStages], v_full[kPrStages],
+      s_full[2][kPrStages], p_empty[2][kPrStages], s_empty[2], p_full[2], sc_full[2], sc_empty[2],
+      o_full[2], drain[2];
   __shared__ float4 scales[2][32];  // key scale, log2 and reciprocal of the value scale, by tile
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
@@ -87,21 +93,22 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
   const int r_last = min(rows, r0 + kPrRows) - 1;
   const bool two = r_last - r0 >= 128;  // the second row tile has rows
   if (tid == 0) {
-    mbar_init(smem_u32(&q_full), 256);
+    mbar_init(smem_u32(&q_full), 8);  // one arrival per warp, here and below
     for (int i = 0; i < kPrStages; ++i) {
-      mbar_init(smem_u32(k_full + i), 128);
-      mbar_init(smem_u32(v_full + i), 128);
-      mbar_init(smem_u32(k_empty + i), two ? 2 : 1);
-      mbar_init(smem_u32(v_empty + i), two ? 2 : 1);
+      mbar_init(smem_u32(k_full + i), 4);
+      mbar_init(smem_u32(v_full + i), 4);
+      for (int t = 0; t < 2; ++t) {
+        mbar_init(smem_u32(&s_full[t][i]), 1);
+        mbar_init(smem_u32(&p_empty[t][i]), 1);
+      }
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(s_full + i), 1);
-      mbar_init(smem_u32(s_empty + i), 128);
-      mbar_init(smem_u32(p_full + i), 128);
-      mbar_init(smem_u32(p_empty + i), 1);
+      mbar_init(smem_u32(s_empty + i), 4);
+      mbar_init(smem_u32(p_full + i), 4);
       mbar_init(smem_u32(sc_full + i), 1);
       mbar_init(smem_u32(sc_empty + i), two ? 8 : 4);
       mbar_init(smem_u32(o_full + i), 1);
+      mbar_init(smem_u32(drain + i), 1);
     }
     abort_flag = 0;
     fence_barrier_init();
@@ -128,6 +135,17 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
   // page of key tile kt (not yet checked: a use right behind the load would wait for it)
   const int *table = p.table + b * p.ldt + first;
   auto page_of = [&](int kt) { return kt < n ? table[kt] : -1; };
+  // A wait that runs out raises the flag, and everybody goes on without waiting: the loops keep their
+  // shape (their warps stay together) and end, with a result that the caller is told not to use.
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (!mbar_wait(smem_u32(bar), parity, p.budget, abort)) *abort = 1;
+    __syncwarp();
+  };
+  // one arrival for the warp: 32 of them on one barrier would queue up in shared memory
+  auto arrive = [&](uint64_t *bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(bar));
+  };
   auto known = [&](int page) { return page >= 0 && page < p.n_pages; };
 
   if (wg < 2) {
@@ -192,29 +210,29 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
       }
     }
     tc_fence_before();
-    mbar_arrive(smem_u32(&q_full));
+    arrive(&q_full);
 
     const uint32_t lane_base = static_cast<uint32_t>((warp % 4) * 32) << 16;
     const uint32_t s_addr = tmem + lane_base + kColS + wg * kBlockTokens;
     const uint32_t p_addr = tmem + lane_base + kColP + wg * (kBlockTokens / 2);
     const uint32_t o_addr = tmem + lane_base + wg * D;
     float m = -INFINITY, l = 0.f;
-    bool ok = true;
     if (wg == 0 || two) {
-      auto wait = [&](uint64_t *bar, int parity) {
-        const bool got = mbar_wait(smem_u32(bar), parity, p.budget, abort);
-        if (!__all_sync(0xffffffffu, got)) {
-          *abort = 1;
-          ok = false;
-        }
-        return ok;
-      };
+      // key tiles that every row of the warp sees whole: [whole0, whole1)
+      const int whole0 = __reduce_max_sync(
+          0xffffffffu, static_cast<int>(min(static_cast<long long>(n),
+                                            max(0ll, (see.lo + kBlockTokens - 1) / kBlockTokens - first))));
+      const int whole1 = __reduce_min_sync(
+          0xffffffffu, static_cast<int>(min(static_cast<long long>(n),
+                                            max(0ll, see.hi / kBlockTokens - first))));
       for (int kt = 0; kt < n; ++kt) {
-        if (kt % 32 == 0 && !wait(sc_full + (kt / 32 & 1), kt / 64 & 1)) break;
-        const float4 block = scales[kt / 32 & 1][kt % 32];
+        const uint32_t st = static_cast<uint32_t>(kt) % kPrStages;
+        const uint32_t ph = static_cast<uint32_t>(kt) / kPrStages & 1;
+        if (kt % 32 == 0) wait(sc_full + (kt >> 5 & 1), kt >> 6 & 1);
+        const float4 block = scales[kt >> 5 & 1][kt & 31];
         const float c = fmaxf(qc * block.x, 1e-37f);  // above 0: masked scores stay -inf
         const float lvs = block.y, ivs = block.z;
-        if (!wait(s_full + wg, kt & 1)) break;
+        wait(&s_full[wg][st], ph);
         tc_fence_after();
         uint32_t sc[kBlockTokens];
         tmem_ld32_issue(s_addr, sc);
@@ -223,10 +241,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
         tmem_ld32_after_wait(sc);
         tmem_ld32_after_wait(sc + 32);
         tc_fence_before();
-        mbar_arrive(smem_u32(s_empty + wg));
-        // the row's keys of this tile, where it does not see them all
-        const long long base = (first + kt) * kBlockTokens;
-        if (__any_sync(0xffffffffu, base < see.lo || base + kBlockTokens > see.hi)) {
+        arrive(s_empty + wg);
+        if (kt < whole0 || kt >= whole1) {  // the row's keys of this tile
+          const long long base = (first + kt) * kBlockTokens;
           const int from = static_cast<int>(max(-1ll, min(see.lo - base, 64ll)));
           const int upto = static_cast<int>(max(-1ll, min(see.hi - base, 64ll)));
 #pragma unroll
@@ -234,21 +251,20 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
             if (i < from || i >= upto) sc[i] = 0xff800000u;
         }
         uint32_t w[kBlockTokens / 2];
-        bool raise = __any_sync(0xffffffffu, m == -INFINITY);
+        bool raise = kt == 0, mine = raise;  // for some row of the warp, for this row
         while (true) {
           if (raise) {  // a look at the maximum, and the row's weights taken against it from here on
             float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int i = 0; i < kBlockTokens; ++i) t[i % 4] = fmaxf(t[i % 4], __uint_as_float(sc[i]));
-            const float nm = fmaf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), c, lvs);
-            float alpha = 1.f;
-            if (nm > m + kLazy || (m == -INFINITY && nm > m)) {
-              alpha = ex2(m - nm);
-              m = nm;
-            }
+            // (a row that did not ask for it stays as it is, whoever its neighbours are)
+            const float nm =
+                mine ? fmaxf(m, fmaf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), c, lvs)) : m;
+            const float alpha = nm == m ? 1.f : ex2(m - nm);
+            m = nm;
             l *= alpha;
             if (kt > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-              if (!wait(p_empty + wg, (kt - 1) & 1)) break;  // O is at rest
+              wait(&p_empty[wg][(kt - 1) % kPrStages], (kt - 1) / kPrStages & 1);  // O is at rest
               tc_fence_after();
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
@@ -263,7 +279,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
           }
           const float d = lvs - ((m == -INFINITY ? 0.f : m) - kPShift);
           const float2 cc = make_float2(c, c), dd = make_float2(d, d);
-          uint32_t big = 0;
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int i = 0; i < kBlockTokens / 2; ++i) {
@@ -272,26 +287,26 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
             u.x = ex2(u.x), u.y = ex2(u.y);
             sum[i % 2] = add2(sum[i % 2], u);
             w[i] = f16x2(u.x, u.y);
-            big = __vmaxu2(big, w[i]);
           }
-          // weights are positive, so their bits order them: 2^15 and above (NaN too) is too far ahead
-          const bool far = (big & 0xffffu) >= 0x7800u || (big >> 16) >= 0x7800u;
-          if (raise || !__any_sync(0xffffffffu, far)) {
-            l = fmaf((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y), ivs, l);
-            break;
+          // the weights' sum bounds them: below 2^15 (and not NaN) all fit in f16; a row that has
+          // seen no key yet needs its first maximum
+          const float all = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          if (!raise) {
+            mine = !(all < 32768.f) || m == -INFINITY;
+            raise = __any_sync(0xffffffffu, mine);
+            if (raise) continue;
           }
-          raise = true;
+          l = fmaf(all, ivs, l);
+          break;
         }
-        if (kt > 0 && !wait(p_empty + wg, (kt - 1) & 1)) break;  // the last weights are used up
+        // the last weights are used up
+        if (kt > 0) wait(&p_empty[wg][(kt - 1) % kPrStages], (kt - 1) / kPrStages & 1);
         tc_fence_after();
         tmem_st32(p_addr, w);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(smem_u32(p_full + wg));
-        if (kt % 32 == 31) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(sc_empty + (kt / 32 & 1)));
-        }
+        arrive(p_full + wg);
+        if (kt % 32 == 31) arrive(sc_empty + (kt >> 5 & 1));
       }
     }
     // outputs
@@ -382,6 +397,34 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
                              vr[i].w & keep[3]);
       }
     };
+    // the stage of key tile kt is free when both row tiles are done with its last use
+    auto freed = [&](uint64_t (*bars)[kPrStages], int kt) {
+      const uint32_t st = static_cast<uint32_t>(kt) % kPrStages;
+      const uint32_t ph = (static_cast<uint32_t>(kt) / kPrStages & 1) ^ 1;
+      if (kt < kPrStages) return;
+      wait(&bars[0][st], ph);
+      if (two) wait(&bars[1][st], ph);
+    };
+    // warp 8 hands the softmax threads the scales of 32 key tiles at a time, a lane each, and loads
+    // the next 32 then
+    float ks = 1.f, vs = 0.f;
+    auto fetch_scales = [&](int i0) {  // no page: no weight
+      ks = 1.f, vs = 0.f;
+      const int page = page_of(i0 + lane);
+      if (known(page)) {
+        const long long slot = static_cast<long long>(page) * p.kv_heads + hk;
+        ks = p.ks[slot], vs = fmaxf(p.vs[slot], kScaleMin);
+      }
+    };
+    auto put_scales = [&](int i0) {
+      const int half = i0 / 32 & 1;
+      if (i0 >= 64) wait(sc_empty + half, (i0 / 64 - 1) & 1);
+      scales[half][lane] =
+          make_float4(ks, vs == 0.f ? -INFINITY : log2f(vs), vs == 0.f ? 0.f : 1.f / vs, 0.f);
+      arrive(sc_full + half);
+      fetch_scales(i0 + 32);
+    };
+    if (warp == 8) fetch_scales(0);
     int next = page_of(1);
     if (n > 0) {
       const int page = page_of(0);
@@ -389,118 +432,81 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
       load_v(page, 0);
     }
     for (int kt = 0; kt < n; ++kt) {
-      const int st = kt % kPrStages, ph = kt / kPrStages & 1;
+      const uint32_t st = static_cast<uint32_t>(kt) % kPrStages;
       const int after = page_of(kt + 2);
-      if (kt >= kPrStages && !mbar_wait(smem_u32(k_empty + st), ph ^ 1, p.budget, abort)) {
-        *abort = 1;
-        break;
-      }
+      if (warp == 8 && kt % 32 == 0) put_scales(kt);
+      freed(s_full, kt);
       const uint32_t kd = sk + st * S::kK, vd = sv + st * S::kV;
 #pragma unroll
       for (int i = 0; i < kPerK; ++i)
         store_codes(kd + i / 2 * S::kSlab, row0 + 32 * (i % 2), 2 * quarter, kr[i]);
       fence_proxy_async_smem();
-      mbar_arrive(smem_u32(k_full + st));
+      arrive(k_full + st);
       if (kt + 1 < n) load_k(next);
-      if (kt >= kPrStages && !mbar_wait(smem_u32(v_empty + st), ph ^ 1, p.budget, abort)) {
-        *abort = 1;
-        break;
-      }
+      freed(p_empty, kt);
 #pragma unroll
       for (int i = 0; i < kPerV; ++i) store_codes(vd, row0 + 32 * i, 2 * quarter, vr[i]);
       fence_proxy_async_smem();
-      mbar_arrive(smem_u32(v_full + st));
+      arrive(v_full + st);
       if (kt + 1 < n) load_v(next, kt + 1);
       next = after;
     }
   } else {
     regs_dec<kPrRestRegs>();
-    const int t = warp - 12;  // the row tile whose products the warp issues
-    if (t == 0 || (t == 1 && two)) {
+    // The row tile is a compile-time number here: operands that the compiler does not see to be the
+    // same for the warp are moved into place for every MMA, which then waits for that (measured: 8 MMAs
+    // of 32 cycles each took 1400 to issue with the tile taken from the warp's number).
+    auto issue = [&](auto tile, auto what) {
+      constexpr int t = decltype(tile)::value, kind = decltype(what)::value;
       constexpr uint32_t kIdS = idesc_f16_f32(128, kBlockTokens), kIdO = idesc_f16_f32(128, D);
-      bool ok = true;
-      auto wait = [&](uint64_t *bar, int parity) {
-        const bool landed = mbar_wait(smem_u32(bar), parity, p.budget, abort);
-        if (!__all_sync(0xffffffffu, landed)) {
-          *abort = 1;
-          ok = false;
-        }
-        return ok;
-      };
-      auto scores = [&](int kt) {  // S over key tile kt
-        tc_fence_after();
-        const uint32_t k = sw128_desc_lo(sk + kt % kPrStages * S::kK), q = sw128_desc_lo(sq);
-        const uint32_t d = tmem + kColS + t * kBlockTokens, a = tmem + kColQ + t * (D / 2);
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          const uint32_t b = k + s / 4 * (S::kSlab >> 4) + s % 4 * 2;
-          if (D == 64 || t == 0)
-            mma_f16_warp_ts(d, a + 8 * s, b, kSw128DescHi, kIdS, s > 0 ? 1u : 0u);
-          else
-            mma_f16_warp_ss(d, q + s / 4 * (128 * 128 >> 4) + s % 4 * 2, b, kSw128DescHi, kIdS,
-                            s > 0 ? 1u : 0u);
-        }
-        mma_commit_warp(smem_u32(s_full + t));
-        mma_commit_warp(smem_u32(k_empty + kt % kPrStages));
-      };
-      auto values = [&](int kt) {  // O += P V
-        tc_fence_after();
-        const uint32_t v = sw128_desc_lo(sv + kt % kPrStages * S::kV);
-#pragma unroll
-        for (int s = 0; s < kBlockTokens / 16; ++s)
-          mma_f16_warp_ts(tmem + t * D, tmem + kColP + t * (kBlockTokens / 2) + 8 * s, v + 2 * s,
-                          kSw128DescHi, kIdO, kt > 0 || s > 0 ? 1u : 0u);
-        mma_commit_warp(smem_u32(p_empty + t));
-        mma_commit_warp(smem_u32(v_empty + kt % kPrStages));
-      };
-      if (n > 0 && wait(&q_full, 0) && wait(k_full, 0)) {
-        scores(0);
+      if (kind == 0) {  // S over one key tile after the other
+        const uint32_t q = sw128_desc_lo(sq), d = tmem + kColS + t * kBlockTokens;
+        const uint32_t a = tmem + kColQ + t * (D / 2);
+        if (n > 0) wait(&q_full, 0);
         for (int kt = 0; kt < n; ++kt) {
-          if (kt + 1 < n) {
-            if (!wait(k_full + (kt + 1) % kPrStages, (kt + 1) / kPrStages & 1) ||
-                !wait(s_empty + t, kt & 1))
-              break;
-            scores(kt + 1);
+          const uint32_t st = static_cast<uint32_t>(kt) % kPrStages;
+          wait(k_full + st, static_cast<uint32_t>(kt) / kPrStages & 1);
+          if (kt > 0) wait(s_empty + t, (kt - 1) & 1);
+          tc_fence_after();
+          const uint32_t k = sw128_desc_lo(sk + st * S::kK);
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            const uint32_t b = k + s / 4 * (S::kSlab >> 4) + s % 4 * 2;
+            if constexpr (D == 64 || t == 0)
+              mma_f16_warp_ts(d, a + 8 * s, b, kSw128DescHi, kIdS, s > 0 ? 1u : 0u);
+            else
+              mma_f16_warp_ss(d, q + s / 4 * (128 * 128 >> 4) + s % 4 * 2, b, kSw128DescHi, kIdS,
+                              s > 0 ? 1u : 0u);
           }
-          if (!wait(v_full + kt % kPrStages, kt / kPrStages & 1) || !wait(p_full + t, kt & 1)) break;
-          values(kt);
+          mma_commit_warp(smem_u32(&s_full[t][st]));
+        }
+      } else {  // O += P V
+        for (int kt = 0; kt < n; ++kt) {
+          const uint32_t st = static_cast<uint32_t>(kt) % kPrStages;
+          wait(v_full + st, static_cast<uint32_t>(kt) / kPrStages & 1);
+          wait(p_full + t, kt & 1);
+          tc_fence_after();
+          const uint32_t v = sw128_desc_lo(sv + st * S::kV);
+#pragma unroll
+          for (int s = 0; s < kBlockTokens / 16; ++s)
+            mma_f16_warp_ts(tmem + t * D, tmem + kColP + t * (kBlockTokens / 2) + 8 * s, v + 2 * s,
+                            kSw128DescHi, kIdO, kt > 0 || s > 0 ? 1u : 0u);
+          mma_commit_warp(smem_u32(&p_empty[t][st]));
         }
       }
       // after a give-up too: everything issued is done before tensor memory is freed
-      mma_commit_warp(smem_u32(o_full + t));
-      if (!mbar_wait(smem_u32(o_full + t), 0, 4 * p.budget, &never)) *abort = 1;
+      uint64_t *end = kind == 0 ? drain + t : o_full + t;
+      mma_commit_warp(smem_u32(end));
+      if (!mbar_wait(smem_u32(end), 0, 4 * p.budget, &never)) *abort = 1;
       __syncwarp();
       if (*abort && lane == 0 && p.timeout) *p.timeout = 1;
-    } else if (t == 2) {
-      // scales of 32 tiles at a time, a lane each, the next 32 loaded while these are used
-      auto fetch = [&](int i0) {
-        float ks = 1.f, vs = 0.f;  // no page: no weight
-        const int page = page_of(i0 + lane);
-        if (known(page)) {
-          const long long slot = static_cast<long long>(page) * p.kv_heads + hk;
-          ks = p.ks[slot], vs = fmaxf(p.vs[slot], kScaleMin);
-        }
-        return make_float2(ks, vs);
-      };
-      float2 f = fetch(0);
-      for (int i0 = 0; i0 < n; i0 += 32) {
-        const int half = i0 / 32 & 1;
-        const float2 next = fetch(i0 + 32);
-        if (i0 >= 64) {
-          const bool free =
-              mbar_wait(smem_u32(sc_empty + half), (i0 / 64 - 1) & 1, p.budget, abort);
-          if (!__all_sync(0xffffffffu, free)) {
-            *abort = 1;
-            break;
-          }
-        }
-        scales[half][lane] = make_float4(f.x, f.y == 0.f ? -INFINITY : log2f(f.y),
-                                         f.y == 0.f ? 0.f : 1.f / f.y, 0.f);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(sc_full + half));
-        f = next;
-      }
-    }
+    };
+    using Zero = std::integral_constant<int, 0>;
+    using One = std::integral_constant<int, 1>;
+    if (warp == 12) issue(Zero(), Zero());
+    if (warp == 13 && two) issue(One(), Zero());
+    if (warp == 14) issue(Zero(), One());
+    if (warp == 15 && two) issue(One(), One());
   }
   tc_fence_before();
   __syncthreads();
