@@ -363,9 +363,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
     regs_dec<kPrConvRegs>();
     const int ct = tid - 256, quarter = ct % 4, row0 = ct / 4;
     constexpr int kPerK = 2 * (D / 64), kPerV = D / 32;  // 16-code pieces of a thread
-    uint4 kr[kPerK], vr[kPerV];
+    uint4 kr[2][kPerK], vr[2][kPerV];  // codes of two key tiles under way
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    auto load_k = [&](int page) {
+    auto load_k = [&](uint4 (&kr)[kPerK], int page) {
 #pragma unroll
       for (int i = 0; i < kPerK; ++i) {
         const int row = row0 + 32 * (i % 2), slab = i / 2;
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
                                                kBlockTokens + row) * D + 64 * slab + 16 * quarter);
       }
     };
-    auto load_v = [&](int page, int kt) {
+    auto load_v = [&](uint4 (&vr)[kPerV], int page, int kt) {
 #pragma unroll
       for (int i = 0; i < kPerV; ++i)
         vr[i] = !known(page) ? zero
@@ -425,31 +425,39 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
       fetch_scales(i0 + 32);
     };
     if (warp == 8) fetch_scales(0);
-    int next = page_of(1);
+    int pages[2] = {page_of(2), page_of(3)};  // of the tiles to load next
     if (n > 0) {
-      const int page = page_of(0);
-      load_k(page);
-      load_v(page, 0);
+      const int page0 = page_of(0), page1 = page_of(1);
+      load_k(kr[0], page0);
+      load_v(vr[0], page0, 0);
+      if (n > 1) load_k(kr[1], page1);
+      if (n > 1) load_v(vr[1], page1, 1);
     }
-    for (int kt = 0; kt < n; ++kt) {
+    // A tile's loads are issued two tiles ahead: one tile is not enough to cover them.
+    auto step = [&](int kt, auto which) {
+      constexpr int w = decltype(which)::value;
       const uint32_t st = static_cast<uint32_t>(kt) % kPrStages;
-      const int after = page_of(kt + 2);
+      const int page = pages[w];
+      pages[w] = page_of(kt + 4);
       if (warp == 8 && kt % 32 == 0) put_scales(kt);
       freed(s_full, kt);
       const uint32_t kd = sk + st * S::kK, vd = sv + st * S::kV;
 #pragma unroll
       for (int i = 0; i < kPerK; ++i)
-        store_codes(kd + i / 2 * S::kSlab, row0 + 32 * (i % 2), 2 * quarter, kr[i]);
+        store_codes(kd + i / 2 * S::kSlab, row0 + 32 * (i % 2), 2 * quarter, kr[w][i]);
       fence_proxy_async_smem();
       arrive(k_full + st);
-      if (kt + 1 < n) load_k(next);
+      if (kt + 2 < n) load_k(kr[w], page);
       freed(p_empty, kt);
 #pragma unroll
-      for (int i = 0; i < kPerV; ++i) store_codes(vd, row0 + 32 * i, 2 * quarter, vr[i]);
+      for (int i = 0; i < kPerV; ++i) store_codes(vd, row0 + 32 * i, 2 * quarter, vr[w][i]);
       fence_proxy_async_smem();
       arrive(v_full + st);
-      if (kt + 1 < n) load_v(next, kt + 1);
-      next = after;
+      if (kt + 2 < n) load_v(vr[w], page, kt + 2);
+    };
+    for (int kt = 0; kt < n; kt += 2) {
+      step(kt, std::integral_constant<int, 0>());
+      if (kt + 1 < n) step(kt + 1, std::integral_constant<int, 1>());
     }
   } else {
     regs_dec<kPrRestRegs>();
