@@ -439,8 +439,10 @@ voc_status check_cache(const void *kc, const void *vc, const float *ks, const fl
 
 template <typename T, int D>
 cudaError_t launch_append(dim3 grid, const voc::LmAppendArgs &a, voc_stream_t stream) {
-  return launch(voc::append_kernel<T, D>, grid, dim3(voc::AppendShape<D>::kThreads), 0, 1, stream,
-                a);
+  const dim3 block(voc::AppendShape<D>::kThreads);
+  if (a.max_q < voc::kBlockTokens)
+    return launch(voc::append_kernel<T, D, true>, grid, block, 0, 1, stream, a);
+  return launch(voc::append_kernel<T, D, false>, grid, block, 0, 1, stream, a);
 }
 
 }  // namespace
@@ -467,8 +469,16 @@ VOC_API voc_status vocoder_lm_kv_append(void *k_cache, void *v_cache, float *k_s
   if (n_tokens == 0 || max_q == 0) return finish(*dev, stream, flags);
   voc::LmAppendArgs a{static_cast<uint8_t *>(k_cache), static_cast<uint8_t *>(v_cache), k_scale,
                       v_scale, k, v, ldk, hsk, ldv, hsv, page_table, kv_lens, cu_q, ldt, n_pages,
-                      table_cols, kv_heads, n_seq, n_tokens, max_q};
-  const dim3 grid((max_q - 1 + voc::kBlockTokens - 1) / voc::kBlockTokens + 1, kv_heads, n_seq);
+                      table_cols, kv_heads, n_seq, n_tokens, max_q, 0};
+  // Blocks that max_q tokens can touch, for every sequence, or (prompts of different lengths) all that
+  // n_tokens can touch.
+  const long long each = (max_q - 1 + voc::kBlockTokens - 1) / voc::kBlockTokens + 1ll;
+  const long long all = n_tokens / voc::kBlockTokens + 2ll * n_seq;
+  dim3 grid(static_cast<unsigned>(max_q == 1 ? 1 : each), kv_heads, n_seq);
+  if (max_q > 1 && n_seq <= voc::kFlatSeqs && all < each * n_seq) {
+    a.flat = 1;
+    grid = dim3(static_cast<unsigned>(all), kv_heads, 1);
+  }
   cudaError_t e;
   if (dtype == VOC_LM_F16)
     e = head_dim == 64 ? launch_append<__half, 64>(grid, a, stream)
