@@ -561,3 +561,69 @@ def test_operators_on_a_stream_of_their_own():
     side.synchronize()
     for o in out:
         assert torch.equal(o, ref)
+
+
+# ------------------------------------------------------------------ the binding's two ways
+def test_compiled_and_python_marshalling_agree(monkeypatch):
+    """The compiled binding and the Python one make the same calls, with defaults and with every
+    operand given; both refuse wrong tensors with VOC_INVALID_ARG."""
+    V._lm_setup()
+    if V._LM.fast is None:
+        pytest.skip("lm_torch.so is not built")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x, r = (torch.randn(5, 96, generator=g, device="cuda").bfloat16() for _ in range(2))
+    w8, ws = _codes(g, 70, 96), torch.rand(70, generator=g, device="cuda")
+    bias = torch.randn(70, generator=g, device="cuda")
+    nw = torch.rand(96, generator=g, device="cuda").bfloat16()
+
+    def calls():
+        bt = Batch([70, 300, 64], [6, 1, 64], 2, 64, seed=1, filled=False)
+        single = Batch([900, 5], [1, 1], 2, 64, seed=2)
+        k, v = (torch.from_numpy(bt.rng.standard_normal((bt.total, 2, 64))).cuda().bfloat16()
+                for _ in range(2))
+        out = [*V.rows_fp8(x, weight=nw, residual=r),
+               *V.rows_fp8(x, V.VOC_LM_NONE, scale=torch.empty(5, device="cuda"),
+                           out=torch.empty(5, 96, device="cuda").to(F8))[:2],
+               *V.rows_fp8(x[:, :70], V.VOC_LM_GATED)[:2]]
+        for kw in (dict(), dict(bias=bias, out_dtype=torch.float32),
+                   dict(out=torch.empty(5, 75, device="cuda").half()[:, :70])):
+            out.append(V.linear_fp8(out[0], out[1], w8, ws, **kw))
+        V.kv_append_fp8(bt.cache, k, v, **bt.args())
+        q, q1 = _queries(bt, 4), _queries(single, 6, "f16")
+        out += [bt.cache.k, bt.cache.v, bt.cache.k_scale, bt.cache.v_scale,
+                V.attention_fp8(q, bt.cache, **bt.args()),
+                V.attention_fp8(q, bt.cache, window=20, causal=False, softmax_scale=0.3,
+                                out=torch.empty_like(q), max_kv=300, **bt.args()),
+                V.attention_fp8(q1, single.cache, **single.args()),
+                V.attention_fp8(q1, single.cache, max_kv=900, ws=torch.empty(
+                    1 << 20, dtype=torch.uint8, device="cuda"), **single.args())]
+        torch.cuda.synchronize()
+        for bad in (lambda: V.rows_fp8(x.double()), lambda: V.rows_fp8(x, weight=nw[:9]),
+                    lambda: V.rows_fp8(x.T), lambda: V.rows_fp8(x, weight=nw.float()),
+                    lambda: V.rows_fp8(x, V.VOC_LM_NONE, sum_out=x),
+                    lambda: V.rows_fp8(x), lambda: V.rows_fp8(x.cpu(), V.VOC_LM_NONE),
+                    lambda: V.linear_fp8(out[0], out[1][:3], w8, ws),
+                    lambda: V.linear_fp8(out[0], out[1], w8[:, :90], ws),
+                    lambda: V.linear_fp8(out[0], out[1], w8, ws, out_dtype=torch.int32),
+                    lambda: V.linear_fp8(out[0][:, 3:], out[1], w8[:, 3:], ws),
+                    lambda: V.KVCacheFP8(bt.cache.k, bt.cache.k, bt.cache.k_scale, bt.cache.v_scale)
+                    if bt.cache.k.shape != bt.cache.v.shape else V.rows_fp8(x),
+                    lambda: V.kv_append_fp8(bt.cache, k, v.half(), **bt.args()),
+                    lambda: V.kv_append_fp8(bt.cache, k, v, bt.t_table.long(), bt.t_lens),
+                    lambda: V.kv_append_fp8(bt.cache, k, v, bt.t_table, bt.t_lens, max_q=1),
+                    lambda: V.attention_fp8(q[:, :3], bt.cache, **bt.args()),
+                    lambda: V.attention_fp8(q, bt.cache, window=-1, **bt.args()),
+                    lambda: V.attention_fp8(q, bt.cache, out=q[:, :2], **bt.args())):
+            with pytest.raises(V.VocoderError) as e:
+                bad()
+            assert e.value.status == V.VOC_INVALID_ARG
+        return out
+
+    fast = calls()
+    monkeypatch.setattr(V._LM, "fast", None)
+    slow = calls()
+    assert len(fast) == len(slow)
+    for a, b in zip(fast, slow):
+        assert (a is None and b is None) or (
+            a.dtype == b.dtype and a.shape == b.shape and a.stride() == b.stride() and
+            torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8)))
