@@ -48,13 +48,16 @@ L2_FLUSH_BYTES = 256 << 20
 
 
 def source_hash() -> str:
-    """Hash of the CUDA sources and the C header: identifies the kernels a profile was taken on."""
+    """Hash of the decoder's CUDA sources and the C header (not of the 8-bit operators' lm_* files):
+    identifies the kernels a profile was taken on."""
     import glob
     import hashlib
     h = hashlib.sha1()
     files = sorted(glob.glob(os.path.join(ROOT, "dac_vocoder_decode_gb300", "csrc", "*.cu*")) +
                    glob.glob(os.path.join(ROOT, "include", "*.h")))
     for f in files:
+        if os.path.basename(f).startswith("lm_"):
+            continue
         h.update(os.path.basename(f).encode())
         with open(f, "rb") as fh:
             h.update(fh.read())
