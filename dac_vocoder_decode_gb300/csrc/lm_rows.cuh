@@ -244,9 +244,13 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LmRowsArgs p, c
       float u[N];
       Vec::unpack(a[i], h[i]);
       Vec::unpack(b[i], u);
+      if (MODE != kRowsGated) {
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        h[i][j] = MODE == kRowsGated ? silu_mul(h[i][j], u[j]) : h[i][j] + u[j];
+        for (int j = 0; j < N; ++j) h[i][j] += u[j];
+      } else if (lane + i * tpr < chunks) {  // nothing for the places beyond the row (their h is 0)
+#pragma unroll
+        for (int j = 0; j < N; ++j) h[i][j] = silu_mul(h[i][j], u[j]);
+      }
     }
     if (MODE != kRowsGated && p.sum) {
       T *s = static_cast<T *>(p.sum) + row * p.lds;
