@@ -82,10 +82,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
   const int never = 0;
 
   const int b = blockIdx.z / p.splits, split = blockIdx.z % p.splits, hk = blockIdx.y;
+  pdl_wait();
   const SeqSpan span = seq_span(p.cu, b, p.n_seq, p.n_tokens, p.max_q);
   const int rows = span.count * p.group;
-  pdl_wait();
-  pdl_launch_dependents();
   // the latest rows see the most keys: they start first
   const int tile_max = static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x);
   const int r0 = tile_max * kPrRows;
@@ -120,6 +119,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // Only now: a later kernel's CTA that came before this allocation and took columns on this SM would
+  // wait for this grid while this grid waited for its columns.
+  pdl_launch_dependents();
   const uint32_t tmem = tmem_slot;  // columns: two outputs, two scores, two weights, queries
   constexpr uint32_t kColS = 2 * D, kColP = kColS + 2 * kBlockTokens, kColQ = kColP + kBlockTokens;
   const long long len = max(0ll, min(static_cast<long long>(p.lens[b]),
