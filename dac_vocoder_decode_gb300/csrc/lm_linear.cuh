@@ -362,6 +362,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t empty0 = mapa_shared(smem_u32(acc_empty), 0u);
     const uint32_t stage = smem_u32(ring) + kManyStages * kManyStage + warp * (32 * 64);
     int k = 0;
+    bool ok = true;  // after a give-up the warps go on without work: all meet at every barrier
     for (long long job = job0; job < jobs; job += step, ++k) {
       const int acc = k & 1;
       const int row0 = static_cast<int>(job / n_tiles) * kManyTile + 128 * static_cast<int>(rank) +
@@ -374,10 +375,12 @@ __global__ void __launch_bounds__(kManyThreads, 1) __cluster_dims__(2, 1, 1)
       }
       const float xs = row0 + lane < p.M ? p.xs[row0 + lane] : 0.f;
       asm volatile("bar.sync 1, 256;" ::: "memory");  // the epilogue warps
-      const bool got = mbar_wait_cluster(smem_u32(acc_full + acc), (k / 2) & 1, 4 * p.budget, abort);
+      const bool got =
+          ok && mbar_wait_cluster(smem_u32(acc_full + acc), (k / 2) & 1, 4 * p.budget, abort);
       if (!__all_sync(0xffffffffu, got)) {
-        if (lane == 0) raise();
-        break;
+        if (ok && lane == 0) raise();
+        ok = false;
+        continue;
       }
       tc_fence_after();
       const int c_end = min(cols, c_first + kManyTile / 2);
