@@ -1,5 +1,5 @@
 // lm_common.cuh -- pieces shared by the 8-bit operators of a token model (lm_*.cuh): element
-// types, e4m3 conversions, reductions.
+// types and e4m3 conversions.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -37,21 +37,9 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
 }
 
-// 16 bytes of T <-> floats.
+// 16 bytes of a 16-bit type <-> floats.
 template <typename T>
 struct Vec16;
-template <>
-struct Vec16<float> {
-  static constexpr int N = 4;
-  static __device__ __forceinline__ void unpack(const uint4 &u, float (&f)[4]) {
-    f[0] = __uint_as_float(u.x), f[1] = __uint_as_float(u.y);
-    f[2] = __uint_as_float(u.z), f[3] = __uint_as_float(u.w);
-  }
-  static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                      __float_as_uint(f[3]));
-  }
-};
 template <>
 struct Vec16<__half> {
   static constexpr int N = 8;
@@ -166,38 +154,6 @@ __device__ __forceinline__ float max_abs(float m, float v) {
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float pow2(int e) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-}
-
-// Over the threads of a group of TPR (a power of two) consecutive threads: the sum in a fixed
-// order.  Groups larger than a warp go through `red` (32 floats per group).
-template <int TPR>
-__device__ __forceinline__ float group_sum(float v, float *red) {
-#pragma unroll
-  for (int o = (TPR < 32 ? TPR : 32) / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (TPR > 32) {
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
-    __syncthreads();
-    const int base = threadIdx.x / TPR * (TPR / 32);
-    v = 0.f;
-    for (int i = 0; i < TPR / 32; ++i) v += red[base + i];
-  }
-  return v;
-}
-template <int TPR>
-__device__ __forceinline__ uint32_t group_max(uint32_t v, float *red) {
-#pragma unroll
-  for (int o = (TPR < 32 ? TPR : 32) / 2; o; o >>= 1)
-    v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
-  if (TPR > 32) {
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = __uint_as_float(v);
-    __syncthreads();
-    const int base = threadIdx.x / TPR * (TPR / 32);
-    v = 0;
-    for (int i = 0; i < TPR / 32; ++i) v = max(v, __float_as_uint(red[base + i]));
-  }
-  return v;
 }
 
 }  // namespace voc

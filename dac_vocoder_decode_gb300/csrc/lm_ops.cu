@@ -215,8 +215,8 @@ cudaError_t launch_rows_vec(int sms, const voc::LmRowsArgs &a, voc_stream_t stre
 template <typename T, int MODE>
 cudaError_t launch_rows(int sms, const voc::LmRowsArgs &a, voc_stream_t stream) {
   if (a.d > voc::kRowThreads * voc::kRowValues)
-    return launch(voc::rows_any_kernel<T, MODE>, dim3(static_cast<unsigned>(a.rows)), dim3(256), 0,
-                  1, stream, a);
+    return launch(voc::rows_any_kernel<T, MODE>, dim3(static_cast<unsigned>(a.rows)),
+                  dim3(voc::kAnyThreads), 0, 1, stream, a);
   const size_t e = sizeof(T);
   auto fits = [&](size_t vb) {  // rows start on vb bytes, codes on as many values
     const long long n = static_cast<long long>(vb / e);
@@ -226,11 +226,9 @@ cudaError_t launch_rows(int sms, const voc::LmRowsArgs &a, voc_stream_t stream) 
   };
   if (fits(16)) return launch_rows_vec<T, MODE, 16>(sms, a, stream);
   if (fits(8)) return launch_rows_vec<T, MODE, 8>(sms, a, stream);
-  if (fits(4)) return launch_rows_vec<T, MODE, 4>(sms, a, stream);
   if constexpr (sizeof(T) == 2)
-    return launch_rows_vec<T, MODE, 2>(sms, a, stream);
-  else
-    return cudaErrorInvalidValue;  // not reached: every f32 buffer is aligned to 4
+    if (!fits(4)) return launch_rows_vec<T, MODE, 2>(sms, a, stream);
+  return launch_rows_vec<T, MODE, 4>(sms, a, stream);
 }
 
 template <int MODE>
@@ -380,9 +378,8 @@ VOC_API voc_status vocoder_lm_linear_fp8(const void *x8, long long ldx, const fl
     if (e != cudaSuccess) return cuda_fail(e, "launch linear");
     return finish(*dev, stream, flags);
   }
-  const int m_tiles = (M + 255) / 256;
+  const int m_tiles = (M + 255) / 256;  // (few: fewer than 32 of 256 x 256)
   a.nt = ((M + m_tiles - 1) / m_tiles + 15) / 16 * 16;  // equal tiles of up to 256 tokens
-  if ((M + a.nt - 1) / a.nt > 65535) return fail(VOC_UNSUPPORTED, "linear: too many rows");
   a.tmem_cols = 32;
   while (a.tmem_cols < a.nt) a.tmem_cols *= 2;
   // Up to 64 tokens leave room for two CTAs on an SM.  K is split over up to 8 CTAs as long as all
@@ -592,6 +589,8 @@ VOC_API voc_status vocoder_lm_attention(
   if (!known_flags(flags)) return fail(VOC_INVALID_ARG, "attention: flags");
   if (heads < kv_heads || heads % kv_heads || heads > 65536)
     return fail(VOC_INVALID_ARG, "attention: heads must be a multiple of kv_heads");
+  if (static_cast<long long>(heads / kv_heads) * max_q > (1ll << 30))
+    return fail(VOC_UNSUPPORTED, "attention: too many rows of a key head");
   if (max_kv < 0 || window < 0 || (causal != 0 && causal != 1))
     return fail(VOC_INVALID_ARG, "attention: max_kv, window or causal");
   if (!std::isfinite(softmax_scale)) return fail(VOC_INVALID_ARG, "attention: softmax_scale");

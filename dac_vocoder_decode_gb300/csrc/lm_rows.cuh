@@ -9,8 +9,6 @@
 // The norm is taken of the 32-bit sum, not of the rounded one: the sum is at hand and one
 // rounding less reaches q.
 #pragma once
-#include <type_traits>
-
 #include "lm_common.cuh"
 
 namespace voc {
@@ -65,11 +63,43 @@ __device__ __forceinline__ float2 row_scale(uint32_t amax) {
   return make_float2(a / kE4m3Max, kE4m3Max / a);
 }
 
+constexpr int kRowValues = 32;    // values of a row that a thread keeps in registers
+constexpr int kAnyThreads = 256;  // threads of a row of any width
+constexpr int kRowThreads = 512;  // most threads of a row: rows of up to 16384 values
+
+// Sum, or maximum of magnitudes as bits (NaN kept), over a row's `tpr` threads (a power of two from 32 on);
+// `red` has a float per warp.  The order is fixed.
+__device__ __forceinline__ float row_sum(float v, int tpr, float *red) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (tpr > 32) {
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
+    __syncthreads();
+    const int base = threadIdx.x / tpr * (tpr / 32);
+    v = red[base];
+    for (int i = 1; i < tpr / 32; ++i) v += red[base + i];
+  }
+  return v;
+}
+__device__ __forceinline__ uint32_t row_max(uint32_t bits, int tpr, float *red) {
+  uint32_t v = __reduce_max_sync(0xffffffffu, bits);
+  if (tpr > 32) {
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = __uint_as_float(v);
+    __syncthreads();
+    const int base = threadIdx.x / tpr * (tpr / 32);
+    v = __float_as_uint(red[base]);
+    for (int i = 1; i < tpr / 32; ++i) v = max(v, __float_as_uint(red[base + i]));
+  }
+  return v;
+}
+
 // Any width, stride and alignment: one CTA per row, the row read once per pass (the later passes
 // from cache).
 template <typename T, int MODE>
-__global__ void __launch_bounds__(256) rows_any_kernel(const LmRowsArgs p) {
-  __shared__ float red[32];
+__global__ void __launch_bounds__(kAnyThreads) rows_any_kernel(const LmRowsArgs p) {
+  __shared__ float red[kAnyThreads / 32];
   pdl_wait();
   pdl_launch_dependents();
   const long long row = blockIdx.x;
@@ -86,21 +116,21 @@ __global__ void __launch_bounds__(256) rows_any_kernel(const LmRowsArgs p) {
   if (MODE == kRowsRms) {
     float ss = 0.f;
     uint32_t m = 0;
-    for (int i = threadIdx.x; i < p.d; i += 256) {
+    for (int i = threadIdx.x; i < p.d; i += kAnyThreads) {
       const float h = load(i);
       ss += h * h;
       m = max(m, abs_bits(h));
     }
-    ss = group_sum<256>(ss, red);
-    m = group_max<256>(m, red);
+    ss = row_sum(ss, kAnyThreads, red);
+    m = row_max(m, kAnyThreads, red);
     if (rms_needs_scaling(m)) {
       pre = rms_prescale(m);
       ss = 0.f;
-      for (int i = threadIdx.x; i < p.d; i += 256) {
+      for (int i = threadIdx.x; i < p.d; i += kAnyThreads) {
         const float h = load(i) * pre;
         ss += h * h;
       }
-      ss = group_sum<256>(ss, red);
+      ss = row_sum(ss, kAnyThreads, red);
     }
     rs = rms_factor(ss, p.d, p.eps, pre);
   }
@@ -108,11 +138,11 @@ __global__ void __launch_bounds__(256) rows_any_kernel(const LmRowsArgs p) {
     return MODE == kRowsRms ? h * pre * rs * to_f32(w[i]) : h;
   };
   uint32_t m = 0;
-  for (int i = threadIdx.x; i < p.d; i += 256) m = max(m, abs_bits(norm(load(i), i)));
-  m = group_max<256>(m, red);
+  for (int i = threadIdx.x; i < p.d; i += kAnyThreads) m = max(m, abs_bits(norm(load(i), i)));
+  m = row_max(m, kAnyThreads, red);
   const float2 sc = row_scale(m);
   if (threadIdx.x == 0) p.scale[row] = sc.x;
-  for (int i = threadIdx.x; i < p.d; i += 256) {
+  for (int i = threadIdx.x; i < p.d; i += kAnyThreads) {
     const float h = load(i);  // read before the sum's store: the sum may take x's or r's place
     if (s) s[i] = from_f32<T>(h);
     p.out[row * p.ldo + i] = e4m3(norm(h, i) * sc.y);
@@ -175,37 +205,6 @@ struct RowVec {
     }
   }
 };
-
-constexpr int kRowValues = 32;    // values of a row that a thread keeps in registers
-constexpr int kRowThreads = 512;  // most threads of a row: rows of up to 16384 values
-
-// Sum, or maximum of magnitudes (NaN kept), over a row's `tpr` threads (a power of two from 32 on);
-// `red` has a float per warp.  The order is fixed.
-__device__ __forceinline__ float row_sum(float v, int tpr, float *red) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (tpr > 32) {
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
-    __syncthreads();
-    const int base = threadIdx.x / tpr * (tpr / 32);
-    v = red[base];
-    for (int i = 1; i < tpr / 32; ++i) v += red[base + i];
-  }
-  return v;
-}
-__device__ __forceinline__ uint32_t row_max(float m, int tpr, float *red) {
-  uint32_t v = __reduce_max_sync(0xffffffffu, abs_bits(m));
-  if (tpr > 32) {
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = __uint_as_float(v);
-    __syncthreads();
-    const int base = threadIdx.x / tpr * (tpr / 32);
-    v = __float_as_uint(red[base]);
-    for (int i = 1; i < tpr / 32; ++i) v = max(v, __float_as_uint(red[base + i]));
-  }
-  return v;
-}
 
 // Rows of up to 16384 values, each read once and kept in registers by its `tpr` threads, CH
 // vectors of VB bytes each.  VB is the widest access that the row's buffers and strides allow.
@@ -288,7 +287,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LmRowsArgs p, c
       for (int i = 0; i < CH; ++i)
 #pragma unroll
         for (int j = 0; j < N; ++j) m = max_abs(m, h[i][j]);
-      const uint32_t top = row_max(m, tpr, red);
+      const uint32_t top = row_max(abs_bits(m), tpr, red);
       if (!holds && rms_needs_scaling(top)) pre = rms_prescale(top);
       float again = 0.f;
 #pragma unroll
@@ -317,7 +316,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LmRowsArgs p, c
   for (int i = 0; i < CH; ++i)
 #pragma unroll
     for (int j = 0; j < N; ++j) m = max_abs(m, h[i][j]);
-  const float2 sc = row_scale(row_max(m, tpr, red));
+  const float2 sc = row_scale(row_max(abs_bits(m), tpr, red));
   if (live && lane == 0) p.scale[row] = sc.x;
   uint8_t *out = p.out + row * p.ldo;
 #pragma unroll

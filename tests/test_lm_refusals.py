@@ -103,6 +103,12 @@ def test_attention_refusals(lib, change, text, status):
     _refused(lib, "vocoder_lm_attention", {**ATTN, **change}.values(), text, status)
 
 
+def test_attention_refuses_rows_beyond_its_counters(lib):
+    """heads / kv_heads times max_q rows share a key head; they are counted in 32 bits."""
+    call = {**ATTN, "heads": 65536, "kv_heads": 1, "max_q": 1 << 16, "n_tokens": 1 << 18}
+    _refused(lib, "vocoder_lm_attention", call.values(), "too many rows", V.VOC_UNSUPPORTED)
+
+
 def test_binding_refuses_wrong_tensors():
     torch = pytest.importorskip("torch")
     f8 = torch.zeros(4, 64, dtype=torch.uint8).view(torch.float8_e4m3fn)
