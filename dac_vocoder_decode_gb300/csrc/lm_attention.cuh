@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttn
   float *acc = reinterpret_cast<float *>(smem + kStages * 2 * kBytes);  // [two warps][row][kLd]
   __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
   __shared__ int prefix[kShareSeqs + 1];
-  __shared__ float2 ml[kAttnWarps][kRows];
+  __shared__ float2 ml[kAttnWarps][kRows], row_ml[kRows];  // maximum and sum: by warp, together
   __shared__ int abort_flag;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int g = lane / 4, t = lane % 4;
@@ -524,6 +524,14 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttn
         if (g == 0) ml[warp][8 * n + 2 * t + x] = make_float2(m[n][x], l[n][x]);
       }
     asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (tid < kRows) {
+      float top = -INFINITY, sum = 0.f;
+      for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, ml[w][tid].x);
+      for (int w = 0; w < kAttnWarps; ++w)
+        // a warp that saw no key has a sum of 0, or NaN where it met NaN alone
+        sum += ml[w][tid].x == -INFINITY ? ml[w][tid].y : ml[w][tid].y * ex2(ml[w][tid].x - top);
+      row_ml[tid] = make_float2(top, sum);
+    }
     // warps 2 and 3 hand their parts to 0 and 1, which add their own
 #pragma unroll
     for (int turn = 1; turn >= 0; --turn) {
@@ -545,24 +553,29 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttn
       }
       asm volatile("bar.sync 1, 128;" ::: "memory");
     }
-    for (int i = tid; i < kRows * D; i += 32 * kAttnWarps) {
-      const int r = i / D, d = i % D;
+    for (int i = tid; i < kRows * D / 4; i += 32 * kAttnWarps) {
+      const int r = i / (D / 4), d = i % (D / 4) * 4;
       if (r0 + r > r_last) break;
-      float top = -INFINITY;
-      for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, ml[w][r].x);
-      float sum = 0.f, v = 0.f;
-      for (int w = 0; w < kAttnWarps; ++w)
-        // a warp that saw no key has a sum of 0, or NaN where it met NaN alone
-        sum += ml[w][r].x == -INFINITY ? ml[w][r].y : ml[w][r].y * ex2(ml[w][r].x - top);
-      v = acc[r * kLd + d] + acc[(kRows + r) * kLd + d];
+      const float4 a0 = *reinterpret_cast<const float4 *>(acc + r * kLd + d);
+      const float4 a1 = *reinterpret_cast<const float4 *>(acc + (kRows + r) * kLd + d);
+      const float v[4] = {a0.x + a1.x, a0.y + a1.y, a0.z + a1.z, a0.w + a1.w};
       if (s.begins && s.ends) {
         const int tok = (r0 + r) / p.group, h = s.hk * p.group + (r0 + r) % p.group;
-        static_cast<T *>(p.out)[(s.w.span.first + tok) * p.ldo + h * p.hso + d] =
-            from_f32<T>(sum == 0.f ? 0.f : v / sum);
+        T *dst = static_cast<T *>(p.out) + (s.w.span.first + tok) * p.ldo + h * p.hso + d;
+        const float sum = row_ml[r].y, inv = 1.f / sum;
+        float f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = sum == 0.f ? 0.f : v[j] * inv;
+        if (reinterpret_cast<uintptr_t>(dst) % 8 == 0) {
+          *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) dst[j] = from_f32<T>(f[j]);
+        }
       } else {  // slot 2c: the tile began in an earlier CTA, 2c + 1: it begins here
         const long long slot = (2ll * blockIdx.x + (s.begins ? 1 : 0)) * kRows + r;
-        p.part_o[slot * D + d] = v;
-        if (d == 0) p.part_ml[slot] = make_float2(top, sum);
+        *reinterpret_cast<float4 *>(p.part_o + slot * D + d) = make_float4(v[0], v[1], v[2], v[3]);
+        if (d == 0) p.part_ml[slot] = row_ml[r];
       }
     }
     asm volatile("bar.sync 1, 128;" ::: "memory");  // the buffers are free for the next piece
@@ -575,7 +588,6 @@ template <typename T, int D, int ROWS, bool SHARES>
 __global__ void __launch_bounds__(D) attn_join_kernel(const LmAttnArgs p) {
   constexpr int kWarps = D / 32;
   __shared__ int counts[2][kWarps];
-  __shared__ float red[2][kWarps], factor[D];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int b = blockIdx.z, hk = blockIdx.y, row = blockIdx.x;
   // Lengths and counts were complete before the kernel that this one follows started its work, and
@@ -619,35 +631,35 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const LmAttnArgs p) {
     const long long slot = SHARES ? (s == 0 ? 2ll * c0 + 1 : 2ll * (c0 + s)) : tile * p.splits + s;
     return slot * ROWS + row % ROWS;
   };
-  float top = -INFINITY;
-  for (int s = tid; s < parts; s += D) top = fmaxf(top, p.part_ml[slot_of(s)].x);
+  // Every warp weighs the parts for itself, a lane each, without a barrier.  The first values are
+  // fetched beside the maxima: what the join takes is its chain of reads.
+  constexpr int kEarly = 8;
+  float early[kEarly], top = -INFINITY;
+  for (int s = lane; s < parts; s += 32) top = fmaxf(top, p.part_ml[slot_of(s)].x);
+#pragma unroll
+  for (int s = 0; s < kEarly; ++s) early[s] = s < parts ? p.part_o[slot_of(s) * D + tid] : 0.f;
 #pragma unroll
   for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) red[0][warp] = top;
-  __syncthreads();
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, red[0][w]);
   float sum = 0.f, v = 0.f;
-  for (int s0 = 0; s0 < parts; s0 += D) {  // factors of up to D parts, then their sum
+  for (int s0 = 0; s0 < parts; s0 += 32) {
     float f = 0.f;
-    if (s0 + tid < parts) {
-      const float2 x = p.part_ml[slot_of(s0 + tid)];
+    if (s0 + lane < parts) {
+      const float2 x = p.part_ml[slot_of(s0 + lane)];
       // a part that saw no key has a sum of 0, or NaN where it met NaN alone
       f = x.x == -INFINITY ? 0.f : ex2(x.x - top);
       sum += x.x == -INFINITY ? x.y : x.y * f;
     }
-    __syncthreads();
-    factor[tid] = f;
-    __syncthreads();
-    const int n = min(D, parts - s0);
+    if (s0 == 0) {
+#pragma unroll
+      for (int s = 0; s < kEarly; ++s) v = fmaf(__shfl_sync(0xffffffffu, f, s), early[s], v);
+    }
+    const int n = min(32, parts - s0);
 #pragma unroll 8
-    for (int s = 0; s < n; ++s) v = fmaf(factor[s], p.part_o[slot_of(s0 + s) * D + tid], v);
+    for (int s = s0 ? 0 : kEarly; s < n; ++s)
+      v = fmaf(__shfl_sync(0xffffffffu, f, s), p.part_o[slot_of(s0 + s) * D + tid], v);
   }
 #pragma unroll
   for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) red[1][warp] = sum;
-  __syncthreads();
-  sum = 0.f;
-  for (int w = 0; w < kWarps; ++w) sum += red[1][w];
   const int tok = row / p.group, h = hk * p.group + row % p.group;
   static_cast<T *>(p.out)[(span.first + tok) * p.ldo + h * p.hso + tid] =
       from_f32<T>(sum == 0.f ? 0.f : v / sum);
