@@ -87,6 +87,9 @@ struct AppendShape {
 // as they were read, so both are read once.  A warp covers 32 tokens x 32 channels: its loads and
 // its stores of K rows and of V rows (4 tokens of a channel are one word) all fill 32-byte sectors,
 // without a pass through shared memory.
+// Measured: prompts of 13423 tokens, 8 heads of 128 channels (95 MB): 23.0 us, 4.1 TB/s: the chain of
+// lengths, page and tokens, block maximum, stores, covered by the 4 CTAs of an SM only in part.  8
+// single tokens 3.2 us, the same chain.
 // FEW: for single tokens and short chunks, whose time is the chain of dependent reads: words of V that
 // new and earlier tokens share are read beside the scales, at the cost of registers that whole blocks
 // have a better use for (8 single tokens 5.8 -> 3.9 us; prompts 22.9 -> 26.6 us).

@@ -182,7 +182,8 @@ bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % 
 bool known_flags(unsigned f) { return (f & ~static_cast<unsigned>(VOC_FLAG_SYNC)) == 0; }
 
 // Threads of a row: as few as hold it in registers, and more of them while there are too few rows
-// to fill the GPU (up to a chunk of values per thread).
+// to fill the GPU (up to a chunk of values per thread).  Measured, without / with more: 8 x 1024 2.8 /
+// 2.2 us, 256 x 4096 3.6 / 3.1 us.
 int row_threads(int sms, long long rows, int d, int chunk) {
   int t = 32;
   while (t * voc::kRowValues < d) t *= 2;
@@ -382,10 +383,11 @@ VOC_API voc_status vocoder_lm_linear_fp8(const void *x8, long long ldx, const fl
   a.nt = ((M + m_tiles - 1) / m_tiles + 15) / 16 * 16;  // equal tiles of up to 256 tokens
   a.tmem_cols = 32;
   while (a.tmem_cols < a.nt) a.tmem_cols *= 2;
-  // Up to 64 tokens leave room for two CTAs on an SM.  K is split over up to 8 CTAs as long as all
-  // clusters run at once, and each keeps 4 stages of K once every SM has a CTA.  Measured at 33 tokens,
-  // N x K = 12288 x 4096 (96 tiles): split 1 14.7, 2 12.5, 3 12.8 (does not fit), 4 17.2 us; 8 tokens,
-  // 2048 x 8192 (16 tiles): split 1 21.9, 4 7.9, 8 5.9 us.
+  // Up to 64 tokens leave room for two CTAs on an SM (measured, one / two, N x K = 12288 x 4096: 33
+  // tokens 13.8 / 12.5 us, 64 tokens 14.5 / 13.5; 4096 x 4096: 16 tokens 5.9 / 5.7, 64 tokens 6.8 /
+  // 7.8).  K is split over up to 8 CTAs as long as all clusters run at once, and each keeps 4 stages of
+  // K once every SM has a CTA.  Measured at 33 tokens, 12288 x 4096 (96 tiles): split 1 14.7, 2 12.5,
+  // 3 12.8 (does not fit), 4 17.2 us; 8 tokens, 2048 x 8192 (16 tiles): split 1 21.9, 4 7.9, 8 5.9 us.
   const int stage = (voc::kLinRows + a.nt) * voc::kLinK;
   const int tiles = ((N + voc::kLinRows - 1) / voc::kLinRows) * ((M + a.nt - 1) / a.nt);
   const int per_sm = a.nt <= 64 ? 2 : 1;
@@ -489,9 +491,22 @@ VOC_API voc_status vocoder_lm_kv_append(void *k_cache, void *v_cache, float *k_s
 
 namespace {
 
-// From this many rows (queries that share a key head) of a sequence the attention runs on tiles of
-// 256 rows, below on tiles of 8 or 16.
+// From kPromptRows rows (queries that share a key head) of a sequence the attention runs on tiles of
+// 256 rows (prompt kernel), below on tiles of 8 or 16 (row kernel).  Measured, 8 sequences of 4000
+// tokens, 8 heads of 128 channels (us, row / prompt kernel): 16 rows 31.2 / 38.4, 32 rows 41.9 / 39.6,
+// 36 rows 51.9 / 40.1; 8 of 15504: 32 rows 108 / 126; one of 15504: 32 rows 29 / 22.
+// Up to kShortBlocks blocks of keys the row kernel takes more rows too, as long as all its tiles run at
+// once: the prompt kernel has about 10 us before its first and after its last product.  Measured, 256
+// rows x 4 heads: 500 tokens 7.3 / 13.3, 1000 tokens 10.0 / 13.4; 64 rows x 16 heads, 2000 tokens
+// (beyond the limit): 22.3 / 14.0.
 constexpr int kPromptRows = 33;
+constexpr int kShortBlocks = 16;
+// A tile of the row kernel is a CTA's, unless equal shares of all blocks spare the busiest CTA this
+// many: a share that starts inside a tile and the join of its parts cost about as much.  Measured (us,
+// whole tiles / shares), 128 tiles of 64 channels: 16 blocks 8.0 / 11.7, 32 blocks 13.3 / 14.1, 63
+// blocks 23.8 / 20.5; 16 tiles: 16 blocks 7.9 / 7.0, 32 blocks 12.8 / 7.2; 256 tiles of 128 channels,
+// 63 blocks 42.9 / 49.1.
+constexpr int kShareGain = 20;
 
 struct AttnPlan {
   bool prompt = false;
@@ -503,9 +518,11 @@ struct AttnPlan {
   size_t ws_bytes = 0;
 };
 
-// Row kernel: two CTAs per SM in equal shares, unless no tile has more than two of the smallest
-// shares' blocks (then a tile is a CTA's) or there are too many sequences to count through.  Prompt
-// kernel: keys are split while there are fewer tiles than SMs, into parts of 8 blocks or more.
+// Row kernel: a CTA per tile, or equal shares for two CTAs per SM (kShareGain).  Prompt kernel: keys
+// are split while there are fewer tiles than SMs, into parts of 4 blocks or more, and no more than
+// 1.5 sqrt(blocks) of them, beyond which the parts' join costs what the shorter parts save.  Measured,
+// 256 rows x 4 heads, 1000 tokens: parts of 16 blocks 25.3, 8 22.7, 4 19.2 us; 8000 tokens: 7 parts
+// 32.9, 17 24.2, 31 26.6 us.
 AttnPlan plan_attention(int sms, int n_seq, int max_q, int heads, int kv_heads, int head_dim,
                         int max_kv, int window) {
   AttnPlan p;
@@ -513,23 +530,24 @@ AttnPlan plan_attention(int sms, int n_seq, int max_q, int heads, int kv_heads, 
   const long long heads_all = static_cast<long long>(n_seq) * kv_heads;
   long long keys = max_kv;
   if (window > 0) keys = std::min<long long>(keys, static_cast<long long>(window) + max_q);
-  p.prompt = rows >= kPromptRows;
+  const long long blocks = keys / voc::kBlockTokens + 1, slots = 2ll * sms;
+  p.tile = rows <= 8 ? 8 : 16;
+  const long long row_tiles = (rows + p.tile - 1) / p.tile, tiles = heads_all * row_tiles;
+  p.prompt = rows >= kPromptRows && !(blocks <= kShortBlocks && tiles <= slots);
   if (p.prompt) {
     p.row_tiles = static_cast<int>((rows + voc::kPartRows - 1) / voc::kPartRows);
-    const long long tiles = heads_all * ((rows + voc::kPrRows - 1) / voc::kPrRows);
-    const long long steps = keys / voc::kBlockTokens + 1;
-    const long long splits = tiles >= sms ? 1 : sms / tiles;
-    p.splits = static_cast<int>(std::max(1ll, std::min({splits, steps / 8, 65535ll / n_seq})));
+    const long long ctas = heads_all * ((rows + voc::kPrRows - 1) / voc::kPrRows);
+    const long long fits = std::min({ctas >= sms ? 1 : sms / ctas, blocks / 4, 65535ll / n_seq});
+    while (p.splits < fits && 4ll * (p.splits + 1) * (p.splits + 1) <= 9 * blocks) ++p.splits;
     if (p.splits > 1)
       p.slots = static_cast<size_t>(heads_all) * p.row_tiles * p.splits * voc::kPartRows;
   } else {
-    p.tile = rows <= 8 ? 8 : 16;
-    p.row_tiles = static_cast<int>((rows + p.tile - 1) / p.tile);
-    const long long blocks = keys / voc::kBlockTokens + 1;
-    const long long units = heads_all * p.row_tiles * blocks;
-    if (n_seq <= voc::kShareSeqs && blocks > 2 * voc::kShareMin && units < (1ll << 30)) {
-      p.ctas = static_cast<int>(
-          std::min<long long>(2 * sms, (units + voc::kShareMin - 1) / voc::kShareMin));
+    p.row_tiles = static_cast<int>(row_tiles);
+    const long long units = tiles * blocks;
+    const long long alone = (tiles + slots - 1) / slots * blocks;  // blocks of the busiest CTA
+    const long long shared = std::max<long long>((units + slots - 1) / slots, voc::kShareMin);
+    if (n_seq <= voc::kShareSeqs && alone >= shared + kShareGain && units < (1ll << 30)) {
+      p.ctas = static_cast<int>(std::min(slots, (units + voc::kShareMin - 1) / voc::kShareMin));
       p.slots = 2ull * p.ctas * p.tile;
     }
   }

@@ -95,8 +95,9 @@ __device__ __forceinline__ uint32_t row_max(uint32_t bits, int tpr, float *red) 
   return v;
 }
 
-// Any width, stride and alignment: one CTA per row, the row read once per pass (the later passes
-// from cache).
+// Rows of more than 16384 values, any stride and alignment: one CTA per row, the row read once per
+// pass (the later passes from cache), a value at a time.  Bound by its dependent loads: 512 x 20000
+// bf16 with norm and residual 65 us (1.1 TB/s), gated 31 us.
 template <typename T, int MODE>
 __global__ void __launch_bounds__(kAnyThreads) rows_any_kernel(const LmRowsArgs p) {
   __shared__ float red[kAnyThreads / 32];
@@ -211,6 +212,11 @@ struct RowVec {
 // With d values a row moves 7 d bytes (16-bit, residual), and the kernel has to spend few
 // instructions on a value to keep up with that: conversions two at a time, and magnitudes before
 // the norm are looked at only where the sum of squares says that squares overflowed or vanished.
+// Measured (bf16, residual): 15504 x 1536 27.8 us, 6.0 TB/s, where a plain copy reaches 6.8 (one value
+// at a time it was 46.5 us); 2000 x 16384 40 us, 5.7 TB/s; 8 x 1024 2.2 us, a launch and a chain of two
+// loads and two reductions.  Gated 4001 x 4100 f16: 20.1 us, 4.1 TB/s: 8-byte accesses (the rows'
+// second halves start on 8 bytes) and rows of one load, one reduction and one store, whose chain the
+// few resident rows cover only in part.
 template <typename T, int MODE, int VB, int CH>
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LmRowsArgs p, const int tpr) {
   using Vec = RowVec<T, VB>;
