@@ -146,7 +146,7 @@ struct Segment {
 // queries a head: 47.9 us with the join, 5.3 TB/s; in its middle the kernel reads about 7, and some
 // 11 us are the launch, the first blocks' way in, CTAs that end at different times, and the join.  With
 // 16-row tiles the same call takes 59 us (twice the products and registers): 8 rows and fewer have
-// tiles of their own.  A warp a block and whole blocks per warp, with the rows as the MMA's 16, took
+// tiles of their own.  With the products the other way round and a fixed split of each tile it took
 // 76 us.  One sequence of 250 tokens: 4.2 us, latency.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttnArgs p) {
