@@ -17,7 +17,8 @@ constexpr int kAttnThreads = 32 * (kAttnWarps + 1);
 constexpr float kLazy = 8.f;    // log2 of how far the weights' maximum may run ahead
 constexpr float kPShift = 7.f;  // weights are kept times 2^7 in 16 bits, so below 2^15
 constexpr int kShareSeqs = 512;   // sequences up to which CTAs take equal shares of the work
-constexpr int kShareMin = 4;      // blocks of the smallest share
+constexpr int kShareMin = 4;      // units of the smallest share
+constexpr int kTileCost = 8;      // units that a tile counts beside its blocks
 
 struct LmAttnArgs {
   const void *q;
@@ -91,6 +92,11 @@ struct SeqWork {
   int blk0, blocks;
   int units;
 };
+// Units of one of its tiles: the first kTileCost stand for the way to its first product and from its
+// last one, a unit for each block follows (one for a tile without keys: it has zeros to write).
+__device__ __forceinline__ int tile_units(const SeqWork &w) {
+  return kTileCost + max(w.blocks, 1);
+}
 template <int ROWS>
 __device__ __forceinline__ SeqWork seq_work(const LmAttnArgs &p, int b) {
   SeqWork w;
@@ -104,13 +110,13 @@ __device__ __forceinline__ SeqWork seq_work(const LmAttnArgs &p, int b) {
   const long long hi = visible(p, w.p0 + w.span.count - 1, w.len).hi;
   w.blk0 = static_cast<int>(lo / kBlockTokens);
   w.blocks = hi > lo ? static_cast<int>((hi - 1) / kBlockTokens) + 1 - w.blk0 : 0;
-  // a tile without keys still has zeros to write: one unit of work
-  w.units = max(w.blocks, 1) * p.kv_heads * w.tiles;
+  w.units = tile_units(w) * p.kv_heads * w.tiles;
   return w;
 }
 
 // Share of the total work: CTA c has the units [c q, (c + 1) q) in the order (sequence, key head, row
-// tile, block).  The host shares only where the units fit 30 bits.
+// tile, block), a tile's blocks behind its first kTileCost units.  The host shares only where the
+// units fit 30 bits.
 __device__ __forceinline__ int share_of(int total, int ctas) {
   return max((total + ctas - 1) / ctas, kShareMin);
 }
@@ -129,6 +135,7 @@ struct Segment {
   SeqWork w;
   int b, hk, rt, first, count;
   bool begins, ends;  // the tile's work starts / ends in this CTA
+  bool none;          // the share ends before the tile's first block
 };
 
 // Rows (queries that share a key head) in tiles of 8 NT, for the few rows of single tokens.  K and
@@ -214,19 +221,22 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttn
       }
       s.b = a;
       s.w = seq_work<kRows>(p, a);
-      const int per = max(s.w.blocks, 1);
+      const int per = tile_units(s.w);
       const int tile = (at - prefix[a]) / per;
       const int begin = (at - prefix[a]) % per;
       const int end = min(per, begin + (hi - at));
       s.hk = tile / s.w.tiles, s.rt = tile % s.w.tiles;
-      s.begins = begin == 0, s.ends = end == per;
-      s.first = s.w.blk0 + begin;
-      s.count = min(end, s.w.blocks) - begin;
+      const int from = max(begin - kTileCost, 0), upto = end - kTileCost;  // the tile's blocks
+      s.begins = from == 0, s.ends = end == per;
+      s.none = upto <= 0;
+      s.first = s.w.blk0 + from;
+      s.count = s.none ? 0 : min(upto, s.w.blocks) - from;
       next = at + (end - begin);
     } else {
       s.b = blockIdx.z, s.hk = blockIdx.y, s.rt = blockIdx.x;
       s.w = seq_work<kRows>(p, s.b);
       s.begins = s.ends = true;
+      s.none = false;
       s.first = s.w.blk0;
       s.count = s.rt < s.w.tiles ? s.w.blocks : 0;
       next = hi;
@@ -289,7 +299,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttn
   for (int at = lo, next; at < hi; at = next) {
     const Segment s = segment(at, next);
     const int r0 = s.rt * kRows, r_last = min(s.w.rows, r0 + kRows) - 1;
-    if (r0 > r_last) continue;  // whole-tile launches cover max_q tokens
+    if (r0 > r_last || s.none) continue;  // whole-tile launches cover max_q tokens
     // scales of this warp's blocks (every other one): loaded one of them ahead of their use, the
     // pages two ahead
     const int *table = p.table + s.b * p.ldt + s.first;
@@ -623,10 +633,10 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const LmAttnArgs p) {
       for (int w = 0; w < kWarps; ++w) both[k] += counts[k][w];
     }
     const SeqWork w = seq_work<ROWS>(p, b);
-    const int per = max(w.blocks, 1);
+    const int per = tile_units(w);
     const int q = share_of(both[1], p.ctas);
     const int at = both[0] + (hk * w.tiles + row / ROWS) * per;
-    c0 = at / q, c1 = (at + per - 1) / q;
+    c0 = (at + kTileCost) / q, c1 = (at + per - 1) / q;
   }
   pdl_wait();
   pdl_launch_dependents();

@@ -543,8 +543,8 @@ AttnPlan plan_attention(int sms, int n_seq, int max_q, int heads, int kv_heads, 
       p.slots = static_cast<size_t>(heads_all) * p.row_tiles * p.splits * voc::kPartRows;
   } else {
     p.row_tiles = static_cast<int>(row_tiles);
-    const long long units = tiles * blocks;
-    const long long alone = (tiles + slots - 1) / slots * blocks;  // blocks of the busiest CTA
+    const long long units = tiles * (blocks + voc::kTileCost);
+    const long long alone = (tiles + slots - 1) / slots * (blocks + voc::kTileCost);  // the busiest CTA's
     const long long shared = std::max<long long>((units + slots - 1) / slots, voc::kShareMin);
     if (n_seq <= voc::kShareSeqs && alone >= shared + kShareGain && units < (1ll << 30)) {
       p.ctas = static_cast<int>(std::min(slots, (units + voc::kShareMin - 1) / voc::kShareMin));
@@ -621,7 +621,7 @@ VOC_API voc_status vocoder_lm_attention(
   AttnPlan plan =
       plan_attention(dev->sms, n_seq, max_q, heads, kv_heads, head_dim, max_kv, window);
   // lengths are on the device and may exceed max_kv: what the page table can hold bounds them
-  if (static_cast<double>(n_seq) * kv_heads * plan.row_tiles * (table_cols + 1.0) >= 0x1p30)
+  if (static_cast<double>(n_seq) * kv_heads * plan.row_tiles * (table_cols + 1.0 + voc::kTileCost) >= 0x1p30)
     plan.ctas = 0;
   if (plan.ws_bytes && (!ws || ws_bytes < plan.ws_bytes))
     return fail(VOC_WORKSPACE_TOO_SMALL, "attention: workspace below vocoder_lm_attention_ws_bytes");
