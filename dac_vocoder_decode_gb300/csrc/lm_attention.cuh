@@ -17,6 +17,8 @@ constexpr int kAttnThreads = 32 * (kAttnWarps + 1);
 constexpr float kLazy = 8.f;    // log2 of how far the weights' maximum may run ahead
 constexpr float kPShift = 7.f;  // weights are kept times 2^7 in 16 bits, so below 2^15
 constexpr int kShareSeqs = 512;   // sequences up to which CTAs take equal shares of the work
+constexpr int kPrRows = 256;      // rows of a tile of the prompt kernel
+constexpr int kFlatTiles = 512;   // sequences up to which its CTAs count through the tiles
 constexpr int kShareMin = 4;      // units of the smallest share
 constexpr int kTileCost = 8;      // units that a tile counts beside its blocks
 
@@ -31,8 +33,8 @@ struct LmAttnArgs {
   int n_pages, table_cols, heads, kv_heads, group, n_seq, n_tokens, max_q;
   float scale_log2;  // softmax_scale * log2(e)
   int causal, window;
-  int row_tiles;     // of the kernel's own tile size, for max_q tokens
   int splits;        // prompt kernel: parts of a tile's keys
+  int flat;          // prompt kernel: tiles that CTAs count through, or 0: blockIdx.z is the sequence
   int ctas;          // row kernel: CTAs that share the work, or 0 (one tile each)
   float *part_o;     // partial outputs [slot][row][D] and their maxima and sums [slot][row]
   float2 *part_ml;
@@ -81,6 +83,11 @@ __device__ __forceinline__ KeySpan visible(const LmAttnArgs &p, long long pos, l
   s.hi = p.causal ? min(len, pos + 1) : len;
   s.lo = p.window > 0 ? max(0ll, pos - p.window + 1) : 0;
   return s;
+}
+
+// Tiles of the prompt kernel for one sequence.
+__device__ __forceinline__ int prompt_tiles(const LmAttnArgs &p, const SeqSpan &s) {
+  return (s.count * p.group + kPrRows - 1) / kPrRows;
 }
 
 // What the row kernel does for one sequence: its rows, the blocks [blk0, blk0 + blocks) that any of
@@ -599,10 +606,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttn
   }
 }
 
-// Joins the parts of a tile's row, one CTA of D threads per row, a channel each.  SHARES: the row
-// kernel's parts (ROWS = 8 NT); else the prompt kernel's, [tile of ROWS rows][split][ROWS].  Bound by
-// its chain of reads: with barriers and the values read after the maxima it took 3 us more.
-template <typename T, int D, int ROWS, bool SHARES>
+// Joins the parts of a row kernel's tile, one CTA of D threads per row, a channel each.  Bound by its
+// chain of reads: with barriers and the values read after the maxima it took 3 us more.
+template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(D) attn_join_kernel(const LmAttnArgs p) {
   constexpr int kWarps = D / 32;
   __shared__ int counts[2][kWarps];
@@ -611,43 +617,36 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const LmAttnArgs p) {
   // Lengths and counts were complete before the kernel that this one follows started its work, and
   // it writes neither, so they are read before waiting for it.
   const SeqSpan span = seq_span(p.cu, b, p.n_seq, p.n_tokens, p.max_q);
-  int c0 = 0, c1 = 0;
-  if (SHARES) {
-    // the work before this sequence and in all, as attn_rows_kernel counts it
-    int both[2] = {0, 0};
-    for (int i = tid; i < p.n_seq; i += D) {
-      const int u = seq_work<ROWS>(p, i).units;
-      both[1] += u;
-      if (i < b) both[0] += u;
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-#pragma unroll
-      for (int o = 16; o; o /= 2) both[k] += __shfl_xor_sync(0xffffffffu, both[k], o);
-      if (lane == 0) counts[k][warp] = both[k];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      both[k] = 0;
-      for (int w = 0; w < kWarps; ++w) both[k] += counts[k][w];
-    }
-    const SeqWork w = seq_work<ROWS>(p, b);
-    const int per = tile_units(w);
-    const int q = share_of(both[1], p.ctas);
-    const int at = both[0] + (hk * w.tiles + row / ROWS) * per;
-    c0 = (at + kTileCost) / q, c1 = (at + per - 1) / q;
+  // the work before this sequence and in all, as attn_rows_kernel counts it
+  int both[2] = {0, 0};
+  for (int i = tid; i < p.n_seq; i += D) {
+    const int u = seq_work<ROWS>(p, i).units;
+    both[1] += u;
+    if (i < b) both[0] += u;
   }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+#pragma unroll
+    for (int o = 16; o; o /= 2) both[k] += __shfl_xor_sync(0xffffffffu, both[k], o);
+    if (lane == 0) counts[k][warp] = both[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    both[k] = 0;
+    for (int w = 0; w < kWarps; ++w) both[k] += counts[k][w];
+  }
+  const SeqWork w = seq_work<ROWS>(p, b);
+  const int per = tile_units(w);
+  const int q = share_of(both[1], p.ctas);
+  const int at = both[0] + (hk * w.tiles + row / ROWS) * per;
+  const int c0 = (at + kTileCost) / q, c1 = (at + per - 1) / q;
   pdl_wait();
   pdl_launch_dependents();
-  if (row >= span.count * p.group) return;
-  if (SHARES && c0 == c1) return;  // one CTA had the whole tile
-  const long long tile =
-      (static_cast<long long>(b) * p.kv_heads + hk) * p.row_tiles + row / ROWS;
-  const int parts = SHARES ? c1 - c0 + 1 : p.splits;
+  if (row >= span.count * p.group || c0 == c1) return;  // c0 == c1: one CTA had the whole tile
+  const int parts = c1 - c0 + 1;
   auto slot_of = [&](int s) {
-    const long long slot = SHARES ? (s == 0 ? 2ll * c0 + 1 : 2ll * (c0 + s)) : tile * p.splits + s;
-    return slot * ROWS + row % ROWS;
+    return (s == 0 ? 2ll * c0 + 1 : 2ll * (c0 + s)) * ROWS + row % ROWS;
   };
   // Every warp weighs the parts for itself, a lane each, without a barrier.  The first values are
   // fetched beside the maxima: what the join takes is its chain of reads.
@@ -681,6 +680,93 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const LmAttnArgs p) {
   const int tok = row / p.group, h = hk * p.group + row % p.group;
   static_cast<T *>(p.out)[(span.first + tok) * p.ldo + h * p.hso + tid] =
       from_f32<T>(sum == 0.f ? 0.f : v / sum);
+}
+
+// The sequence that the prompt kernel's tile `index` (counted over all sequences) is of, or -1, and
+// which of its tiles that is.  For whole warps.
+__device__ __forceinline__ int find_tile(const LmAttnArgs &p, int index, int lane, int &nth) {
+  for (int i0 = 0, before = 0; i0 < p.n_seq; i0 += 32) {
+    const int tiles =
+        i0 + lane < p.n_seq
+            ? prompt_tiles(p, seq_span(p.cu, i0 + lane, p.n_seq, p.n_tokens, p.max_q)) : 0;
+    int upto = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int u = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += u;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, before + upto > index);
+    if (past) {
+      const int at = __ffs(past) - 1;
+      nth = index - before - __shfl_sync(0xffffffffu, upto - tiles, at);
+      return i0 + at;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return -1;
+}
+
+// Joins the parts of the prompt kernel's tiles, a warp per row.  One CTA per row of the longest chunk
+// and sequence took 25 us for 8 chunks of 1 to 200 tokens, most of them for rows that are not there.
+constexpr int kJoinRows = 8;
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kJoinRows) attn_join_tiles_kernel(const LmAttnArgs p) {
+  constexpr int kPer = D / 32;  // channels of a lane
+  const int lane = threadIdx.x % 32, hk = blockIdx.y;
+  int nth = 0;
+  const int b = find_tile(p, blockIdx.x, lane, nth);  // (counts may be read early: attn_join_kernel)
+  pdl_wait();
+  pdl_launch_dependents();
+  if (b < 0) return;
+  const SeqSpan span = seq_span(p.cu, b, p.n_seq, p.n_tokens, p.max_q);
+  const int local = blockIdx.z * kJoinRows + threadIdx.x / 32, row = nth * kPrRows + local;
+  if (row >= span.count * p.group) return;
+  const long long tile = static_cast<long long>(blockIdx.x) * p.kv_heads + hk;
+  auto slot_of = [&](int s) { return (tile * p.splits + s) * kPrRows + local; };
+  float top = -INFINITY;
+  for (int s = lane; s < p.splits; s += 32) top = fmaxf(top, p.part_ml[slot_of(s)].x);
+#pragma unroll
+  for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float sum = 0.f, v[kPer] = {};
+  for (int s0 = 0; s0 < p.splits; s0 += 32) {
+    float f = 0.f;
+    if (s0 + lane < p.splits) {
+      const float2 x = p.part_ml[slot_of(s0 + lane)];
+      // a part that saw no key has a sum of 0, or NaN where it met NaN alone
+      f = x.x == -INFINITY ? 0.f : ex2(x.x - top);
+      sum += x.x == -INFINITY ? x.y : x.y * f;
+    }
+    const int n = min(32, p.splits - s0);
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const float g = __shfl_sync(0xffffffffu, f, s);
+      const float *from = p.part_o + slot_of(s0 + s) * D + kPer * lane;
+      float o[kPer];
+      if constexpr (kPer == 4) {
+        const float4 w = *reinterpret_cast<const float4 *>(from);
+        o[0] = w.x, o[1] = w.y, o[2] = w.z, o[3] = w.w;
+      } else {
+        const float2 w = *reinterpret_cast<const float2 *>(from);
+        o[0] = w.x, o[1] = w.y;
+      }
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) v[k] = fmaf(g, o[k], v[k]);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const int tok = row / p.group, h = hk * p.group + row % p.group;
+  T *dst = static_cast<T *>(p.out) + (span.first + tok) * p.ldo + h * p.hso + kPer * lane;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) v[k] = sum == 0.f ? 0.f : v[k] / sum;
+  if (reinterpret_cast<uintptr_t>(dst) % 4 == 0) {
+#pragma unroll
+    for (int k = 0; k < kPer; k += 2)
+      reinterpret_cast<uint32_t *>(dst)[k / 2] = pack2<T>(v[k], v[k + 1]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) dst[k] = from_f32<T>(v[k]);
+  }
 }
 
 }  // namespace voc

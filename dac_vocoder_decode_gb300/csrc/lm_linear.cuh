@@ -216,27 +216,29 @@ constexpr int kManyStages = 6;
 constexpr int kManyOut = 8 * 32 * 64;        // output staging: 32 rows of 64 bytes for each warp
 constexpr size_t kManySmem = static_cast<size_t>(kManyStages) * kManyStage + kManyOut + 1024;
 
-// 16 bytes of an output row, as far as the row goes (`left` values), in the widest stores that its
-// place allows.
-template <typename T>
-__device__ __forceinline__ void store_out16(T *dst, const uint4 &v, int left) {
-  constexpr int kPer = 16 / static_cast<int>(sizeof(T));
-  const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst)) & 15;
-  if (left >= kPer && at == 0) {
-    *reinterpret_cast<uint4 *>(dst) = v;
-  } else if (left >= kPer && at == 8) {
-    reinterpret_cast<uint2 *>(dst)[0] = make_uint2(v.x, v.y);
-    reinterpret_cast<uint2 *>(dst)[1] = make_uint2(v.z, v.w);
-  } else if (left >= kPer && at % 4 == 0) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// A staged piece, 32 rows of 64 bytes of which `left` values are of the row, to rows that start on
+// sizeof(U) bytes, in U: lanes next to each other write what lies next to each other.
+template <typename T, typename U>
+__device__ __forceinline__ void store_piece(T *dst, long long ldo, const uint8_t *stage, int rows,
+                                            int left, int lane) {
+  constexpr int kUnits = 64 / static_cast<int>(sizeof(U)), kRows = 32 / kUnits;
+  constexpr int kVals = static_cast<int>(sizeof(U) / sizeof(T));
+  const int u = lane % kUnits, c = u * kVals;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t *>(dst)[i] = w[i];
-  } else {
-    T e[kPer];
-    memcpy(e, &v, 16);
+  for (int i = 0; i < 32 / kRows; ++i) {
+    const int r = i * kRows + lane / kUnits, at = u * static_cast<int>(sizeof(U));
+    const U v = *reinterpret_cast<const U *>(stage + r * 64 + ((at / 16 ^ (r >> 1 & 3)) << 4) + at % 16);
+    if (r >= rows) continue;
+    T *to = dst + r * ldo + c;
+    if (c + kVals <= left) {
+      *reinterpret_cast<U *>(to) = v;
+    } else if constexpr (kVals > 1) {
+      T e[kVals];
+      memcpy(e, &v, sizeof(U));
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (i < left) dst[i] = e[i];
+      for (int j = 0; j < kVals; ++j)
+        if (c + j < left) to[j] = e[j];
+    }
   }
 }
 
@@ -365,6 +367,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) __cluster_dims__(2, 1, 1)
     constexpr int kPer = 16 / static_cast<int>(sizeof(T));
     const int quad = warp % 4, c_first = warp / 4 * (kManyTile / 2);
     T *out = static_cast<T *>(p.out);
+    // what every output row (and so every piece of one, 64 bytes apart) starts on
+    const uint32_t start = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(out)) |
+                           static_cast<uint32_t>(p.ldo * sizeof(T));
     const uint32_t empty0 = mapa_shared(smem_u32(acc_empty), 0u);
     const uint32_t stage = smem_u32(ring) + kManyStages * kManyStage + warp * (32 * 64);
     int k = 0;
@@ -420,13 +425,14 @@ __global__ void __launch_bounds__(kManyThreads, 1) __cluster_dims__(2, 1, 1)
           sts128(stage + lane * 64 + (((i / kPer) ^ (lane >> 1 & 3)) << 4), v);
         }
         __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = 8 * i + lane / 4, u = lane % 4, c = c0 + u * kPer;
-          const uint4 v = lds128(stage + rr * 64 + ((u ^ (rr >> 1 & 3)) << 4));
-          if (row0 + rr < p.M && c < cols)
-            store_out16(out + static_cast<long long>(row0 + rr) * p.ldo + n0 + c, v, cols - c);
-        }
+        T *dst = out + static_cast<long long>(row0) * p.ldo + n0 + c0;
+        const uint8_t *piece = ring + kManyStages * kManyStage + warp * (32 * 64);
+        if (start % 16 == 0)
+          store_piece<T, uint4>(dst, p.ldo, piece, p.M - row0, cols - c0, lane);
+        else if (start % 4 == 0)
+          store_piece<T, uint32_t>(dst, p.ldo, piece, p.M - row0, cols - c0, lane);
+        else
+          store_piece<T, T>(dst, p.ldo, piece, p.M - row0, cols - c0, lane);
       }
       __syncwarp();
       tc_fence_before();

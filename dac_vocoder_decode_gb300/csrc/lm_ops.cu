@@ -191,45 +191,45 @@ int row_threads(int sms, long long rows, int d, int chunk) {
   return t;
 }
 
-template <typename T, int MODE, int VB, int CH>
+template <typename T, int MODE, int VB, int CH, bool ANY>
 cudaError_t launch_rows_ch(int tpr, const voc::LmRowsArgs &a, voc_stream_t stream) {
   const int threads = std::max(128, tpr);
   const long long per = threads / tpr;
-  return launch(voc::rows_kernel<T, MODE, VB, CH>,
+  return launch(voc::rows_kernel<T, MODE, VB, CH, ANY>,
                 dim3(static_cast<unsigned>((a.rows + per - 1) / per)), dim3(threads), 0, 1, stream,
                 a, tpr);
 }
 
-// As many vectors per thread as the row needs: in quarters of kRowValues values.
-template <typename T, int MODE, int VB>
-cudaError_t launch_rows_vec(int sms, const voc::LmRowsArgs &a, voc_stream_t stream) {
+// As many vectors per thread as the row needs: in quarters of kRowValues values.  `d`: values that the
+// vectors have to cover.
+template <typename T, int MODE, int VB, bool ANY>
+cudaError_t launch_rows_vec(int sms, int d, const voc::LmRowsArgs &a, voc_stream_t stream) {
   constexpr int n = VB / static_cast<int>(sizeof(T)), most = voc::kRowValues / n;
-  const int tpr = row_threads(sms, a.rows, a.d, n);
-  const int need = (a.d + n * tpr - 1) / (n * tpr);
-  if (4 * need <= most) return launch_rows_ch<T, MODE, VB, most / 4>(tpr, a, stream);
-  if (2 * need <= most) return launch_rows_ch<T, MODE, VB, most / 2>(tpr, a, stream);
-  if (4 * need <= 3 * most) return launch_rows_ch<T, MODE, VB, 3 * most / 4>(tpr, a, stream);
-  return launch_rows_ch<T, MODE, VB, most>(tpr, a, stream);
+  const int tpr = row_threads(sms, a.rows, d, n);
+  const int need = (d + n * tpr - 1) / (n * tpr);
+  if (4 * need <= most) return launch_rows_ch<T, MODE, VB, most / 4, ANY>(tpr, a, stream);
+  if (2 * need <= most) return launch_rows_ch<T, MODE, VB, most / 2, ANY>(tpr, a, stream);
+  if (4 * need <= 3 * most) return launch_rows_ch<T, MODE, VB, 3 * most / 4, ANY>(tpr, a, stream);
+  return launch_rows_ch<T, MODE, VB, most, ANY>(tpr, a, stream);
 }
 
-// The widest access that the width, the strides and the buffers allow.
+// The widest access that the width, the strides and the buffers allow in every row; below 8 bytes each
+// row and buffer by its own.
 template <typename T, int MODE>
 cudaError_t launch_rows(int sms, const voc::LmRowsArgs &a, voc_stream_t stream) {
-  if (a.d > voc::kRowThreads * voc::kRowValues)
-    return launch(voc::rows_any_kernel<T, MODE>, dim3(static_cast<unsigned>(a.rows)),
-                  dim3(voc::kAnyThreads), 0, 1, stream, a);
-  const size_t e = sizeof(T);
+  constexpr int most = voc::kRowThreads * voc::kRowValues;
+  constexpr int lead = 16 / static_cast<int>(sizeof(T)) - 1;  // places before a row's first value
   auto fits = [&](size_t vb) {  // rows start on vb bytes, codes on as many values
-    const long long n = static_cast<long long>(vb / e);
-    return a.d % n == 0 && a.ldx % n == 0 && (!a.res || a.ldr % n == 0) &&
+    const long long n = static_cast<long long>(vb / sizeof(T));
+    return a.d <= most && a.d % n == 0 && a.ldx % n == 0 && (!a.res || a.ldr % n == 0) &&
            (!a.sum || a.lds % n == 0) && a.ldo % n == 0 && aligned(a.x, vb) &&
            aligned(a.res, vb) && aligned(a.sum, vb) && aligned(a.w, vb) && aligned(a.out, n);
   };
-  if (fits(16)) return launch_rows_vec<T, MODE, 16>(sms, a, stream);
-  if (fits(8)) return launch_rows_vec<T, MODE, 8>(sms, a, stream);
-  if constexpr (sizeof(T) == 2)
-    if (!fits(4)) return launch_rows_vec<T, MODE, 2>(sms, a, stream);
-  return launch_rows_vec<T, MODE, 4>(sms, a, stream);
+  if (fits(16)) return launch_rows_vec<T, MODE, 16, false>(sms, a.d, a, stream);
+  if (fits(8)) return launch_rows_vec<T, MODE, 8, false>(sms, a.d, a, stream);
+  if (a.d + lead <= most) return launch_rows_vec<T, MODE, 16, true>(sms, a.d + lead, a, stream);
+  return launch(voc::rows_any_kernel<T, MODE>, dim3(static_cast<unsigned>(a.rows)),
+                dim3(voc::kAnyThreads), 0, 1, stream, a);
 }
 
 template <int MODE>
@@ -511,20 +511,26 @@ constexpr int kShareGain = 20;
 struct AttnPlan {
   bool prompt = false;
   int tile = 8;       // rows of a tile of the row kernel
-  int row_tiles = 0;  // of `tile` rows, or for the prompt kernel's partial outputs of 16 rows
+  int row_tiles = 0;  // of a sequence, at the kernel's own tile size
+  int flat_tiles = 0; // prompt kernel: tiles of all sequences, or 0: row_tiles for each
   int splits = 1;     // prompt kernel: parts of the keys
   int ctas = 0;       // row kernel: CTAs that share the work; 0: a CTA has whole tiles
   size_t slots = 0;   // partial rows in the workspace
   size_t ws_bytes = 0;
 };
 
+// Partial rows in the workspace: a channel's sum each, the maximum and the sum of the weights.
+size_t part_bytes(size_t slots, int head_dim) { return slots * (head_dim * sizeof(float) + 8); }
+
 // Row kernel: a CTA per tile, or equal shares for two CTAs per SM (kShareGain).  Prompt kernel: keys
 // are split while there are fewer tiles than SMs, into parts of 4 blocks or more, and no more than
 // 1.5 sqrt(blocks) of them, beyond which the parts' join costs what the shorter parts save.  Measured,
 // 256 rows x 4 heads, 1000 tokens: parts of 16 blocks 25.3, 8 22.7, 4 19.2 us; 8000 tokens: 7 parts
 // 32.9, 17 24.2, 31 26.6 us.
-AttnPlan plan_attention(int sms, int n_seq, int max_q, int heads, int kv_heads, int head_dim,
-                        int max_kv, int window) {
+// Its CTAs look for their tiles, which n_tokens bounds, so that sequences with few new tokens cost
+// none (flat_tiles); splits grow as n_tokens falls, and parts are never more than one per SM.
+AttnPlan plan_attention(int sms, int n_seq, long long n_tokens, int max_q, int heads, int kv_heads,
+                        int head_dim, int max_kv, int window) {
   AttnPlan p;
   const long long rows = static_cast<long long>(heads / kv_heads) * max_q;
   const long long heads_all = static_cast<long long>(n_seq) * kv_heads;
@@ -535,49 +541,54 @@ AttnPlan plan_attention(int sms, int n_seq, int max_q, int heads, int kv_heads, 
   const long long row_tiles = (rows + p.tile - 1) / p.tile, tiles = heads_all * row_tiles;
   p.prompt = rows >= kPromptRows && !(blocks <= kShortBlocks && tiles <= slots);
   if (p.prompt) {
-    p.row_tiles = static_cast<int>((rows + voc::kPartRows - 1) / voc::kPartRows);
-    const long long ctas = heads_all * ((rows + voc::kPrRows - 1) / voc::kPrRows);
-    const long long fits = std::min({ctas >= sms ? 1 : sms / ctas, blocks / 4, 65535ll / n_seq});
-    while (p.splits < fits && 4ll * (p.splits + 1) * (p.splits + 1) <= 9 * blocks) ++p.splits;
-    if (p.splits > 1)
-      p.slots = static_cast<size_t>(heads_all) * p.row_tiles * p.splits * voc::kPartRows;
+    p.row_tiles = static_cast<int>((rows + voc::kPrRows - 1) / voc::kPrRows);
+    long long all = static_cast<long long>(n_seq) * p.row_tiles;
+    if (n_seq <= voc::kFlatTiles) {
+      all = std::min(all, n_tokens * (heads / kv_heads) / voc::kPrRows + n_seq);
+      p.flat_tiles = static_cast<int>(all);
+      const long long fits = blocks > kShortBlocks ? std::min(sms / (all * kv_heads), blocks / 4) : 1;
+      while (p.splits < fits && 4ll * (p.splits + 1) * (p.splits + 1) <= 9 * blocks) ++p.splits;
+      if (p.splits > 1)
+        p.slots = static_cast<size_t>(all) * kv_heads * p.splits * voc::kPrRows;
+    }
   } else {
     p.row_tiles = static_cast<int>(row_tiles);
     const long long units = tiles * (blocks + voc::kTileCost);
-    const long long alone = (tiles + slots - 1) / slots * (blocks + voc::kTileCost);  // the busiest CTA's
+    const long long alone =  // the busiest CTA's units
+        (tiles + slots - 1) / slots * (blocks + voc::kTileCost);
     const long long shared = std::max<long long>((units + slots - 1) / slots, voc::kShareMin);
     if (n_seq <= voc::kShareSeqs && alone >= shared + kShareGain && units < (1ll << 30)) {
       p.ctas = static_cast<int>(std::min(slots, (units + voc::kShareMin - 1) / voc::kShareMin));
       p.slots = 2ull * p.ctas * p.tile;
     }
   }
-  p.ws_bytes = p.slots * (static_cast<size_t>(head_dim) * 4 + 8);
+  p.ws_bytes = part_bytes(p.slots, head_dim);
   return p;
 }
 
 template <typename T, int D, int NT>
-cudaError_t launch_rows_attention(const voc::LmAttnArgs &a, voc_stream_t stream) {
-  const dim3 grid = a.ctas ? dim3(a.ctas) : dim3(a.row_tiles, a.kv_heads, a.n_seq);
+cudaError_t launch_rows_attention(const voc::LmAttnArgs &a, int row_tiles, voc_stream_t stream) {
+  const dim3 grid = a.ctas ? dim3(a.ctas) : dim3(row_tiles, a.kv_heads, a.n_seq);
   cudaError_t e = launch(voc::attn_rows_kernel<T, D, NT>, grid, dim3(voc::kAttnThreads),
                          voc::attn_smem<D, NT>(), 1, stream, a);
   if (e != cudaSuccess || !a.ctas) return e;
-  return launch(voc::attn_join_kernel<T, D, 8 * NT, true>,
+  return launch(voc::attn_join_kernel<T, D, 8 * NT>,
                 dim3(a.group * a.max_q, a.kv_heads, a.n_seq), dim3(D), 0, 1, stream, a);
 }
 
 template <typename T, int D>
 cudaError_t launch_attention(const voc::LmAttnArgs &a, const AttnPlan &plan, voc_stream_t stream) {
   if (!plan.prompt)
-    return plan.tile == 8 ? launch_rows_attention<T, D, 1>(a, stream)
-                          : launch_rows_attention<T, D, 2>(a, stream);
-  const int rows = a.group * a.max_q;
-  cudaError_t e =
-      launch(voc::attn_prompt_kernel<T, D>,
-             dim3((rows + voc::kPrRows - 1) / voc::kPrRows, a.kv_heads, a.n_seq * a.splits),
-             dim3(voc::kPrThreads), voc::PromptSmem<D>::kBytes, 1, stream, a);
+    return plan.tile == 8 ? launch_rows_attention<T, D, 1>(a, plan.row_tiles, stream)
+                          : launch_rows_attention<T, D, 2>(a, plan.row_tiles, stream);
+  const dim3 grid = a.flat ? dim3(plan.flat_tiles, a.kv_heads, a.splits)
+                           : dim3(plan.row_tiles, a.kv_heads, a.n_seq);
+  cudaError_t e = launch(voc::attn_prompt_kernel<T, D>, grid, dim3(voc::kPrThreads),
+                         voc::PromptSmem<D>::kBytes, 1, stream, a);
   if (e != cudaSuccess || a.splits == 1) return e;
-  return launch(voc::attn_join_kernel<T, D, voc::kPartRows, false>,
-                dim3(rows, a.kv_heads, a.n_seq), dim3(D), 0, 1, stream, a);
+  return launch(voc::attn_join_tiles_kernel<T, D>,
+                dim3(plan.flat_tiles, a.kv_heads, voc::kPrRows / voc::kJoinRows),
+                dim3(32 * voc::kJoinRows), 0, 1, stream, a);
 }
 
 }  // namespace
@@ -589,7 +600,10 @@ VOC_API size_t vocoder_lm_attention_ws_bytes(int n_seq, int max_q, int heads, in
     return 0;
   Device *dev;
   if (device(&dev) != VOC_OK) return 0;
-  return plan_attention(dev->sms, n_seq, max_q, heads, kv_heads, head_dim, max_kv, window).ws_bytes;
+  // the number of tokens is not known here: the fewest, which have the most parts, stand for any
+  const AttnPlan p =
+      plan_attention(dev->sms, n_seq, max_q, max_q, heads, kv_heads, head_dim, max_kv, window);
+  return p.splits > 1 ? part_bytes(static_cast<size_t>(dev->sms) * voc::kPrRows, head_dim) : p.ws_bytes;
 }
 
 VOC_API voc_status vocoder_lm_attention(
@@ -619,7 +633,7 @@ VOC_API voc_status vocoder_lm_attention(
   if (voc_status st = device(&dev); st != VOC_OK) return st;
   if (n_tokens == 0 || max_q == 0) return finish(*dev, stream, flags);
   AttnPlan plan =
-      plan_attention(dev->sms, n_seq, max_q, heads, kv_heads, head_dim, max_kv, window);
+      plan_attention(dev->sms, n_seq, n_tokens, max_q, heads, kv_heads, head_dim, max_kv, window);
   // lengths are on the device and may exceed max_kv: what the page table can hold bounds them
   if (static_cast<double>(n_seq) * kv_heads * plan.row_tiles * (table_cols + 1.0 + voc::kTileCost) >= 0x1p30)
     plan.ctas = 0;
@@ -635,7 +649,7 @@ VOC_API voc_status vocoder_lm_attention(
   a.n_seq = n_seq, a.n_tokens = n_tokens, a.max_q = max_q;
   a.scale_log2 = softmax_scale * 1.44269504f;
   a.causal = causal, a.window = window;
-  a.row_tiles = plan.row_tiles, a.splits = plan.splits, a.ctas = plan.ctas;
+  a.splits = plan.splits, a.flat = plan.flat_tiles, a.ctas = plan.ctas;
   if (plan.slots) {
     a.part_o = static_cast<float *>(ws);
     a.part_ml = reinterpret_cast<float2 *>(a.part_o + plan.slots * head_dim);

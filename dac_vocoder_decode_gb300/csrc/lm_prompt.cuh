@@ -36,9 +36,7 @@
 namespace voc {
 
 constexpr int kPrThreads = 512;
-constexpr int kPrRows = 256;       // rows of a CTA
 constexpr int kPrStages = 4;       // key tiles in shared memory
-constexpr int kPartRows = 16;      // rows of a tile of partial outputs
 // Registers: 256 softmax threads, 128 converting, 128 others: 256 x 184 + 128 x 104 + 128 x 40 =
 // 65536, the block's registers at launch (512 x 128).
 constexpr int kPrSoftRegs = 184, kPrConvRegs = 104, kPrRestRegs = 40;
@@ -88,14 +86,19 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
   volatile int *abort = &abort_flag;
   const int never = 0;
 
-  const int b = blockIdx.z / p.splits, split = blockIdx.z % p.splits, hk = blockIdx.y;
+  const int hk = blockIdx.y;
+  int b = blockIdx.z, split = 0, nth = blockIdx.x;  // nth: which of the sequence's tiles
   pdl_wait();
+  if (p.flat) {
+    split = blockIdx.z;
+    b = find_tile(p, blockIdx.x, lane, nth);  // no CTAs for tiles that short chunks do not have
+    if (b < 0) return;  // the whole block, before any barrier or allocation
+  }
   const SeqSpan span = seq_span(p.cu, b, p.n_seq, p.n_tokens, p.max_q);
   const int rows = span.count * p.group;
   // the latest rows see the most keys: they start first
-  const int tile_max = static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x);
-  const int r0 = tile_max * kPrRows;
-  if (r0 >= rows) return;  // the whole block, before any barrier or allocation
+  const int r0 = (prompt_tiles(p, span) - 1 - nth) * kPrRows;
+  if (r0 < 0) return;  // likewise
   const int r_last = min(rows, r0 + kPrRows) - 1;
   const bool two = r_last - r0 >= 128;  // the second row tile has rows
   if (tid == 0) {
@@ -328,9 +331,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) attn_prompt_kernel(const LmAttn
       const float inv = l == 0.f ? 0.f : 1.f / l;
       T *dst = static_cast<T *>(p.out) + (span.first + tok) * p.ldo + head * p.hso;
       const bool vec = (reinterpret_cast<uintptr_t>(dst) & 15) == 0;
-      const long long tile16 =
-          (static_cast<long long>(b) * p.kv_heads + hk) * p.row_tiles + r / kPartRows;
-      const long long at = (tile16 * p.splits + split) * kPartRows + r % kPartRows;
+      // the parts of a tile: [tile, its sequence's first one first][head][split][row]
+      const long long tile = static_cast<long long>(blockIdx.x) - nth + r0 / kPrRows;
+      const long long at = ((tile * p.kv_heads + hk) * p.splits + split) * kPrRows + r - r0;
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {

@@ -65,7 +65,7 @@ __device__ __forceinline__ float2 row_scale(uint32_t amax) {
 
 constexpr int kRowValues = 32;    // values of a row that a thread keeps in registers
 constexpr int kAnyThreads = 256;  // threads of a row of any width
-constexpr int kRowThreads = 512;  // most threads of a row: rows of up to 16384 values
+constexpr int kRowThreads = 512;  // most threads of a row that is kept in registers: 16384 values
 
 // Sum, or maximum of magnitudes as bits (NaN kept), over a row's `tpr` threads (a power of two from 32 on);
 // `red` has a float per warp.  The order is fixed.
@@ -95,7 +95,7 @@ __device__ __forceinline__ uint32_t row_max(uint32_t bits, int tpr, float *red) 
   return v;
 }
 
-// Rows of more than 16384 values, any stride and alignment: one CTA per row, the row read once per
+// Rows of more than 16384 values (less a vector, unaligned), any stride and alignment: one CTA per row, the row read once per
 // pass (the later passes from cache), a value at a time.  Bound by its dependent loads: 512 x 20000
 // bf16 with norm and residual 65 us (1.1 TB/s), gated 31 us.
 template <typename T, int MODE>
@@ -150,74 +150,114 @@ __global__ void __launch_bounds__(kAnyThreads) rows_any_kernel(const LmRowsArgs 
   }
 }
 
-// Loads and stores of VB bytes of T (N values).
+// Loads and stores of VB bytes of T (N values), 16 or 8.
 template <typename T, int VB>
 struct RowVec {
   static constexpr int N = VB / static_cast<int>(sizeof(T));
-  static constexpr int kWords = VB >= 4 ? VB / 4 : 1;
-  static __device__ __forceinline__ void load_raw(const T *p, uint32_t (&w)[kWords]) {
+  static constexpr int kWords = VB / 4;
+  using Words = uint32_t[kWords];
+  static __device__ __forceinline__ void load(const T *p, Words &w) {
     if constexpr (VB == 16) {
       const uint4 u = *reinterpret_cast<const uint4 *>(p);
       w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-    } else if constexpr (VB == 8) {
+    } else {
       const uint2 u = *reinterpret_cast<const uint2 *>(p);
       w[0] = u.x, w[1] = u.y;
-    } else if constexpr (VB == 4) {
-      w[0] = *reinterpret_cast<const uint32_t *>(p);
-    } else {
-      w[0] = *reinterpret_cast<const uint16_t *>(p);
     }
   }
-  static __device__ __forceinline__ void unpack(const uint32_t (&w)[kWords], float (&f)[N]) {
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int j = 0; j < N; ++j) f[j] = __uint_as_float(w[j]);
-    } else if constexpr (N == 1) {
-      float unused;
-      unpack2<T>(w[0], f[0], unused);
-    } else {
-#pragma unroll
-      for (int j = 0; j < kWords; ++j) unpack2<T>(w[j], f[2 * j], f[2 * j + 1]);
-    }
+  static __device__ __forceinline__ void store(T *p, const Words &w) {
+    if constexpr (VB == 16)
+      *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else
+      *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
   }
-  static __device__ __forceinline__ void load(const T *p, float (&f)[N]) {
-    uint32_t w[kWords];
-    load_raw(p, w);
-    unpack(w, f);
-  }
-  static __device__ __forceinline__ void store(T *p, const float (&f)[N]) {
-    if constexpr (N == 1) {
-      *p = from_f32<T>(f[0]);
-    } else {
-      uint32_t w[kWords];
+  static __device__ __forceinline__ void unpack(const Words &w, float (&f)[N]) {
 #pragma unroll
-      for (int j = 0; j < kWords; ++j) {
-        if constexpr (sizeof(T) == 4)
-          w[j] = __float_as_uint(f[j]);
-        else
-          w[j] = pack2<T>(f[2 * j], f[2 * j + 1]);
-      }
-      if constexpr (VB == 16)
-        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-      else if constexpr (VB == 8)
-        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    for (int j = 0; j < kWords; ++j) {
+      if constexpr (sizeof(T) == 4)
+        f[j] = __uint_as_float(w[j]);
       else
-        *reinterpret_cast<uint32_t *>(p) = w[0];
+        unpack2<T>(w[j], f[2 * j], f[2 * j + 1]);
+    }
+  }
+  static __device__ __forceinline__ void pack(const float (&f)[N], Words &w) {
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) {
+      if constexpr (sizeof(T) == 4)
+        w[j] = __float_as_uint(f[j]);
+      else
+        w[j] = pack2<T>(f[2 * j], f[2 * j + 1]);
+    }
+  }
+  // The same from and to any place of T's alignment: whole words where they are, and 16-bit values at
+  // the ends of a stretch that starts between two.
+  static __device__ __forceinline__ void load_any(const T *p, Words &w) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    if (at % VB == 0) {
+      load(p, w);
+    } else if (at % 4 == 0) {
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) w[j] = reinterpret_cast<const uint32_t *>(p)[j];
+    } else {
+      const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+      uint32_t mid[kWords - 1];
+#pragma unroll
+      for (int j = 0; j < kWords - 1; ++j) mid[j] = *reinterpret_cast<const uint32_t *>(h + 1 + 2 * j);
+      const uint32_t first = h[0], last = h[2 * kWords - 1];
+      w[0] = first | mid[0] << 16;
+#pragma unroll
+      for (int j = 1; j < kWords - 1; ++j) w[j] = __funnelshift_r(mid[j - 1], mid[j], 16);
+      w[kWords - 1] = mid[kWords - 2] >> 16 | last << 16;
+    }
+  }
+  static __device__ __forceinline__ void store_any(T *p, const Words &w) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    if (at % VB == 0) {
+      store(p, w);
+    } else if (at % 4 == 0) {
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) reinterpret_cast<uint32_t *>(p)[j] = w[j];
+    } else {
+      uint16_t *h = reinterpret_cast<uint16_t *>(p);
+      h[0] = static_cast<uint16_t>(w[0]);
+#pragma unroll
+      for (int j = 0; j < kWords - 1; ++j)
+        *reinterpret_cast<uint32_t *>(h + 1 + 2 * j) = __funnelshift_r(w[j], w[j + 1], 16);
+      h[2 * kWords - 1] = static_cast<uint16_t>(w[kWords - 1] >> 16);
+    }
+  }
+  // Those of the values that lie in [0, d), the first of them at row[e0]; zeros for the others.
+  static __device__ __forceinline__ void load_part(const T *row, int e0, int d, Words &w) {
+    constexpr int kPer = 4 / static_cast<int>(sizeof(T));
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      uint32_t v = 0;
+      if (e0 + j >= 0 && e0 + j < d) {
+        if constexpr (kPer == 1)
+          v = reinterpret_cast<const uint32_t *>(row)[e0 + j];
+        else
+          v = reinterpret_cast<const uint16_t *>(row)[e0 + j];
+      }
+      w[j / kPer] = j % kPer ? w[j / kPer] | v << 16 : v;
     }
   }
 };
 
 // Rows of up to 16384 values, each read once and kept in registers by its `tpr` threads, CH
-// vectors of VB bytes each.  VB is the widest access that the row's buffers and strides allow.
+// vectors of VB bytes each.  VB is the widest access that the row's buffers and strides allow, 16 or 8.
 // With d values a row moves 7 d bytes (16-bit, residual), and the kernel has to spend few
 // instructions on a value to keep up with that: conversions two at a time, and magnitudes before
 // the norm are looked at only where the sum of squares says that squares overflowed or vanished.
+// ANY: rows of any alignment (odd widths).  The vectors lie on the codes' 8-byte grid (4 for f32), each
+// buffer is read and written at them in the widest accesses of its own alignment, and the first and
+// the last vector, where the row covers them only in part, value by value.
 // Measured (bf16, residual): 15504 x 1536 27.8 us, 6.0 TB/s, where a plain copy reaches 6.8 (one value
-// at a time it was 46.5 us); 2000 x 16384 40 us, 5.7 TB/s; 8 x 1024 2.2 us, a launch and a chain of two
+// at a time it was 46.5 us); 15504 x 1537 TODO us (in the accesses that every row allows, 2 bytes, 137),
+// 1538 TODO (4 bytes: 51); 2000 x 16384 40 us, 5.7 TB/s; 8 x 1024 2.2 us, a launch and a chain of two
 // loads and two reductions.  Gated 4001 x 4100 f16: 20.1 us, 4.1 TB/s: 8-byte accesses (the rows'
 // second halves start on 8 bytes) and rows of one load, one reduction and one store, whose chain the
 // few resident rows cover only in part.
-template <typename T, int MODE, int VB, int CH>
+template <typename T, int MODE, int VB, int CH, bool ANY>
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LmRowsArgs p, const int tpr) {
   using Vec = RowVec<T, VB>;
   constexpr int N = Vec::N;
@@ -228,20 +268,33 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LmRowsArgs p, c
   const long long row =
       static_cast<long long>(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
   const bool live = row < p.rows;  // spare threads of the last block keep to the barriers
-  const int chunks = live ? p.d / N : 0;
   const T *x = static_cast<const T *>(p.x) + row * p.ldx;
+  const T *w = static_cast<const T *>(p.w);
+  uint8_t *out = p.out + row * p.ldo;
+  const int lead = ANY ? static_cast<int>(reinterpret_cast<uintptr_t>(out) % N) : 0;
+  const int chunks = live ? (p.d + lead + (ANY ? N - 1 : 0)) / N : 0;
+  auto whole = [&](int c) { return !ANY || (c * N >= lead && (c + 1) * N <= p.d + lead); };
+  auto load = [&](const T *from, int c, typename Vec::Words &v) {  // vector c of a row
+    const int e0 = c * N - lead;
+    if (!whole(c))
+      Vec::load_part(from, e0, p.d, v);
+    else if (ANY)
+      Vec::load_any(from + e0, v);
+    else
+      Vec::load(from + e0, v);
+  };
   float h[CH][N];
   if (MODE == kRowsGated || p.res) {
     const T *r = MODE == kRowsGated ? x + p.d : static_cast<const T *>(p.res) + row * p.ldr;
-    uint32_t a[CH][Vec::kWords], b[CH][Vec::kWords];
+    typename Vec::Words a[CH], b[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = lane + i * tpr;
 #pragma unroll
       for (int j = 0; j < Vec::kWords; ++j) a[i][j] = b[i][j] = 0;
       if (c < chunks) {
-        Vec::load_raw(x + c * N, a[i]);
-        Vec::load_raw(r + c * N, b[i]);
+        load(x, c, a[i]);
+        load(r, c, b[i]);
       }
     }
 #pragma unroll
@@ -261,18 +314,30 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LmRowsArgs p, c
       T *s = static_cast<T *>(p.sum) + row * p.lds;
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const int c = lane + i * tpr;
-        if (c < chunks) Vec::store(s + c * N, h[i]);
+        const int c = lane + i * tpr, e0 = c * N - lead;
+        if (c >= chunks) continue;
+        if (whole(c)) {
+          typename Vec::Words v;
+          Vec::pack(h[i], v);
+          if (ANY)
+            Vec::store_any(s + e0, v);
+          else
+            Vec::store(s + e0, v);
+        } else {
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            if (e0 + j >= 0 && e0 + j < p.d) s[e0 + j] = from_f32<T>(h[i][j]);
+        }
       }
     }
   } else {
-    uint32_t a[CH][Vec::kWords];
+    typename Vec::Words a[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = lane + i * tpr;
 #pragma unroll
       for (int j = 0; j < Vec::kWords; ++j) a[i][j] = 0;
-      if (c < chunks) Vec::load_raw(x + c * N, a[i]);
+      if (c < chunks) load(x, c, a[i]);
     }
 #pragma unroll
     for (int i = 0; i < CH; ++i) Vec::unpack(a[i], h[i]);
@@ -310,8 +375,10 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LmRowsArgs p, c
     for (int i = 0; i < CH; ++i) {
       const int c = lane + i * tpr;
       if (c < chunks) {
+        typename Vec::Words v;
         float u[N];
-        Vec::load(static_cast<const T *>(p.w) + c * N, u);
+        load(w, c, v);
+        Vec::unpack(v, u);
 #pragma unroll
         for (int j = 0; j < N; ++j) h[i][j] = h[i][j] * rs * u[j];
       }
@@ -324,27 +391,26 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LmRowsArgs p, c
     for (int j = 0; j < N; ++j) m = max_abs(m, h[i][j]);
   const float2 sc = row_scale(row_max(abs_bits(m), tpr, red));
   if (live && lane == 0) p.scale[row] = sc.x;
-  uint8_t *out = p.out + row * p.ldo;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int c = lane + i * tpr;
-    if (c < chunks) {
-      if constexpr (N == 1) {
-        out[c] = e4m3(h[i][0] * sc.y);
-      } else {
-        uint32_t q[(N + 3) / 4];
+    const int c = lane + i * tpr, e0 = c * N - lead;
+    if (c >= chunks) continue;
+    uint32_t q[(N + 3) / 4];
 #pragma unroll
-        for (int j = 0; j < N; j += 2) {
-          const uint32_t two = e4m3x2(h[i][j] * sc.y, h[i][j + 1] * sc.y);
-          q[j / 4] = j % 4 ? q[j / 4] | two << 16 : two;
-        }
-        if constexpr (N == 8)
-          *reinterpret_cast<uint2 *>(out + c * N) = make_uint2(q[0], q[1]);
-        else if constexpr (N == 4)
-          *reinterpret_cast<uint32_t *>(out + c * N) = q[0];
-        else
-          *reinterpret_cast<uint16_t *>(out + c * N) = static_cast<uint16_t>(q[0]);
-      }
+    for (int j = 0; j < N; j += 2) {
+      const uint32_t two = e4m3x2(h[i][j] * sc.y, h[i][j + 1] * sc.y);
+      q[j / 4] = j % 4 ? q[j / 4] | two << 16 : two;
+    }
+    if (!whole(c)) {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (e0 + j >= 0 && e0 + j < p.d) out[e0 + j] = static_cast<uint8_t>(q[j / 4] >> 8 * (j % 4));
+    } else if constexpr (N == 8) {
+      *reinterpret_cast<uint2 *>(out + e0) = make_uint2(q[0], q[1]);
+    } else if constexpr (N == 4) {
+      *reinterpret_cast<uint32_t *>(out + e0) = q[0];
+    } else {
+      *reinterpret_cast<uint16_t *>(out + e0) = static_cast<uint16_t>(q[0]);
     }
   }
 }

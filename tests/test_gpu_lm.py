@@ -525,6 +525,110 @@ def test_attention_far_offsets():
     assert torch.equal(big.v.view(torch.uint8)[idx], bt.cache.v.view(torch.uint8))
 
 
+RAGGED = [[1, 40, 3000, 0, 64, 17, 1500, 700], [2900, 1], [5, 5, 5, 2048], [1, 0, 2, 4100]]
+
+
+@pytest.mark.parametrize("d,heads,kv_heads", [(64, 8, 8), (128, 7, 1), (128, 20, 2), (64, 1, 1)])
+@pytest.mark.parametrize("lens", RAGGED)
+def test_attention_shares_of_ragged_lengths(d, heads, kv_heads, lens):
+    """Long and short sequences side by side: CTAs whose share ends inside a tile, before its first
+    block, or holds many tiles; tiles in more than 32 parts."""
+    bt = Batch(lens, [1] * len(lens), kv_heads, d, seed=3)
+    q = _queries(bt, heads)
+    _check_attention(bt, q, max_kv=16000)
+    if len(lens) > 2:
+        bt.table[2, 0] = -1  # and a page that holds no tokens
+        bt.t_table = torch.from_numpy(bt.table).cuda()
+        _check_attention(bt, q, max_kv=16000)
+
+
+MANY = [([333], [333]), ([200, 130, 700], [200, 1, 150]), ([0, 520], [9, 300])]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d,heads,kv_heads", [(64, 16, 16), (128, 16, 16), (64, 32, 16)])
+@pytest.mark.parametrize("lens,new", MANY)
+def test_attention_many_rows_and_heads(dtype, d, heads, kv_heads, lens, new):
+    bt = Batch(lens, new, kv_heads, d, seed=lens[0])
+    _check_attention(bt, _queries(bt, heads, dtype))
+
+
+@pytest.mark.parametrize("n_seq", [600])
+def test_attention_many_sequences(n_seq):
+    """More sequences than CTAs count through; a tile or two for each."""
+    lens = [40 + i % 50 for i in range(n_seq)]
+    new = [min(n, 36 + i % 3) for i, n in enumerate(lens)]
+    bt = Batch(lens, new, 1, 64, seed=1)
+    _check_attention(bt, _queries(bt, 1))
+
+
+@pytest.fixture
+def long_announced(monkeypatch):
+    """Announces every length as 4000: more than 32 rows then take tiles of 256 rows, their keys in
+    parts, and fewer rows shares."""
+    real = V.attention_fp8
+    monkeypatch.setattr(V, "attention_fp8",
+                        lambda *a, max_kv=None, **kw: real(*a, max_kv=max_kv or 4000, **kw))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d,heads,kv_heads", [(64, 4, 2), (128, 4, 1), (128, 2, 2), (64, 7, 1)])
+@pytest.mark.parametrize("lens,new", CHUNKS + MANY)
+def test_attention_chunks_in_parts(long_announced, dtype, d, heads, kv_heads, lens, new):
+    test_attention_chunks(dtype, d, heads, kv_heads, lens, new)
+
+
+@pytest.mark.parametrize("window", [1, 2, 63, 64, 72, 250])
+@pytest.mark.parametrize("lens,new", [([300, 64, 1], [1, 1, 1]), ([333, 200], [200, 70]),
+                                      ([900], [129])])
+def test_attention_window_in_parts(long_announced, window, lens, new):
+    test_attention_window(window, lens, new)
+
+
+@pytest.mark.parametrize("case,args", [
+    (test_attention_not_causal, ([200, 130], [60, 130], 0)),
+    (test_attention_not_causal, ([200, 130], [60, 130], 100)),
+    (test_attention_rows_without_keys_are_zero, ([0, 200], [9, 150])),
+    (test_attention_rows_without_keys_are_zero, ([10, 300], [150, 150])),
+    (test_attention_missing_pages_hold_no_tokens, ()),
+    (test_attention_length_beyond_the_table, ()),
+    (test_attention_strided_queries_and_output, ([40, 170],)),
+    (test_attention_block_scales_far_apart, ([1, 130, 20],)),
+    (test_attention_query_magnitudes, ("bf16", 1e-4, [129, 64])),
+    (test_attention_query_magnitudes, ("f16", 20.0, [129, 64])),
+    (test_attention_nan_stays_with_who_sees_it, ([1, 1],)),
+    (test_attention_nan_stays_with_who_sees_it, ([150, 64],))],
+    ids=lambda v: v.__name__[5:] if callable(v) else "-".join(map(str, v)))
+def test_attention_in_parts(long_announced, case, args):
+    case(*args)
+
+
+def test_attention_workspace_holds_for_any_number_of_tokens():
+    """The size asked for without the number of tokens covers the fewest and the most."""
+    lib = V.load_library()
+    for new in ([200, 1, 1], [200, 200, 200], [1, 200, 90]):
+        bt = Batch([700, 650, 900], new, 2, 64, seed=2)
+        q = _queries(bt, 2)
+        need = lib.vocoder_lm_attention_ws_bytes(3, 200, 2, 2, 64, 4000, 0)
+        ws = torch.full((max(need, 16),), 0xff, dtype=torch.uint8, device="cuda")
+        _check_attention(bt, q, max_kv=4000, ws=ws)
+
+
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("n,at,ld", [(515, 0, 515), (514, 0, 514), (513, 1, 514), (512, 3, 520),
+                                     (500, 4, 504), (516, 2, 518)])
+def test_linear_output_rows_on_any_start(out, n, at, ld):
+    """Rows of every alignment from many tokens; what lies beside them stays."""
+    g = torch.Generator(device="cuda").manual_seed(n + at)
+    m, k = 4100, 64
+    x, w = _codes(g, m, k), _codes(g, n, k)
+    xs, ws = (torch.rand(r, generator=g, device="cuda") / 8 + 0.01 for r in (m, n))
+    buf = torch.full((m, ld), -7.0, dtype=TYPES[out], device="cuda")
+    V.linear_fp8(x, xs, w, ws, out=buf[:, at:at + n], flags=SYNC)
+    _check_linear(x, xs, w, ws, None, buf[:, at:at + n])
+    assert torch.all(buf[:, :at] == -7) and torch.all(buf[:, at + n:] == -7)
+
+
 # ------------------------------------------------------------------ streams and empties
 def test_empty_batches():
     bt = Batch([70], [1], 1, 64)
