@@ -685,7 +685,8 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const LmAttnArgs p) {
 // The sequence that the prompt kernel's tile `index` (counted over all sequences) is of, or -1, and
 // which of its tiles that is.  For whole warps.
 __device__ __forceinline__ int find_tile(const LmAttnArgs &p, int index, int lane, int &nth) {
-  for (int i0 = 0, before = 0; i0 < p.n_seq; i0 += 32) {
+  int b = -1;
+  for (int i0 = 0, before = 0; i0 < p.n_seq && b < 0; i0 += 32) {
     const int tiles =
         i0 + lane < p.n_seq
             ? prompt_tiles(p, seq_span(p.cu, i0 + lane, p.n_seq, p.n_tokens, p.max_q)) : 0;
@@ -698,12 +699,12 @@ __device__ __forceinline__ int find_tile(const LmAttnArgs &p, int index, int lan
     const uint32_t past = __ballot_sync(0xffffffffu, before + upto > index);
     if (past) {
       const int at = __ffs(past) - 1;
+      b = i0 + at;
       nth = index - before - __shfl_sync(0xffffffffu, upto - tiles, at);
-      return i0 + at;
     }
     before += __shfl_sync(0xffffffffu, upto, 31);
   }
-  return -1;
+  return b;
 }
 
 // Joins the parts of the prompt kernel's tiles, a warp per row.  One CTA per row of the longest chunk

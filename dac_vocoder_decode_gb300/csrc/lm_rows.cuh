@@ -95,8 +95,8 @@ __device__ __forceinline__ uint32_t row_max(uint32_t bits, int tpr, float *red) 
   return v;
 }
 
-// Rows of more than 16384 values (less a vector, unaligned), any stride and alignment: one CTA per row, the row read once per
-// pass (the later passes from cache), a value at a time.  Bound by its dependent loads: 512 x 20000
+// Rows of more than 16384 values (unaligned: less a vector), any stride and alignment: one CTA per row,
+// the row read once per pass (the later passes from cache), a value at a time.  Bound by its dependent loads: 512 x 20000
 // bf16 with norm and residual 65 us (1.1 TB/s), gated 31 us.
 template <typename T, int MODE>
 __global__ void __launch_bounds__(kAnyThreads) rows_any_kernel(const LmRowsArgs p) {
@@ -252,8 +252,8 @@ struct RowVec {
 // buffer is read and written at them in the widest accesses of its own alignment, and the first and
 // the last vector, where the row covers them only in part, value by value.
 // Measured (bf16, residual): 15504 x 1536 27.8 us, 6.0 TB/s, where a plain copy reaches 6.8 (one value
-// at a time it was 46.5 us); 15504 x 1537 TODO us (in the accesses that every row allows, 2 bytes, 137),
-// 1538 TODO (4 bytes: 51); 2000 x 16384 40 us, 5.7 TB/s; 8 x 1024 2.2 us, a launch and a chain of two
+// at a time it was 46.5 us); 15504 x 1537 57 us (in the accesses that every row allows, 2 bytes, 137),
+// 1538 40 (4 bytes: 51); 2000 x 16384 40 us, 5.7 TB/s; 8 x 1024 2.2 us, a launch and a chain of two
 // loads and two reductions.  Gated 4001 x 4100 f16: 20.1 us, 4.1 TB/s: 8-byte accesses (the rows'
 // second halves start on 8 bytes) and rows of one load, one reduction and one store, whose chain the
 // few resident rows cover only in part.
