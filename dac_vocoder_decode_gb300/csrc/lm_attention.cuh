@@ -20,7 +20,10 @@ constexpr int kShareSeqs = 512;   // sequences up to which CTAs take equal share
 constexpr int kPrRows = 256;      // rows of a tile of the prompt kernel
 constexpr int kFlatTiles = 512;   // sequences up to which its CTAs count through the tiles
 constexpr int kShareMin = 4;      // units of the smallest share
-constexpr int kTileCost = 8;      // units that a tile counts beside its blocks
+// Units that a tile counts beside its blocks, for what its first and last steps take.  Measured with 0,
+// 4, 8 and 16: 16 sequences of 1 to 10012 tokens 61.2, 23.5, 20.7 and 20.9 us, 8 of 4000 with 16 rows
+// 31.0, 28.7, 26.1 and 27.1.
+constexpr int kTileCost = 8;
 
 struct LmAttnArgs {
   const void *q;
@@ -157,9 +160,9 @@ struct Segment {
 // lengths, and a tile that several CTAs share is joined by attn_join_kernel.  Two CTAs per SM.
 //
 // Bound by the cache's bytes: 8 sequences of 15504 tokens, 8 key heads of 128 channels (254 MB), 4
-// queries a head: 47.9 us with the join, 5.3 TB/s; in its middle the kernel reads about 7, and some
-// 11 us are the launch, the first blocks' way in, CTAs that end at different times, and the join.  With
-// 16-row tiles the same call takes 59 us (twice the products and registers): 8 rows and fewer have
+// queries a head: 46 us with the join, 5.5 TB/s; in its middle the kernel reads about 7, and some
+// 9 us are the launch, the first blocks' way in, CTAs that end at different times, and the join.  With
+// 16-row tiles the same call took 59 us (twice the products and registers): 8 rows and fewer have
 // tiles of their own.  With the products the other way round and a fixed split of each tile it took
 // 76 us.  One sequence of 250 tokens: 4.2 us, latency.
 template <typename T, int D, int NT>

@@ -493,19 +493,20 @@ namespace {
 
 // From kPromptRows rows (queries that share a key head) of a sequence the attention runs on tiles of
 // 256 rows (prompt kernel), below on tiles of 8 or 16 (row kernel).  Measured, 8 sequences of 4000
-// tokens, 8 heads of 128 channels (us, row / prompt kernel): 16 rows 31.2 / 38.4, 32 rows 41.9 / 39.6,
-// 36 rows 51.9 / 40.1; 8 of 15504: 32 rows 108 / 126; one of 15504: 32 rows 29 / 22.
+// tokens, 8 heads of 128 channels (us, row / prompt kernel): 16 rows 25.8 / 39.1, 32 rows 39.0 / 40.1,
+// 36 rows 49.3 / 40.3; 8 of 15504: 32 rows 104 / 125, 36 rows 144 / 125; one of 15504: 32 rows 23.8 /
+// 25.2, 36 rows 28.0 / 25.4.
 // Up to kShortBlocks blocks of keys the row kernel takes more rows too, as long as all its tiles run at
 // once: the prompt kernel has about 10 us before its first and after its last product.  Measured, 256
-// rows x 4 heads: 500 tokens 7.3 / 13.3, 1000 tokens 10.0 / 13.4; 64 rows x 16 heads, 2000 tokens
-// (beyond the limit): 22.3 / 14.0.
+// rows x 4 heads of 128 channels: 500 tokens 10.7 / 19.8, 1000 tokens 15.1 / 20.0; 64 rows x 16 heads:
+// 1000 tokens 15.1 / 13.0, 2000 tokens (beyond the limit) 17.9 / 15.2.
 constexpr int kPromptRows = 33;
 constexpr int kShortBlocks = 16;
-// A tile of the row kernel is a CTA's, unless equal shares of all blocks spare the busiest CTA this
-// many: a share that starts inside a tile and the join of its parts cost about as much.  Measured (us,
-// whole tiles / shares), 128 tiles of 64 channels: 16 blocks 8.0 / 11.7, 32 blocks 13.3 / 14.1, 63
-// blocks 23.8 / 20.5; 16 tiles: 16 blocks 7.9 / 7.0, 32 blocks 12.8 / 7.2; 256 tiles of 128 channels,
-// 63 blocks 42.9 / 49.1.
+// A tile of the row kernel is a CTA's, unless equal shares of all units (kTileCost) spare the busiest
+// CTA this many: a share that starts inside a tile and the join of its parts cost about as much.
+// Measured (us, whole tiles / shares), 128 tiles of 64 channels: 16 blocks 7.9 / 10.7, 32 blocks 13.3 /
+// 13.2, 63 blocks 23.8 / 18.8; 16 tiles: 16 blocks 7.9 / 7.0, 32 blocks 12.8 / 7.5; 256 tiles of 128
+// channels: 16 blocks 15.8 / 21.5, 63 blocks 43.1 / 48.7; 16 sequences of 1 to 10012 tokens 65.5 / 20.7.
 constexpr int kShareGain = 20;
 
 struct AttnPlan {
@@ -522,11 +523,12 @@ struct AttnPlan {
 // Partial rows in the workspace: a channel's sum each, the maximum and the sum of the weights.
 size_t part_bytes(size_t slots, int head_dim) { return slots * (head_dim * sizeof(float) + 8); }
 
-// Row kernel: a CTA per tile, or equal shares for two CTAs per SM (kShareGain).  Prompt kernel: keys
-// are split while there are fewer tiles than SMs, into parts of 4 blocks or more, and no more than
+// Row kernel: a CTA per tile, or equal shares for two CTAs per SM (kShareGain).  Prompt kernel: long
+// keys are split while there are fewer tiles than SMs, into parts of 4 blocks or more, and no more than
 // 1.5 sqrt(blocks) of them, beyond which the parts' join costs what the shorter parts save.  Measured,
-// 256 rows x 4 heads, 1000 tokens: parts of 16 blocks 25.3, 8 22.7, 4 19.2 us; 8000 tokens: 7 parts
-// 32.9, 17 24.2, 31 26.6 us.
+// 256 rows x 4 heads: 1100 tokens whole 27.9, 2 parts 24.9, 4 parts 20.4 us; 8000 tokens whole 124, 15
+// parts 26.4, 17 25.6; 64 rows, 16000 tokens: 23 parts 21.8, 31 22.4; 8 chunks over a window of 250 (8
+// blocks): whole 15.0, 2 parts 18.0.
 // Its CTAs look for their tiles, which n_tokens bounds, so that sequences with few new tokens cost
 // none (flat_tiles); splits grow as n_tokens falls, and parts are never more than one per SM.
 AttnPlan plan_attention(int sms, int n_seq, long long n_tokens, int max_q, int heads, int kv_heads,
