@@ -257,9 +257,8 @@ struct RowVec {
 // Measured (bf16, residual): 15504 x 1536 27.8 us, 6.0 TB/s, where a plain copy reaches 6.8 (one value
 // at a time it was 46.5 us); 15504 x 1537 57 us (in the accesses that every row allows, 2 bytes, 137),
 // 1538 40 (4 bytes: 51); 2000 x 16384 40 us, 5.7 TB/s; 8 x 1024 2.2 us, a launch and a chain of two
-// loads and two reductions.  Gated 4001 x 4100 f16: 20.1 us, 4.1 TB/s: 8-byte accesses (the rows'
-// second halves start on 8 bytes) and rows of one load, one reduction and one store, whose chain the
-// few resident rows cover only in part.
+// loads and two reductions.  Gated 4001 x 4100 f16: 18.8 us, 4.4 TB/s: 8-byte accesses (the rows'
+// second halves start on 8 bytes), and instructions issue in three cycles of four.
 template <typename T, int MODE, int VB, int CH, bool ANY>
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LmRowsArgs p, const int tpr) {
   using Vec = RowVec<T, VB>;
