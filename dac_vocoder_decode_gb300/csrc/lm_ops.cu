@@ -505,7 +505,8 @@ namespace {
 // Up to kShortBlocks blocks of keys the row kernel takes more rows too, as long as all its tiles run at
 // once: the prompt kernel has about 10 us before its first and after its last product.  Measured, 256
 // rows x 4 heads of 128 channels: 500 tokens 10.7 / 19.8, 1000 tokens 15.1 / 20.0; 64 rows x 16 heads:
-// 1000 tokens 15.1 / 13.0, 2000 tokens (beyond the limit) 17.9 / 15.2.
+// 1000 tokens 15.1 / 13.0, 2000 tokens (beyond the limit) 17.9 / 15.2; tiles for two turns, 300 rows x
+// 8 heads, 4 queries each, 1000 tokens: 34.2 / 25.0.
 constexpr int kPromptRows = 33;
 constexpr int kShortBlocks = 16;
 // A tile of the row kernel is a CTA's, unless equal shares of all units (kTileCost) spare the busiest
@@ -547,7 +548,10 @@ AttnPlan plan_attention(int sms, int n_seq, long long n_tokens, int max_q, int h
   const long long blocks = keys / voc::kBlockTokens + 1, slots = 2ll * sms;
   p.tile = rows <= 8 ? 8 : 16;
   const long long row_tiles = (rows + p.tile - 1) / p.tile, tiles = heads_all * row_tiles;
-  p.prompt = rows >= kPromptRows && !(blocks <= kShortBlocks && tiles <= slots);
+  const long long live =  // tiles that have rows, at most
+      std::min(tiles, (n_tokens * (heads / kv_heads) / p.tile + n_seq) * kv_heads);
+  const bool brief = rows >= kPromptRows && blocks <= kShortBlocks && live <= slots;
+  p.prompt = rows >= kPromptRows && !brief;
   if (p.prompt) {
     p.row_tiles = static_cast<int>((rows + voc::kPrRows - 1) / voc::kPrRows);
     long long all = static_cast<long long>(n_seq) * p.row_tiles;
@@ -565,7 +569,7 @@ AttnPlan plan_attention(int sms, int n_seq, long long n_tokens, int max_q, int h
     const long long alone =  // the busiest CTA's units
         (tiles + slots - 1) / slots * (blocks + voc::kTileCost);
     const long long shared = std::max<long long>((units + slots - 1) / slots, voc::kShareMin);
-    if (n_seq <= voc::kShareSeqs && alone >= shared + kShareGain && units < (1ll << 30)) {
+    if (!brief && n_seq <= voc::kShareSeqs && alone >= shared + kShareGain && units < (1ll << 30)) {
       p.ctas = static_cast<int>(std::min(slots, (units + voc::kShareMin - 1) / voc::kShareMin));
       p.slots = 2ull * p.ctas * p.tile;
     }

@@ -258,7 +258,7 @@ struct RowVec {
 // at a time it was 46.5 us); 15504 x 1537 57 us (in the accesses that every row allows, 2 bytes, 137),
 // 1538 40 (4 bytes: 51); 2000 x 16384 40 us, 5.7 TB/s; 8 x 1024 2.2 us, a launch and a chain of two
 // loads and two reductions.  Gated 4001 x 4100 f16: 18.8 us, 4.4 TB/s: 8-byte accesses (the rows'
-// second halves start on 8 bytes), and instructions issue in three cycles of four.
+// second halves start on 8 bytes), instructions in two cycles of three, and 4 rows in flight on an SM.
 template <typename T, int MODE, int VB, int CH, bool ANY>
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LmRowsArgs p, const int tpr) {
   using Vec = RowVec<T, VB>;

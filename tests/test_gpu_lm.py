@@ -553,6 +553,16 @@ def test_attention_many_rows_and_heads(dtype, d, heads, kv_heads, lens, new):
     _check_attention(bt, _queries(bt, heads, dtype))
 
 
+@pytest.mark.parametrize("lens,new", [([900, 3, 70, 500], [200, 3, 40, 1]), ([1000], [700]),
+                                      ([600, 600], [33, 600])])
+@pytest.mark.parametrize("window", [0, 90])
+def test_attention_short_caches_with_many_rows(lens, new, window):
+    """Up to 16 blocks of keys: tiles of 16 rows while they all run at once, tiles of 256 beyond."""
+    for heads, kv_heads in ((4, 1), (16, 4), (12, 12)):
+        bt = Batch(lens, new, kv_heads, 64, seed=heads)
+        _check_attention(bt, _queries(bt, heads), window=window)
+
+
 @pytest.mark.parametrize("n_seq", [600])
 def test_attention_many_sequences(n_seq):
     """More sequences than CTAs count through; a tile or two for each."""
