@@ -385,8 +385,14 @@ VOC_API voc_status vocoder_lm_linear_fp8(const void *x8, long long ldx, const fl
     if (e != cudaSuccess) return cuda_fail(e, "launch linear");
     return finish(*dev, stream, flags);
   }
-  const int m_tiles = (M + 255) / 256;  // (few: fewer than 32 of 256 x 256)
-  a.nt = ((M + m_tiles - 1) / m_tiles + 15) / 16 * 16;  // equal tiles of up to 256 tokens
+  // Equal tiles of up to 256 tokens (few: fewer than 32 of 256 x 256), down to 32 as long as all their
+  // parts of K have SMs: a tile's way out grows with its tokens.  Measured (tokens x K x N, us, as large
+  // as they go / so): 444 x 592 x 65 8.9 / 4.3, 172 x 1536 x 694 8.0 / 5.7, 500 x 4096 x 256 10.5 / 6.5.
+  const int n_tiles = (N + voc::kLinRows - 1) / voc::kLinRows;
+  const int most = std::max(1, std::min(8, a.chunks / 2));  // parts of K
+  const int m_tiles =
+      std::max((M + 255) / 256, std::min((M + 31) / 32, dev->sms / most / n_tiles));
+  a.nt = ((M + m_tiles - 1) / m_tiles + 15) / 16 * 16;
   a.tmem_cols = 32;
   while (a.tmem_cols < a.nt) a.tmem_cols *= 2;
   // Up to 64 tokens leave room for two CTAs on an SM (measured, one / two, N x K = 12288 x 4096: 33
@@ -395,11 +401,11 @@ VOC_API voc_status vocoder_lm_linear_fp8(const void *x8, long long ldx, const fl
   // K once every SM has a CTA.  Measured at 33 tokens, 12288 x 4096 (96 tiles): split 1 14.7, 2 12.5,
   // 3 12.8 (does not fit), 4 17.2 us; 8 tokens, 2048 x 8192 (16 tiles): split 1 21.9, 4 7.9, 8 5.9 us.
   const int stage = (voc::kLinRows + a.nt) * voc::kLinK;
-  const int tiles = ((N + voc::kLinRows - 1) / voc::kLinRows) * ((M + a.nt - 1) / a.nt);
+  const int tiles = n_tiles * ((M + a.nt - 1) / a.nt);
   const int per_sm = a.nt <= 64 ? 2 : 1;
   const size_t smem = per_sm == 2 ? kLinSmemTwo : kLinSmem;
   a.stages = std::min<int>(12, static_cast<int>((smem - 1024) / stage));
-  int split = std::max(1, std::min(8, a.chunks / 2));
+  int split = most;
   while (split > 1 && (per_sm * dev->clusters[split] < tiles ||
                        (tiles * split > dev->sms && a.chunks / split < 4)))
     --split;
