@@ -36,8 +36,8 @@ __device__ __forceinline__ bool rms_needs_scaling(uint32_t amax) {
   return amax < kInfBits && a != 0.f && (a > 0x1p50f || a < 0x1p-50f);
 }
 __device__ __forceinline__ float rms_prescale(uint32_t amax) {
-  const int e = static_cast<int>(amax >> 23) - 127;  // -127 for subnormals
-  return pow2(min(100, -e));
+  const int e = static_cast<int>(amax >> 23) - 127;  // -127 for subnormals, 127 at most
+  return pow2(max(-126, min(100, -e)));              // 2^-127 would not be a normal number
 }
 __device__ __forceinline__ float rms_factor(float sumsq, int d, float eps, float pre) {
   const float ms = sumsq / static_cast<float>(d);
