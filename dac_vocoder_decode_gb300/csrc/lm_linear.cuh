@@ -66,11 +66,13 @@ __global__ void __launch_bounds__(kLinThreads, 2)
   const uint32_t tmem = tmem_slot;
   const int never = 0;
   volatile int *abort = &abort_flag;
+  // Every thread, ahead of its first wait with a limit: the kernel before this one may take longer than
+  // the limit, and only from here on does a wait depend on this grid alone.
+  pdl_wait();
+  pdl_launch_dependents();
 
   if (warp == 4) {
     if (lane == 0) {
-      pdl_wait();
-      pdl_launch_dependents();
       int issued = c0;
       for (int c = c0; c < c1; ++c) {
         const int i = c - c0, st = i % p.stages;
@@ -144,7 +146,6 @@ __global__ void __launch_bounds__(kLinThreads, 2)
     tc_fence_after();
     tmem_dealloc(tmem, p.tmem_cols);
   }
-  pdl_wait();
   T *out = static_cast<T *>(p.out);
   const int n = n0 + 4 * lane;  // this lane's four channels
   float ws[4], bias[4];
@@ -292,11 +293,11 @@ __global__ void __launch_bounds__(kManyThreads, 1) __cluster_dims__(2, 1, 1)
   cluster_sync();  // the other CTA's barriers stand before anything arrives there
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  pdl_wait();  // every thread, ahead of its first wait with a limit (as in linear_few_kernel)
+  pdl_launch_dependents();
 
   if (warp == kManyEpi) {
     if (lane == 0) {
-      pdl_wait();
-      pdl_launch_dependents();
       const uint32_t full0 = mapa_shared(smem_u32(full), 0u);
       int it = 0;
       bool ok = true;
@@ -361,8 +362,6 @@ __global__ void __launch_bounds__(kManyThreads, 1) __cluster_dims__(2, 1, 1)
   } else if (warp < kManyEpi) {
     // The accumulator's lanes are token rows.  A warp takes 32 rows of half of the columns and turns
     // pieces of 32 rows x 64 bytes around in shared memory, so that its stores fill whole sectors.
-    pdl_wait();
-    pdl_launch_dependents();
     constexpr int kCols = 64 / static_cast<int>(sizeof(T));  // columns of a staged piece
     constexpr int kPer = 16 / static_cast<int>(sizeof(T));
     const int quad = warp % 4, c_first = warp / 4 * (kManyTile / 2);

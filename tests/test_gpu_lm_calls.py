@@ -1,0 +1,55 @@
+"""GPU: what calls of the 8-bit operators leave to their caller and what they do not: kernels before
+them that take long, streams, defaults, threads."""
+from __future__ import annotations
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # collected on CPU-only machines, never run there
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+from dac_vocoder_decode_gb300 import binding as V  # noqa: E402
+from tests import test_gpu_lm as T  # noqa: E402
+
+SYNC = V.VOC_FLAG_SYNC
+
+
+# ------------------------------------------------------------------ a long kernel in front
+@pytest.mark.parametrize("m,n", [(8, 1536), (2100, 1100)])
+def test_linear_behind_a_kernel_of_seconds(m, n):
+    """A product starts beside the kernel before it where that leaves SMs free.  Its waits' limit
+    (about 2 s) counts from that kernel's end: here an attention of about 3 s on 80 SMs, over caches
+    whose blocks are all one page."""
+    k, seqs, rows = 1000, 80, 200
+    g = torch.Generator(device="cuda").manual_seed(m)
+    x, w = T._codes(g, m, k), T._codes(g, n, k)
+    xs, ws = torch.rand(m, generator=g, device="cuda"), torch.rand(n, generator=g, device="cuda")
+    ref = V.linear_fp8(x, xs, w, ws, flags=SYNC)
+    cache = V.KVCacheFP8.empty(1, 1, 64)
+    q = torch.zeros(seqs * rows, 1, 64, dtype=torch.bfloat16, device="cuda")
+
+    def attend(table, blocks):
+        lens = torch.full((seqs,), 64 * blocks, dtype=torch.int32, device="cuda")
+        marks = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        marks[0].record()
+        V.attention_fp8(q, cache, table, lens, max_q=rows)
+        marks[1].record()
+        return marks
+
+    def seconds(marks):
+        torch.cuda.synchronize()
+        return marks[0].elapsed_time(marks[1]) / 1e3
+
+    few = 20000
+    table = torch.zeros(seqs, few, dtype=torch.int32, device="cuda")
+    attend(table, few)
+    blocks = min(int(few * 3 / seconds(attend(table, few))), 5_000_000)
+    table = torch.zeros(seqs, blocks, dtype=torch.int32, device="cuda")
+    marks = attend(table, blocks)
+    y = V.linear_fp8(x, xs, w, ws)
+    assert 2.2 < seconds(marks) < 6
+    assert torch.equal(y, ref)
+    V.linear_fp8(x, xs, w, ws, flags=SYNC)  # would report a wait that gave up
