@@ -87,12 +87,14 @@ __global__ void __launch_bounds__(kLinThreads, 2)
         tma_load_2d(dst + kLinRows * kLinK, &xmap, bar, c * kLinK, m0);
         issued = c + 1;
       }
-      if (*abort) {  // leave with no copy in flight
-        for (int c = max(c0, issued - p.stages); c < issued; ++c)
-          mbar_wait(smem_u32(full + (c - c0) % p.stages), ((c - c0) / p.stages) & 1, p.budget,
-                    &never);
-        if (p.timeout) *p.timeout = 1;
-      }
+      // leave with no copy in flight, also where the products give up after the last copy was issued
+      for (int c = max(c0, issued - p.stages); c < issued; ++c)
+        if (!mbar_wait(smem_u32(full + (c - c0) % p.stages), ((c - c0) / p.stages) & 1, p.budget,
+                       &never)) {
+          *abort = 1;
+          break;
+        }
+      if (*abort && p.timeout) *p.timeout = 1;
     }
   } else if (warp == 5) {
     const uint32_t idesc = idesc_e4m3_f32(kLinRows, p.nt);
@@ -101,6 +103,7 @@ __global__ void __launch_bounds__(kLinThreads, 2)
       const bool landed = mbar_wait(smem_u32(full + st), (i / p.stages) & 1, p.budget, abort);
       if (!__all_sync(0xffffffffu, landed)) {
         *abort = 1;
+        if (p.timeout) *p.timeout = 1;
         break;
       }
       tc_fence_after();
@@ -317,9 +320,15 @@ __global__ void __launch_bounds__(kManyThreads, 1) __cluster_dims__(2, 1, 1)
           tma_load_2d_pair(dst + kManyStage / 2, &wmap, full0 + st * 8, c * kLinK, n0);
         }
       }
+      // Leave with no copy in flight, also where the products give up after the last copy was issued: the
+      // even CTA's barriers count both CTAs' copies, and neither leaves without the other.
+      if (rank == 0)
+        for (int i = max(0, it - kManyStages); i < it && ok; ++i)
+          ok = mbar_wait_cluster(smem_u32(full + i % kManyStages), (i / kManyStages) & 1, p.budget,
+                                 &never);
       if (!ok) {
         raise();
-        // copies in flight land well within this wait, which nothing ends early
+        // the odd CTA may have issued more: that lands well within this wait, which nothing ends early
         mbar_wait(smem_u32(&unused), 0, p.budget, &never);
       }
     }
