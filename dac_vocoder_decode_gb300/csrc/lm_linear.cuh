@@ -69,11 +69,11 @@ __global__ void __launch_bounds__(kLinThreads, 2)
   // Every thread, ahead of its first wait with a limit: the kernel before this one may take longer than
   // the limit, and only from here on does a wait depend on this grid alone.
   pdl_wait();
-  pdl_launch_dependents();
 
+  int issued = c0;  // copies up to here are under way or done
   if (warp == 4) {
     if (lane == 0) {
-      int issued = c0;
+      pdl_launch_dependents();  // one thread's call stands for the CTA; by all of them it took 0.2 us more
       for (int c = c0; c < c1; ++c) {
         const int i = c - c0, st = i % p.stages;
         if (i >= p.stages &&
@@ -87,14 +87,6 @@ __global__ void __launch_bounds__(kLinThreads, 2)
         tma_load_2d(dst + kLinRows * kLinK, &xmap, bar, c * kLinK, m0);
         issued = c + 1;
       }
-      // leave with no copy in flight, also where the products give up after the last copy was issued
-      for (int c = max(c0, issued - p.stages); c < issued; ++c)
-        if (!mbar_wait(smem_u32(full + (c - c0) % p.stages), ((c - c0) / p.stages) & 1, p.budget,
-                       &never)) {
-          *abort = 1;
-          break;
-        }
-      if (*abort && p.timeout) *p.timeout = 1;
     }
   } else if (warp == 5) {
     const uint32_t idesc = idesc_e4m3_f32(kLinRows, p.nt);
@@ -199,6 +191,14 @@ __global__ void __launch_bounds__(kLinThreads, 2)
           if (n + k < p.N) dst[k] = from_f32<T>(f[k]);
       }
     }
+  }
+  // Leave with no copy in flight.  Without a give-up (a barrier has been passed since the flag was last
+  // raised) the products have waited for every copy.
+  if (warp == 4 && lane == 0 && *abort) {
+    if (p.timeout) *p.timeout = 1;
+    for (int c = max(c0, issued - p.stages); c < issued; ++c)
+      if (!mbar_wait(smem_u32(full + (c - c0) % p.stages), ((c - c0) / p.stages) & 1, p.budget, &never))
+        break;
   }
   if (split > 1) {
     __syncwarp();
