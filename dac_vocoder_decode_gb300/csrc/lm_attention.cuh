@@ -617,8 +617,10 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const LmAttnArgs p) {
   __shared__ int counts[2][kWarps];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int b = blockIdx.z, hk = blockIdx.y, row = blockIdx.x;
-  // Lengths and counts were complete before the kernel that this one follows started its work, and
-  // it writes neither, so they are read before waiting for it.
+  // Lengths and counts too are read after the wait: they may come from the kernel before the one that
+  // this one follows, and nothing else makes that one's stores visible here.
+  pdl_wait();
+  pdl_launch_dependents();
   const SeqSpan span = seq_span(p.cu, b, p.n_seq, p.n_tokens, p.max_q);
   // the work before this sequence and in all, as attn_rows_kernel counts it
   int both[2] = {0, 0};
@@ -644,8 +646,6 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const LmAttnArgs p) {
   const int q = share_of(both[1], p.ctas);
   const int at = both[0] + (hk * w.tiles + row / ROWS) * per;
   const int c0 = (at + kTileCost) / q, c1 = (at + per - 1) / q;
-  pdl_wait();
-  pdl_launch_dependents();
   if (row >= span.count * p.group || c0 == c1) return;  // c0 == c1: one CTA had the whole tile
   const int parts = c1 - c0 + 1;
   auto slot_of = [&](int s) {
@@ -718,9 +718,9 @@ __global__ void __launch_bounds__(32 * kJoinRows) attn_join_tiles_kernel(const L
   constexpr int kPer = D / 32;  // channels of a lane
   const int lane = threadIdx.x % 32, hk = blockIdx.y;
   int nth = 0;
-  const int b = find_tile(p, blockIdx.x, lane, nth);  // (counts may be read early: attn_join_kernel)
-  pdl_wait();
+  pdl_wait();  // ahead of the counts too (attn_join_kernel)
   pdl_launch_dependents();
+  const int b = find_tile(p, blockIdx.x, lane, nth);
   if (b < 0) return;
   const SeqSpan span = seq_span(p.cu, b, p.n_seq, p.n_tokens, p.max_q);
   const int local = blockIdx.z * kJoinRows + threadIdx.x / 32, row = nth * kPrRows + local;

@@ -53,3 +53,24 @@ def test_linear_behind_a_kernel_of_seconds(m, n):
     assert 2.2 < seconds(marks) < 6
     assert torch.equal(y, ref)
     V.linear_fp8(x, xs, w, ws, flags=SYNC)  # would report a wait that gave up
+
+
+# ------------------------------------------------------------------ lengths made just before
+@pytest.mark.parametrize("heads,rows", [(4, 1), (2, 40)])
+def test_attention_takes_lengths_of_the_kernel_in_front(heads, rows):
+    """Lengths (and with them the shares of the CTAs and the parts that are joined) that change from
+    call to call, written right in front of the call, against the same lengths at rest."""
+    seqs, cols = 3, 130
+    bt = T.Batch([64 * cols] * seqs, [rows] * seqs, 1, 64, seed=rows, spare_cols=0)
+    q = T._queries(bt, heads)
+    g = torch.Generator().manual_seed(7)
+    lens = torch.randint(rows, 64 * cols + 1, (40, seqs), generator=g, dtype=torch.int32).cuda()
+    place = torch.zeros(seqs, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    got = []
+    for row in lens:
+        place.copy_(row)
+        got.append(V.attention_fp8(q, bt.cache, bt.t_table, place, max_q=rows))
+    torch.cuda.synchronize()
+    for row, o in zip(lens, got):
+        assert torch.equal(V.attention_fp8(q, bt.cache, bt.t_table, row.clone(), max_q=rows, flags=SYNC), o)

@@ -1,7 +1,9 @@
 """GPU: the 8-bit operators' kernels for many tokens and long caches, over what only large sizes
-reach: rings that wrap, further tiles of a pair.
+reach: rings that wrap, further tiles of a pair, tiles in many parts.
 
-Tolerances are those of tests/test_gpu_lm.py.  A test that is written for one kernel asserts that its
+Tolerances are those of tests/test_gpu_lm.py.  The attention's 64-bit reference is taken on the GPU
+in plain products (`_reference`), by the same definition as tests/lm_ref.py; one test holds the two
+together.  A test that is written for one kernel asserts that its
 call launches it.
 """
 from __future__ import annotations
@@ -9,6 +11,7 @@ from __future__ import annotations
 import os
 import warnings
 
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -19,6 +22,7 @@ if not torch.cuda.is_available():  # collected on CPU-only machines, never run t
     pytest.skip("no CUDA device", allow_module_level=True)
 
 from dac_vocoder_decode_gb300 import binding as V  # noqa: E402
+from tests import lm_ref as R  # noqa: E402
 from tests import test_gpu_lm as T  # noqa: E402
 
 SYNC = V.VOC_FLAG_SYNC
@@ -102,3 +106,99 @@ def test_linear_few_over_many_chunks(tmp_path, out, m, k, n, bias):
     assert "linear_few_kernel" in _launched(tmp_path, call)
     y = V.linear_fp8(x, xs, w, ws, bias=b, out_dtype=T.TYPES[out], flags=SYNC)
     T._check_linear(x, xs, w, ws, b, y)
+
+
+# ------------------------------------------------------------------ attention over long caches
+class Pool:
+    """Sequences whose blocks are drawn from one small pool, so that long caches take little memory;
+    every block and head has scales of its own."""
+
+    def __init__(self, lens, new, kv_heads, d, pages=300, seed=0):
+        rng = np.random.default_rng(seed)
+        self.lens, self.new, self.kv_heads, self.d, self.rng = lens, new, kv_heads, d, rng
+        self.total, self.max_q = sum(new), max(new)
+        cols = max(-(-n // 64) for n in lens)
+        self.table = torch.from_numpy(rng.integers(0, pages, (len(lens), cols)).astype(np.int32)).cuda()
+        grid = lambda *s: torch.from_numpy(  # noqa: E731
+            R.e4m3_round(rng.standard_normal(s) * 100).astype(np.float32)).cuda().to(T.F8)
+        scale = lambda lo, hi: torch.from_numpy(  # noqa: E731
+            np.exp2(rng.integers(lo, hi, (pages, kv_heads))).astype(np.float32)).cuda()
+        self.cache = V.KVCacheFP8(grid(pages, kv_heads, 64, d), grid(pages, kv_heads, d, 64),
+                                  scale(-9, -5), scale(-12, -5))
+        self.t_lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        self.cu = None if len(set(new)) == 1 else torch.from_numpy(cu).cuda()
+
+    def args(self):
+        return dict(page_table=self.table, kv_lens=self.t_lens, cu_q=self.cu, max_q=self.max_q)
+
+    def queries(self, heads, dtype="bf16"):
+        q = self.rng.standard_normal((self.total, heads, self.d))
+        return torch.from_numpy(q).cuda().to(T.TYPES[dtype])
+
+
+def _reference(bt, q, window=0, causal=True):
+    """(o, sum of weights times |v|, largest sum of |q k| times the scale) in 64 bits."""
+    heads, d, scale = q.shape[1], bt.d, bt.d ** -0.5
+    group = heads // bt.kv_heads
+    o = torch.zeros(q.shape, dtype=torch.float64, device="cuda")
+    mag, smax = torch.zeros_like(o), torch.zeros(q.shape[:2], dtype=torch.float64, device="cuda")
+    at = 0
+    for b, (n, m) in enumerate(zip(bt.lens, bt.new)):
+        pages = bt.table[b, :-(-n // 64)].long()
+        pos = torch.arange(n - m, n, device="cuda")[:, None]
+        key = torch.arange(n, device="cuda")[None]
+        seen = (key <= pos) if causal else torch.ones(m, n, dtype=torch.bool, device="cuda")
+        if window:
+            seen = seen & (key > pos - window)
+        for hk in range(bt.kv_heads):
+            k = bt.cache.k[:, hk].double()[pages] * bt.cache.k_scale[:, hk].double()[pages][:, None, None]
+            v = bt.cache.v[:, hk].double()[pages] * bt.cache.v_scale[:, hk].double()[pages][:, None, None]
+            k, v = k.reshape(-1, d)[:n], v.transpose(1, 2).reshape(-1, d)[:n]
+            for h in range(hk * group, (hk + 1) * group):
+                qq = q[at:at + m, h].double()
+                s = (qq @ k.T * scale).masked_fill(~seen, -float("inf"))
+                w = torch.softmax(s, 1)
+                o[at:at + m, h], mag[at:at + m, h] = w @ v, w @ v.abs()
+                smax[at:at + m, h] = (qq.abs() @ k.abs().T * scale).masked_fill(~seen, 0).amax(1)
+        at += m
+    return o, mag, smax
+
+
+def _check(bt, q, window=0, causal=True, **kw):
+    o = V.attention_fp8(q, bt.cache, window=window, causal=causal, flags=SYNC, **bt.args(), **kw)
+    ref, mag, s = _reference(bt, q, window, causal)
+    rel = 2.0 ** -11 + 2.0 ** -16 + 2 * 1.5 * bt.d * 2.0 ** -24 * s
+    tol = rel[..., None] * mag + T.UNIT[q.dtype] * ref.abs() + 2.0 ** -30
+    off = (o.double() - ref).abs()
+    assert bool(torch.isfinite(o).all())
+    assert bool((off <= tol).all()), float((off / tol).max())
+    return o
+
+
+def test_the_two_references_agree():
+    bt = Pool([130, 70, 64], [40, 1, 64], 2, 64, seed=1)
+    q = bt.queries(4)
+    ref, mag, s = R.attention(T._np(q), T._np(bt.cache.k), T._np(bt.cache.v), T._np(bt.cache.k_scale),
+                              T._np(bt.cache.v_scale), bt.table.cpu().numpy(), bt.lens, bt.new, 0.125,
+                              window=50)
+    for a, b in zip(_reference(bt, q, window=50), (ref, mag, s)):
+        np.testing.assert_allclose(T._np(a), b, rtol=1e-10, atol=1e-12)
+
+
+@pytest.mark.parametrize("d,heads", [(64, 1), (128, 8), (64, 9), (128, 16)])
+@pytest.mark.parametrize("n", [2300, 9000, 17000])
+def test_attention_single_tokens_in_many_parts(tmp_path, d, heads, n):
+    """One sequence and key head: 11, 37 and 68 parts of a tile, so the join takes them in one, two
+    and three turns of 32, for tiles of 8 and of 16 rows."""
+    bt = Pool([n], [1], 1, d, seed=n)
+    q = bt.queries(heads)
+    text = _launched(tmp_path, lambda: V.attention_fp8(q, bt.cache, **bt.args()))
+    assert "attn_rows_kernel" in text and "attn_join_kernel" in text
+    _check(bt, q)
+
+
+def test_attention_long_beside_short():
+    """A tile in more than 32 parts beside tiles that a CTA has whole."""
+    bt = Pool([17000, 5, 64, 3000, 1], [1] * 5, 1, 64, seed=9)
+    _check(bt, bt.queries(4))
