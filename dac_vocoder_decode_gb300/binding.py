@@ -798,17 +798,21 @@ def _bad(msg: str):
 
 
 def _lm_stream(dev, stream, made):
-    """Raw stream.  Tensors `made` by the call belong to the current stream; one of the caller's
-    that is another keeps them until its work is done."""
+    """Raw stream.  Tensors `made` by the call belong to the current stream.  Another one of the
+    caller's waits for what the current stream has in its queue, whose last reads of that memory may
+    still be ahead, and keeps the tensors until its own work is done.  (With every output and the
+    workspace given, nothing is made and nothing waits.)"""
     if stream is None:
         return _LM.raw_stream(dev)
     torch = _LM.torch
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=dev)
     if stream.cuda_stream != _LM.raw_stream(dev):
+        made = [t for t in made if t is not None]
+        if made:
+            stream.wait_stream(torch.cuda.current_stream(dev))
         for t in made:
-            if t is not None:
-                t.record_stream(stream)
+            t.record_stream(stream)
     return stream.cuda_stream
 
 

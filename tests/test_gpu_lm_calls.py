@@ -74,3 +74,39 @@ def test_attention_takes_lengths_of_the_kernel_in_front(heads, rows):
     torch.cuda.synchronize()
     for row, o in zip(lens, got):
         assert torch.equal(V.attention_fp8(q, bt.cache, bt.t_table, row.clone(), max_q=rows, flags=SYNC), o)
+
+
+# ------------------------------------------------------------------ streams
+@pytest.mark.parametrize("op", ["rows", "linear", "attention"])
+def test_given_stream_leaves_memory_that_the_current_one_still_reads(op):
+    """A tensor whose last read waits in the current stream's queue is dropped, and a call on another
+    stream gets its memory for a result: the read still finds the old values."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(64, 2048, generator=g, device="cuda").bfloat16()
+    w = torch.ones(2048, device="cuda").bfloat16()
+    x8, xs, _ = V.rows_fp8(x, V.VOC_LM_NONE)
+    bt = T.Batch([300] * 64, [1] * 64, 2, 64, seed=1)
+    q = T._queries(bt, 4)
+    calls = dict(
+        rows=(lambda **kw: V.rows_fp8(x, weight=w, residual=x, **kw), 64 * 2048 * 2),
+        linear=(lambda **kw: (V.linear_fp8(x8, xs, x8, xs, **kw),), 64 * 64 * 2),
+        attention=(lambda **kw: (V.attention_fp8(q, bt.cache, **bt.args(), **kw),), 64 * 4 * 64 * 2))
+    call, size = calls[op]
+    ref = call()  # set-up, and the result
+    ref = [t.clone() for t in ref]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    old = torch.full((size,), 77, dtype=torch.uint8, device="cuda")
+    kept = torch.empty_like(old)
+    torch.cuda.synchronize()
+    where = old.data_ptr()
+    torch.cuda._sleep(400_000_000)  # about 0.2 s
+    kept.copy_(old)
+    del old
+    got = call(stream=side)
+    torch.cuda.synchronize()
+    assert where in [t.data_ptr() for t in got]
+    assert torch.all(kept == 77)
+    for a, b in zip(got, ref):
+        assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
