@@ -956,8 +956,9 @@ def linear_fp8(x, x_scale, w, w_scale, bias=None, out_dtype=None, out=None, stre
 class KVCacheFP8:
     """A pool of 64-token blocks of e4m3 keys and values: k [pages, kv_heads, 64, d] and v [pages,
     kv_heads, d, 64] float8_e4m3fn, k_scale and v_scale fp32 [pages, kv_heads] (see the cache in
-    include/vocoder.h)."""
-    __slots__ = ("k", "v", "k_scale", "v_scale", "_args")
+    include/vocoder.h).  The tensors are written in place and never exchanged (their addresses are
+    kept): a larger pool is a new KVCacheFP8."""
+    __slots__ = ("_tensors", "_args")
 
     def __init__(self, k, v, k_scale, v_scale):
         if not _LM.ready:
@@ -965,8 +966,12 @@ class KVCacheFP8:
         # addresses, pages, key heads, head_dim, device
         args = _LM.fast.cache(k, v, k_scale, v_scale) if _LM.fast is not None else None
         self._args = self._checked(k, v, k_scale, v_scale) if args is None else args
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._tensors = (k, v, k_scale, v_scale)
 
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    k_scale = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
     pages = property(lambda self: self._args[4])
     kv_heads = property(lambda self: self._args[5])
     head_dim = property(lambda self: self._args[6])
