@@ -1021,12 +1021,16 @@ def _batch_args(cache, x, page_table, kv_lens, cu_q):
                  cu, n)
 
 
-def kv_append_fp8(cache: KVCacheFP8, k, v, page_table, kv_lens, cu_q=None, max_q: int = 1,
-                  stream=None, flags: int = 0) -> None:
+def kv_append_fp8(cache: KVCacheFP8, k, v, page_table, kv_lens, cu_q=None,
+                  max_q: Optional[int] = None, stream=None, flags: int = 0) -> None:
     """Store k and v [tokens, kv_heads, head_dim] (bf16 or f16) of new tokens in the cache (see
     vocoder_lm_kv_append in include/vocoder.h).  page_table int32 [sequences, blocks], kv_lens
     int32 [sequences] with the new tokens counted, cu_q int32 [sequences + 1] or None when every
-    sequence has max_q new tokens."""
+    sequence has max_q new tokens.  max_q defaults to 1 without cu_q.  With it, tokens of a sequence
+    beyond max_q would be dropped, so it defaults to the number of tokens; the largest number of a
+    sequence, where the caller knows it, is faster."""
+    if max_q is None:
+        max_q = 1 if cu_q is None else k.shape[0]
     if stream is None and _LM.fast is not None:
         res = _LM.fast.append(cache._args, k, v, page_table, kv_lens, cu_q, max_q, flags)
         if res is not None:
@@ -1046,14 +1050,16 @@ def kv_append_fp8(cache: KVCacheFP8, k, v, page_table, kv_lens, cu_q=None, max_q
         _check(st)
 
 
-def attention_fp8(q, cache: KVCacheFP8, page_table, kv_lens, cu_q=None, max_q: int = 1,
-                  max_kv: Optional[int] = None, softmax_scale: Optional[float] = None,
-                  causal: bool = True, window: int = 0, out=None, ws=None, stream=None,
-                  flags: int = 0):
+def attention_fp8(q, cache: KVCacheFP8, page_table, kv_lens, cu_q=None,
+                  max_q: Optional[int] = None, max_kv: Optional[int] = None,
+                  softmax_scale: Optional[float] = None, causal: bool = True, window: int = 0,
+                  out=None, ws=None, stream=None, flags: int = 0):
     """Attention of the newest tokens' queries q [tokens, heads, head_dim] over the cache (see
     vocoder_lm_attention in include/vocoder.h; the batch as in kv_append_fp8).  max_kv: at least
     the largest kv_len (default: what the page table can hold); softmax_scale defaults to
     1/sqrt(head_dim); ws: uint8 workspace of vocoder_lm_attention_ws_bytes (a new one if None)."""
+    if max_q is None:
+        max_q = 1 if cu_q is None else q.shape[0]
     if stream is None and _LM.fast is not None:
         res = _LM.fast.attention(q, cache._args, page_table, kv_lens, cu_q, max_q,
                                  -1 if max_kv is None else max_kv, softmax_scale, causal, window,

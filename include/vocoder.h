@@ -546,7 +546,8 @@ voc_status vocoder_lm_linear_fp8(const void *x8, long long ldx, const float *x_s
  *   a page outside 0..n_pages-1 holds no tokens (nothing is written to or read from it);
  *   kv_lens [n_seq] int32: tokens of the sequence, the new ones included;
  *   cu_q [n_seq + 1] int32: first new token of each sequence, or NULL when each has max_q;
- *   max_q: the largest number of new tokens of a sequence.
+ *   max_q: the largest number of new tokens of a sequence, or more, up to n_tokens (a sequence's
+ *   tokens beyond it are not stored, and their outputs not written).
  * New token i of a sequence with q of them has position kv_len - q + i.
  *
  * Append stores the new tokens' k and v [n_tokens][kv_heads][head_dim] (bf16 or f16, head_dim

@@ -110,3 +110,38 @@ def test_given_stream_leaves_memory_that_the_current_one_still_reads(op):
     assert torch.all(kept == 77)
     for a, b in zip(got, ref):
         assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+# ------------------------------------------------------------------ defaults
+@pytest.mark.parametrize("lens,new", [([300, 64, 90], [17, 64, 1]), ([5, 700], [1, 0]),
+                                      ([70, 1, 128], [1, 1, 1])])
+def test_sequences_of_any_number_of_tokens_without_max_q(lens, new):
+    """With cu_q every new token is stored and attended to, whether or not max_q is given."""
+    a, b = (T.Batch(lens, new, 2, 64, seed=3, filled=False) for _ in range(2))
+    cu = torch.tensor([sum(new[:i]) for i in range(len(new) + 1)], dtype=torch.int32, device="cuda")
+    k, v = (torch.from_numpy(a.rng.standard_normal((a.total, 2, 64))).cuda().bfloat16()
+            for _ in range(2))
+    q = T._queries(a, 4)
+    batch = dict(page_table=a.t_table, kv_lens=a.t_lens, cu_q=cu)
+    V.kv_append_fp8(a.cache, k, v, flags=SYNC, **batch)
+    V.kv_append_fp8(b.cache, k, v, flags=SYNC, max_q=max(new), **batch)
+    for name in ("k", "v", "k_scale", "v_scale"):
+        x, y = (getattr(t.cache, name).view(torch.uint8) for t in (a, b))
+        assert torch.equal(x, y)
+    T.R.append(a.kc, a.vc, a.ks, a.vs, T._np(k), T._np(v), a.table, lens, new)
+    o = V.attention_fp8(q, a.cache, flags=SYNC, **batch)
+    ref, mag, s = T.R.attention(T._np(q), a.kc, a.vc, a.ks, a.vs, a.table, lens, new, 0.125)
+    rel = 2.0 ** -11 + 2.0 ** -16 + 2 * 1.5 * 64 * 2.0 ** -24 * s
+    tol = rel[..., None] * mag + T.UNIT[q.dtype] * abs(ref) + 2.0 ** -30
+    assert (abs(T._np(o) - ref) <= tol).all()
+
+
+def test_one_token_each_is_the_default_without_cu_q():
+    bt = T.Batch([70, 3], [1, 1], 1, 64)
+    q = T._queries(bt, 2)
+    batch = dict(page_table=bt.t_table, kv_lens=bt.t_lens)
+    assert torch.equal(V.attention_fp8(q, bt.cache, flags=SYNC, **batch),
+                       V.attention_fp8(q, bt.cache, max_q=1, flags=SYNC, **batch))
+    with pytest.raises(V.VocoderError) as e:
+        V.attention_fp8(torch.cat([q, q]), bt.cache, **batch)
+    assert e.value.status == V.VOC_INVALID_ARG
