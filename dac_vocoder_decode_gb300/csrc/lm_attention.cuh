@@ -70,11 +70,12 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
 }
 
 // Scale of a 16-bit query row (a power of two) that brings its largest finite value to
-// [2^14, 2^15): f16 then holds bf16 and f16 values exactly, but for what lies 2^-28 below it.
+// [2^14, 2^15), or below where that is under 2^-96: f16 then holds bf16 and f16 values exactly, but for
+// what lies 2^-28 below it.  bf16's largest values take 2^-113.
 __device__ __forceinline__ int query_exponent(uint32_t amax) {
   if (amax == 0) return 0;
   const int e = 14 - (static_cast<int>(amax >> 23) - 127);
-  return min(max(e, -110), 110);
+  return min(max(e, -113), 110);
 }
 
 // The keys that the rows [r0, r1) of a sequence's tile can see, and those of one row.

@@ -4,6 +4,7 @@ Tolerances, derived before any run: those of tests/test_gpu_lm.py, from its own 
 """
 from __future__ import annotations
 
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -49,3 +50,17 @@ def test_rows_largest_magnitudes(dtype, d):
     rest = (x.double() - half.double()).to(t)
     got = V.rows_fp8(half, weight=w, residual=rest, eps=1e-6, flags=SYNC)
     T._check_rows(half, "rms", w, rest, 1e-6, got, d)
+
+
+# ------------------------------------------------------------------ attention
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [[1, 1], [5, 64], [129, 64]])
+def test_attention_largest_queries(d, new):
+    """bf16 queries from 2^126 to the largest value, over keys so small that scores stay finite."""
+    bt = T.Batch([400, 64], new, 2, d, seed=8)
+    bt.ks = np.full_like(bt.ks, 2.0 ** -90)
+    bt.cache.k_scale.copy_(torch.from_numpy(bt.ks).cuda())
+    q = bt.rng.uniform(-1, 1, (bt.total, 4, d)) * float(torch.finfo(torch.bfloat16).max)
+    q[0, 1, 5] = 2.0 ** 126
+    q[1] *= 2.0 ** -3
+    T._check_attention(bt, torch.from_numpy(q).cuda().bfloat16(), scale=2.0 ** -49)
