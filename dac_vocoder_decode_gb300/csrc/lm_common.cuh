@@ -116,6 +116,26 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
   return w;
 }
 
+// The smaller ones of two pairs of 16-bit values (a number before NaN).
+template <typename T>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b);
+template <>
+__device__ __forceinline__ uint32_t min2<__half>(uint32_t a, uint32_t b) {
+  __half2 x, y;
+  memcpy(&x, &a, 4), memcpy(&y, &b, 4);
+  x = __hmin2(x, y);
+  memcpy(&a, &x, 4);
+  return a;
+}
+template <>
+__device__ __forceinline__ uint32_t min2<__nv_bfloat16>(uint32_t a, uint32_t b) {
+  __nv_bfloat162 x, y;
+  memcpy(&x, &a, 4), memcpy(&y, &b, 4);
+  x = __hmin2(x, y);
+  memcpy(&a, &x, 4);
+  return a;
+}
+
 // Two floats to two e4m3 codes, `lo` in the low byte: round to nearest even, magnitudes over 448
 // (infinities too) to 448, NaN to 0x7f.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {

@@ -47,13 +47,22 @@ __device__ __forceinline__ float rms_factor(float sumsq, int d, float eps, float
   return v > 0.f ? 1.f / sqrtf(v) : (v == 0.f ? 0.f : v);  // a row of zeros without eps: zeros
 }
 
-// The exponential's and the reciprocal's approximations are good to a few 2^-23, far inside half an
-// e4m3 step; e^-g that overflows gives the limit, 0.  (Six instructions a value: the gated rows are bound
-// by how many they issue.)
+// The exponential's and the reciprocal's approximations are good to a few 2^-23 (far below zero the
+// rounding of the exponent's argument makes it 2^-17), far inside half an e4m3 step.  For gates from
+// kGateLow on, where the reciprocal still is a normal number.  (Six instructions a value; with a full
+// division 4001 x 4100 took 0.8 us more.)
+constexpr float kGateLow = -80.f;
 __device__ __forceinline__ float silu_mul(float g, float u) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(-1.44269504f * g)));
   return g * r * u;
+}
+// The same for any gate.  Below kGateLow 1 / (1 + e^-g) is e^g, which u may bring back into range: a half
+// of it goes to either factor.  (NaN takes the first way, and stays.)
+__device__ __forceinline__ float silu_mul_any(float g, float u) {
+  if (!(g < kGateLow)) return silu_mul(g, u);
+  const float t = expf(0.5f * g);
+  return (g * t) * (u * t);
 }
 
 // Whether a row's sum of squares lost nothing: no overflow, and squares that vanished count for less
@@ -112,7 +121,7 @@ __global__ void __launch_bounds__(kAnyThreads) rows_any_kernel(const LmRowsArgs 
   const T *w = static_cast<const T *>(p.w);
   T *s = p.sum ? static_cast<T *>(p.sum) + row * p.lds : nullptr;
   auto load = [&](int i) {
-    if (MODE == kRowsGated) return silu_mul(to_f32(x[i]), to_f32(x[p.d + i]));
+    if (MODE == kRowsGated) return silu_mul_any(to_f32(x[i]), to_f32(x[p.d + i]));
     const float h = to_f32(x[i]);
     return r ? h + to_f32(r[i]) : h;
   };
@@ -192,6 +201,25 @@ struct RowVec {
         w[j] = pack2<T>(f[2 * j], f[2 * j + 1]);
     }
   }
+  // Whether one of the values is below `bound` (NaN is not).
+  template <int CH>
+  static __device__ __forceinline__ bool any_below(const Words (&w)[CH], float bound) {
+    float lo[2] = {INFINITY, INFINITY};
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) lo[j % 2] = fminf(lo[j % 2], __uint_as_float(w[i][j]));
+    } else {
+      uint32_t m = w[0][0];
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) m = min2<T>(m, w[i][j]);
+      unpack2<T>(m, lo[0], lo[1]);
+    }
+    return fminf(lo[0], lo[1]) < bound;
+  }
   // The same from and to any place of T's alignment: whole words where they are, and 16-bit values at
   // the ends of a stretch that starts between two.
   static __device__ __forceinline__ void load_any(const T *p, Words &w) {
@@ -257,8 +285,8 @@ struct RowVec {
 // Measured (bf16, residual): 15504 x 1536 27.8 us, 6.0 TB/s, where a plain copy reaches 6.8 (one value
 // at a time it was 46.5 us); 15504 x 1537 57 us (in the accesses that every row allows, 2 bytes, 137),
 // 1538 40 (4 bytes: 51); 2000 x 16384 40 us, 5.7 TB/s; 8 x 1024 2.2 us, a launch and a chain of two
-// loads and two reductions.  Gated 4001 x 4100 f16: 18.8 us, 4.4 TB/s: 8-byte accesses (the rows'
-// second halves start on 8 bytes), instructions in two cycles of three, and 4 rows in flight on an SM.
+// loads and two reductions.  Gated 4001 x 4100 f16: 19.1 us, 4.3 TB/s: 8-byte accesses (the rows'
+// second halves start on 8 bytes), 4 rows in flight on an SM, each read, reduced and written in turn.
 template <typename T, int MODE, int VB, int CH, bool ANY>
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LmRowsArgs p, const int tpr) {
   using Vec = RowVec<T, VB>;
@@ -299,6 +327,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LmRowsArgs p, c
         load(r, c, b[i]);
       }
     }
+    const bool low = MODE == kRowsGated && Vec::any_below(a, kGateLow);  // rare
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       float u[N];
@@ -310,6 +339,21 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LmRowsArgs p, c
       } else if (lane + i * tpr < chunks) {  // nothing for the places beyond the row (their h is 0)
 #pragma unroll
         for (int j = 0; j < N; ++j) h[i][j] = silu_mul(h[i][j], u[j]);
+      }
+    }
+    if (low) {  // once more, from the row: a look per thread costs less than one per value
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int c = lane + i * tpr;
+        if (c >= chunks) continue;
+        typename Vec::Words v;
+        float g[N], u[N];
+        load(x, c, v);
+        Vec::unpack(v, g);
+        load(r, c, v);
+        Vec::unpack(v, u);
+#pragma unroll
+        for (int j = 0; j < N; ++j) h[i][j] = silu_mul_any(g[j], u[j]);
       }
     }
     if (MODE != kRowsGated && p.sum) {

@@ -1,6 +1,9 @@
 """GPU: the 8-bit operators at the ends of their types' ranges.
 
-Tolerances, derived before any run: those of tests/test_gpu_lm.py, from its own checks.
+Tolerances, derived before any run: those of tests/test_gpu_lm.py, from its own checks.  Gates far
+below zero: e^-|g| by an exponential whose argument, up to 128 in powers of two, is off by half its
+last place (2^-18) and by 2^-25 of itself, together below 5e-6 of the result, and 8 more roundings;
+1e-5 in all.
 """
 from __future__ import annotations
 
@@ -15,6 +18,7 @@ if not torch.cuda.is_available():  # collected on CPU-only machines, never run t
     pytest.skip("no CUDA device", allow_module_level=True)
 
 from dac_vocoder_decode_gb300 import binding as V  # noqa: E402
+from tests import lm_ref as R  # noqa: E402
 from tests import test_gpu_lm as T  # noqa: E402
 
 SYNC = V.VOC_FLAG_SYNC
@@ -50,6 +54,30 @@ def test_rows_largest_magnitudes(dtype, d):
     rest = (x.double() - half.double()).to(t)
     got = V.rows_fp8(half, weight=w, residual=rest, eps=1e-6, flags=SYNC)
     T._check_rows(half, "rms", w, rest, 1e-6, got, d)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [40, 1024, 1031, 4100, 20000])
+def test_rows_gates_far_below_zero(dtype, d):
+    """silu(g) u where e^g is below the smallest normal number and u is large."""
+    t = T.TYPES[dtype]
+    g = torch.Generator(device="cuda").manual_seed(d)
+    rows = 6
+    lo = torch.tensor([-90.0, -100.0, -120.0, -88.0, -150.0, -95.0], device="cuda")[:, None]
+    gate = lo + 8 * torch.rand(rows, d, generator=g, device="cuda")
+    gate[5, ::2] = torch.randn(gate[5, ::2].shape, generator=g, device="cuda")  # beside usual ones
+    up = (0.5 + torch.rand(rows, d, generator=g, device="cuda")) * 2.0 ** 120
+    up *= 1 - 2 * (torch.rand(rows, d, generator=g, device="cuda") < 0.5).float()
+    up[5, ::2] *= 2.0 ** -240
+    x = torch.cat([gate, up], 1).to(t)
+    q, scale, _ = V.rows_fp8(x, V.VOC_LM_GATED, flags=SYNC)
+    n, ref, _ = R.rows(T._np(x), "gated")
+    s = T._np(scale)
+    np.testing.assert_allclose(s, ref, rtol=1e-5, atol=0)
+    v = n / s[:, None]
+    with np.errstate(divide="ignore"):
+        half = np.maximum(np.exp2(np.floor(np.log2(np.abs(v))) - 4), 2.0 ** -10)
+    assert np.all(np.abs(T._np(q) - v) <= half * (1 + 1e-4) + 1e-5 * np.abs(v))
 
 
 # ------------------------------------------------------------------ attention
