@@ -518,7 +518,8 @@ enum { VOC_LM_RMS = 0, VOC_LM_NONE = 1, VOC_LM_GATED = 2 };
  *   VOC_LM_RMS    n = h / sqrt(mean(h^2) + eps) * weight[i]
  *   VOC_LM_NONE   n = h
  *   VOC_LM_GATED  n = silu(x[i]) * x[d + i], x rows of 2d values, no residual
- *   scale[row] = max(max|n|, 2^-96) / 448,  out8[row][i] = e4m3(n / scale), round to nearest even.
+ *   scale[row] = max(max|n|, 2^-96) / 448,  out8[row][i] = e4m3(n / scale), round to nearest even
+ *   (n / scale good to 2^-22 of itself: that close to a tie it may take the code on the other side).
  * x, residual, weight and sum_out have the type `dtype`; sum_out (NULL: not wanted) receives h
  * rounded once and may be the buffer of x or residual (same stride).  The norm takes the
  * unrounded h.  A row that holds a NaN gets a NaN scale and NaN codes, a row that holds an
@@ -573,7 +574,13 @@ voc_status vocoder_lm_kv_append(void *k_cache, void *v_cache, float *k_scale, fl
  * a query's tokens does not reach it, except that stored values (v_cache) of tokens other queries
  * of the call see must not be NaN codes (append never stores one).  max_kv: at least the largest
  * kv_len (it bounds the split of long caches, not the result).  ws: 16-byte aligned, at least
- * vocoder_lm_attention_ws_bytes (0: NULL will do), not used by anything else meanwhile. */
+ * vocoder_lm_attention_ws_bytes (0: NULL will do), not used by anything else meanwhile.
+ *
+ * The softmax's weights enter the product with v as f16 values, relative to the query's largest
+ * weight * v_scale: 11 bits down to 2^-21 of it, fewer below, none from 2^-32 on.  Their own sum is
+ * taken of 32-bit weights, whatever the v_scale, as long as those that a query sees are at most 2^104
+ * apart (f16 values have scales from 2^-96 to 2^8); beyond that, tokens of the smaller scale may be
+ * missing from it. */
 size_t vocoder_lm_attention_ws_bytes(int n_seq, int max_q, int heads, int kv_heads, int head_dim,
                                      int max_kv, int window);
 voc_status vocoder_lm_attention(const void *q, long long ldq, long long hsq, int dtype, int heads,

@@ -92,3 +92,20 @@ def test_attention_largest_queries(d, new):
     q[0, 1, 5] = 2.0 ** 126
     q[1] *= 2.0 ** -3
     T._check_attention(bt, torch.from_numpy(q).cuda().bfloat16(), scale=2.0 ** -49)
+
+
+@pytest.mark.parametrize("top", [0, 4, 8])
+@pytest.mark.parametrize("d,heads", [(64, 2), (128, 1), (128, 12)])
+@pytest.mark.parametrize("new", [[1, 1, 1], [1, 130, 20]])
+def test_attention_value_scales_at_both_ends(top, d, heads, new):
+    """Blocks of the smallest value scale (zeros have it) beside blocks of scales up to the largest of
+    f16 values: the former add nothing to the sum of values, and all of their weight to the sum of
+    weights.  (What the header leaves open starts 2^104 apart.)"""
+    bt = T.Batch([500, 130, 300], new, 1, d, seed=4)
+    e = np.where(bt.rng.random(bt.vs.shape) < 0.5, -96, bt.rng.integers(top - 4, top + 1, bt.vs.shape))
+    e[bt.table[0, 0]], e[bt.table[1, 0]], e[bt.table[2, 0]] = -96, top, -96
+    e[bt.table[0, 1]], e[bt.table[1, 1]], e[bt.table[2, 1]] = top, -96, top
+    bt.vs = np.exp2(e).astype(np.float32)
+    bt.cache.v_scale.copy_(torch.from_numpy(bt.vs).cuda())
+    T._check_attention(bt, T._queries(bt, heads))
+    T._check_attention(bt, T._queries(bt, heads), max_kv=4000)
