@@ -779,12 +779,12 @@ def _lm_setup():
     # the current stream as an integer, without building a Stream object where torch allows it
     _LM.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                              lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-    if os.path.exists(_build.TORCH_LIB):
+    if os.path.exists(_build.torch_lib()):
         import importlib.machinery
         import importlib.util
-        loader = importlib.machinery.ExtensionFileLoader("lm_torch", _build.TORCH_LIB)
+        loader = importlib.machinery.ExtensionFileLoader("lm_torch", _build.torch_lib())
         fast = importlib.util.module_from_spec(
-            importlib.util.spec_from_file_location("lm_torch", _build.TORCH_LIB, loader=loader))
+            importlib.util.spec_from_file_location("lm_torch", _build.torch_lib(), loader=loader))
         loader.exec_module(fast)
         fast.init(*(ctypes.cast(f, ctypes.c_void_p).value
                     for f in (_LM.rows, _LM.linear, _LM.append, _LM.attention,

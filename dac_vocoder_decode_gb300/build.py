@@ -1,5 +1,7 @@
-"""In-tree build of the CUDA library libvocoder.so (sm_103a only) and of lm_torch.so, the compiled
-binding of the 8-bit operators for torch tensors.
+"""In-tree build of the CUDA library libvocoder.so (sm_103a only) and of lm_torch, the compiled
+binding of the 8-bit operators for torch tensors.  The library does not need the binding: where that
+cannot be built (no C++ compiler, a torch without CUDA), the build says so and goes on, and the
+operators are marshalled in Python.
 
     python -m dac_vocoder_decode_gb300.build            # build if sources changed
     python -m dac_vocoder_decode_gb300.build --force    # rebuild
@@ -14,6 +16,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,7 +24,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libvocoder.so")
-TORCH_LIB = os.path.join(LIBDIR, "lm_torch.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -34,16 +36,32 @@ def nvcc() -> str:
 
 
 def sources():
+    """What libvocoder.so is made of."""
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
-                  glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(INCLUDE, "*.h")))
+                  glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def torch_sources():
+    """What the compiled binding is made of."""
+    return sorted(glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def newer(built: str, made_of) -> bool:
+    """Whether `built` is there and no older than its sources."""
+    if not os.path.exists(built):
+        return False
+    t = os.path.getmtime(built)
+    return all(os.path.getmtime(s) <= t for s in made_of)
+
+
+def torch_up_to_date() -> bool:
+    """Whether the compiled binding is as good as it gets: built, tried in vain, or not wanted."""
+    return torch_dir() is None or any(newer(f, torch_sources())
+                                      for f in (torch_lib(), torch_lib() + ".failed"))
 
 
 def up_to_date() -> bool:
-    built = [LIB] + ([TORCH_LIB] if torch_dir() else [])
-    if not all(os.path.exists(b) for b in built):
-        return False
-    t = min(os.path.getmtime(b) for b in built)
-    return all(os.path.getmtime(s) <= t for s in sources())
+    return newer(LIB, sources()) and torch_up_to_date()
 
 
 def torch_dir():
@@ -53,8 +71,12 @@ def torch_dir():
     return where[0] if where else None
 
 
+def torch_lib() -> str:
+    return os.path.join(LIBDIR, "lm_torch.so")
+
+
 def torch_command(out: str):
-    """The compiler call for lm_torch.so."""
+    """The compiler call for the compiled binding."""
     t = torch_dir()
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
@@ -65,38 +87,70 @@ def torch_command(out: str):
             "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath," + os.path.join(t, "lib")]
 
 
+def start(command):
+    """A compiler at work beside the others, or the reason why it did not start."""
+    try:
+        return subprocess.Popen(command(), stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    except (OSError, RuntimeError) as e:
+        return str(e)
+
+
+def finish(job):
+    """(whether it succeeded, what it said)"""
+    if isinstance(job, str):
+        return False, job
+    log = job.communicate()[0]
+    return job.returncode == 0, log
+
+
 def build(force: bool = False, verbose: bool = False, extra=None) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(LIBDIR, exist_ok=True)
+    library = force or not newer(LIB, sources())
+    binding = torch_dir() is not None and (force or not torch_up_to_date())
     tmp = LIB + f".tmp{os.getpid()}"
-    base = [nvcc(), *(extra or []), *(["-Xptxas=-v"] if verbose else []), *ARCH_FLAGS, "-O3",
-            "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden", "-I", INCLUDE,
-            "-I", CSRC]
+    torch_tmp = LIB + f".torch.tmp{os.getpid()}"
+
+    def compile_unit(unit, obj):
+        return [nvcc(), *(extra or []), *(["-Xptxas=-v"] if verbose else []), *ARCH_FLAGS, "-O3",
+                "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden", "-I", INCLUDE,
+                "-I", CSRC, "-c", "-o", obj, unit]
+
     # one object per source file, compiled side by side
-    units = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    units = sorted(glob.glob(os.path.join(CSRC, "*.cu"))) if library else []
     objs = [f"{tmp}.{os.path.basename(u)}.o" for u in units]
-    torch_tmp = TORCH_LIB + f".tmp{os.getpid()}"
     try:
-        cmds = [[*base, "-c", "-o", o, u] for u, o in zip(units, objs)]
-        if torch_dir():
-            cmds.append(torch_command(torch_tmp))
-        procs = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
-                 for c in cmds]
-        logs = [p.communicate()[0] for p in procs]
-        failed = any(p.returncode for p in procs)
-        if not failed:
-            res = subprocess.run([nvcc(), *ARCH_FLAGS, "-shared", "-o", tmp, *objs],
-                                 capture_output=True, text=True)
-            logs.append(res.stdout + res.stderr)
-            failed = res.returncode != 0
-        if failed or verbose:
-            sys.stderr.write("".join(logs))
-        if failed:
-            raise RuntimeError("building libvocoder.so or lm_torch.so failed")
-        os.replace(tmp, LIB)
-        if torch_dir():
-            os.replace(torch_tmp, TORCH_LIB)
+        torch_job = start(lambda: torch_command(torch_tmp)) if binding else None
+        jobs = [start(lambda: compile_unit(u, o)) for u, o in zip(units, objs)]
+        done = [finish(j) for j in jobs]
+        if binding:
+            ok, log = finish(torch_job)
+            if verbose:
+                sys.stderr.write(log)
+            failed = torch_lib() + ".failed"
+            if ok:
+                os.replace(torch_tmp, torch_lib())
+                if os.path.exists(failed):
+                    os.remove(failed)
+            else:
+                if os.path.exists(torch_lib()):  # of other sources than the library's
+                    os.remove(torch_lib())
+                with open(failed, "w") as f:  # not tried again until a source or torch changes
+                    f.write(log)
+                warnings.warn("the compiled binding for torch tensors was not built; the 8-bit operators "
+                              f"are marshalled in Python ({failed} has the compiler's words)",
+                              RuntimeWarning, stacklevel=2)
+        if library:
+            if all(ok for ok, _ in done):
+                done.append(finish(start(
+                    lambda: [nvcc(), *ARCH_FLAGS, "-shared", "-o", tmp, *objs])))
+            failed = not all(ok for ok, _ in done)
+            if failed or verbose:
+                sys.stderr.write("".join(log for _, log in done))
+            if failed:
+                raise RuntimeError("nvcc failed building libvocoder.so")
+            os.replace(tmp, LIB)
     finally:
         for f in [*objs, tmp, torch_tmp]:
             if os.path.exists(f):
