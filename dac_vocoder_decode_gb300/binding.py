@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 from typing import List, Optional, Sequence
 
 import numpy as np
@@ -758,12 +759,33 @@ class Encoder:
 # ------------------------------------------------------------------ 8-bit operators
 # One call of these is a few microseconds of host time beside kernels of the same length, so the
 # checks below stay with what is cheap to ask of a tensor; the library checks the rest.
-# The regular calls go through lm_torch.so (csrc/lm_torch.cpp), which marshals them in a fraction of
+# The regular calls go through lm_torch (csrc/lm_torch.cpp), which marshals them in a fraction of
 # that; it hands back None where something is unusual or wrong, and the code here takes over.
 class _LM:
     """What the wrappers need of torch and the library, looked up with the first call."""
     ready = False
     fast = None
+
+
+def _lm_compiled():
+    """The compiled binding, or None where there is none for this Python and torch."""
+    import importlib.machinery
+    import importlib.util
+    path = _build.torch_lib()
+    if not os.path.exists(path):
+        return None
+    loader = importlib.machinery.ExtensionFileLoader("lm_torch", path)
+    try:
+        fast = importlib.util.module_from_spec(
+            importlib.util.spec_from_file_location("lm_torch", path, loader=loader))
+        loader.exec_module(fast)
+    except (ImportError, OSError) as e:
+        warnings.warn(f"{path} does not load ({e}); the 8-bit operators are marshalled in Python",
+                      RuntimeWarning, stacklevel=2)
+        return None
+    fast.init(*(ctypes.cast(f, ctypes.c_void_p).value
+                for f in (_LM.rows, _LM.linear, _LM.append, _LM.attention, _LM.attention_ws)))
+    return fast
 
 
 def _lm_setup():
@@ -779,17 +801,7 @@ def _lm_setup():
     # the current stream as an integer, without building a Stream object where torch allows it
     _LM.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                              lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-    if os.path.exists(_build.torch_lib()):
-        import importlib.machinery
-        import importlib.util
-        loader = importlib.machinery.ExtensionFileLoader("lm_torch", _build.torch_lib())
-        fast = importlib.util.module_from_spec(
-            importlib.util.spec_from_file_location("lm_torch", _build.torch_lib(), loader=loader))
-        loader.exec_module(fast)
-        fast.init(*(ctypes.cast(f, ctypes.c_void_p).value
-                    for f in (_LM.rows, _LM.linear, _LM.append, _LM.attention,
-                              _LM.attention_ws)))
-        _LM.fast = fast
+    _LM.fast = _lm_compiled()
     _LM.ready = True
 
 

@@ -12,6 +12,7 @@ import argparse
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -71,8 +72,19 @@ def torch_dir():
     return where[0] if where else None
 
 
+def torch_version() -> str:
+    """The installed torch's version (read, not imported)."""
+    try:
+        with open(os.path.join(torch_dir(), "version.py")) as f:
+            found = re.search(r"""^__version__[^=\n]*=\s*['"]([^'"\n]+)""", f.read(), re.M)
+    except OSError:
+        found = None
+    return found.group(1) if found else "unknown"
+
+
 def torch_lib() -> str:
-    return os.path.join(LIBDIR, "lm_torch.so")
+    """The compiled binding for this Python and this torch: with others it is another file."""
+    return os.path.join(LIBDIR, f"lm_torch.{sysconfig.get_config_var('SOABI')}.{torch_version()}.so")
 
 
 def torch_command(out: str):

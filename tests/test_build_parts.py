@@ -80,3 +80,16 @@ def test_a_failing_library_still_raises(place, monkeypatch):
     with pytest.raises(RuntimeError, match="libvocoder"):
         B.build()
     assert not os.path.exists(B.LIB)
+
+
+def test_the_binding_is_for_one_python_and_torch(place):
+    B.build()
+    first = B.torch_lib()
+    place.ran()
+    (place.path / "version.py").write_text("__all__ = ['__version__', 'cuda']\n__version__: str = '9.2.0'\n")
+    assert B.torch_version() == "9.2.0"
+    assert not os.path.exists(B.torch_lib()) and not B.up_to_date()
+    B.build()
+    assert place.ran() and os.path.exists(B.torch_lib()) and B.torch_lib() != first
+    (place.path / "version.py").unlink()
+    assert "unknown" in B.torch_lib()
