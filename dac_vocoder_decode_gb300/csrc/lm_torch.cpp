@@ -66,6 +66,16 @@ PyObject *wrap(PyObject *given, const at::Tensor &made) {
 }
 PyObject *status(voc_status st) { return PyLong_FromLong(st); }
 
+// A call of the library without the interpreter's lock: with VOC_FLAG_SYNC it waits for the stream, and
+// a launch may wait for room in the queue, both possibly for what another Python thread has yet to do.
+template <typename F, typename... Args>
+voc_status unlocked(F call, Args... args) {
+  PyThreadState *state = PyEval_SaveThread();
+  const voc_status st = call(args...);
+  PyEval_RestoreThread(state);
+  return st;
+}
+
 // rows(x, mode, weight, residual, eps, sum_out, out, scale, flags)
 PyObject *rows(PyObject *, PyObject *const *a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -100,12 +110,12 @@ PyObject *rows(PyObject *, PyObject *const *a, Py_ssize_t n) {
   }
   if (!sc) scale = make({count}, at::kFloat, dev);
   const voc_status st =
-      g_rows(x->data_ptr(), ldx, r ? r->data_ptr() : nullptr, ldr, w ? w->data_ptr() : nullptr, code,
-             static_cast<int>(mode), count, static_cast<int>(d), static_cast<float>(eps),
-             s ? s->data_ptr() : r ? sum.data_ptr() : nullptr, lds,
-             o ? o->data_ptr() : out.data_ptr(), ldo,
-             static_cast<float *>(sc ? sc->data_ptr() : scale.data_ptr()), stream_of(dev),
-             static_cast<unsigned>(flags));
+      unlocked(g_rows, x->data_ptr(), ldx, r ? r->data_ptr() : nullptr, ldr,
+               w ? w->data_ptr() : nullptr, code, static_cast<int>(mode), count, static_cast<int>(d),
+               static_cast<float>(eps), s ? s->data_ptr() : r ? sum.data_ptr() : nullptr, lds,
+               o ? o->data_ptr() : out.data_ptr(), ldo,
+               static_cast<float *>(sc ? sc->data_ptr() : scale.data_ptr()), stream_of(dev),
+               static_cast<unsigned>(flags));
   if (st != VOC_OK) return status(st);
   PyObject *res = PyTuple_New(3);
   if (!res) return nullptr;
@@ -151,8 +161,8 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
                code == VOC_LM_BF16 ? at::kBFloat16 : code == VOC_LM_F16 ? at::kHalf : at::kFloat,
                dev);
   }
-  const voc_status st = g_linear(
-      x->data_ptr(), ldx, static_cast<float *>(xs->data_ptr()), w->data_ptr(), ldw,
+  const voc_status st = unlocked(
+      g_linear, x->data_ptr(), ldx, static_cast<float *>(xs->data_ptr()), w->data_ptr(), ldw,
       static_cast<float *>(ws->data_ptr()), b ? static_cast<float *>(b->data_ptr()) : nullptr,
       static_cast<int>(M), static_cast<int>(N), static_cast<int>(K),
       o ? o->data_ptr() : out.data_ptr(), ldo, static_cast<int>(code), stream_of(dev),
@@ -242,8 +252,8 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
       k->stride(2) != 1 || v->stride(2) != 1 || k->size(0) > 0x7fffffff || max_q > 0x7fffffff ||
       max_q < 0 || !b.read(a[3], a[4], a[5], dev))
     Py_RETURN_NONE;
-  const voc_status st = g_append(
-      c.at<void>(0), c.at<void>(1), c.at<float>(2), c.at<float>(3), static_cast<int>(c.pages),
+  const voc_status st = unlocked(
+      g_append, c.at<void>(0), c.at<void>(1), c.at<float>(2), c.at<float>(3), static_cast<int>(c.pages),
       static_cast<int>(c.heads), static_cast<int>(c.d), k->data_ptr(), k->stride(0), k->stride(1),
       v->data_ptr(), v->stride(0), v->stride(1), code, b.table, b.ldt, b.cols, b.lens, b.cu, b.n_seq,
       static_cast<int>(k->size(0)), static_cast<int>(max_q), stream_of(dev),
@@ -296,8 +306,8 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
   }
   const at::Tensor &dst = o ? *o : out;
-  const voc_status st = g_attention(
-      q->data_ptr(), q->stride(0), q->stride(1), code, heads, c.at<void>(0), c.at<void>(1),
+  const voc_status st = unlocked(
+      g_attention, q->data_ptr(), q->stride(0), q->stride(1), code, heads, c.at<void>(0), c.at<void>(1),
       c.at<float>(2), c.at<float>(3), static_cast<int>(c.pages), static_cast<int>(c.heads),
       static_cast<int>(c.d), b.table, b.ldt, b.cols, b.lens, b.cu, b.n_seq,
       static_cast<int>(q->size(0)), static_cast<int>(max_q), static_cast<int>(max_kv),

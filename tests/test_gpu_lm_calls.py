@@ -2,6 +2,9 @@
 them that take long, streams, defaults, threads."""
 from __future__ import annotations
 
+import threading
+import time
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -145,3 +148,37 @@ def test_one_token_each_is_the_default_without_cu_q():
     with pytest.raises(V.VocoderError) as e:
         V.attention_fp8(torch.cat([q, q]), bt.cache, **batch)
     assert e.value.status == V.VOC_INVALID_ARG
+
+
+# ------------------------------------------------------------------ threads
+@pytest.mark.parametrize("op", ["rows", "linear", "append", "attention"])
+def test_other_threads_run_while_a_call_waits_for_its_stream(op):
+    """A call with VOC_FLAG_SYNC behind half a second of work: the interpreter stays free."""
+    x = torch.randn(4, 256, device="cuda").bfloat16()
+    x8, xs, _ = V.rows_fp8(x, V.VOC_LM_NONE)
+    bt = T.Batch([70, 9], [1, 1], 2, 64)
+    q = T._queries(bt, 4)
+    k = torch.zeros(2, 2, 64, device="cuda").bfloat16()
+    call = dict(rows=lambda: V.rows_fp8(x, V.VOC_LM_NONE, flags=SYNC),
+                linear=lambda: V.linear_fp8(x8, xs, x8, xs, flags=SYNC),
+                append=lambda: V.kv_append_fp8(bt.cache, k, k, flags=SYNC, **bt.args()),
+                attention=lambda: V.attention_fp8(q, bt.cache, flags=SYNC, **bt.args()))[op]
+    call()
+    waited = []
+
+    def wait():
+        torch.cuda._sleep(1_000_000_000)
+        start = time.perf_counter()
+        call()
+        waited.append(time.perf_counter() - start)
+
+    thread = threading.Thread(target=wait)
+    thread.start()
+    last, gap = time.perf_counter(), 0.0
+    while thread.is_alive():
+        time.sleep(0.005)
+        now = time.perf_counter()
+        gap, last = max(gap, now - last), now
+    thread.join()
+    assert waited and waited[0] > 0.25
+    assert gap < 0.2
