@@ -1,5 +1,5 @@
 """GPU: the 8-bit operators' kernels for many tokens and long caches, over what only large sizes
-reach: rings that wrap, further tiles of a pair, tiles in many parts.
+reach: rings that wrap, further tiles of a pair, scales handed over in groups, tiles in many parts.
 
 Tolerances are those of tests/test_gpu_lm.py.  The attention's 64-bit reference is taken on the GPU
 in plain products (`_reference`), by the same definition as tests/lm_ref.py; one test holds the two
@@ -184,6 +184,42 @@ def test_the_two_references_agree():
                               window=50)
     for a, b in zip(_reference(bt, q, window=50), (ref, mag, s)):
         np.testing.assert_allclose(T._np(a), b, rtol=1e-10, atol=1e-12)
+
+
+# 20 sequences x 4 key heads: more tiles than half the SMs, so that keys are not split and one CTA
+# walks over up to 141 key tiles; 64 and 200 rows a key head (one and both tiles of 128)
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f16", 64), ("bf16", 64)])
+@pytest.mark.parametrize("rows", [64, 200])
+@pytest.mark.parametrize("window", [0, 8300])
+def test_attention_prompt_tiles_over_long_caches(tmp_path, dtype, d, rows, window):
+    lens = [9000 - 211 * i for i in range(20)]  # 141 to 78 blocks: both sides of 128 and of 96
+    bt = Pool(lens, [rows // 2] * 20, 4, d, seed=rows + d)
+    q = bt.queries(8, dtype)
+    text = _launched(tmp_path, lambda: V.attention_fp8(q, bt.cache, window=window, **bt.args()))
+    assert "attn_prompt_kernel" in text and "attn_join" not in text
+    _check(bt, q, window=window)
+
+
+def test_attention_prompt_tiles_over_long_caches_not_causal():
+    bt = Pool([8200 + 64 * i for i in range(20)], [33] * 20, 4, 64, seed=3)
+    _check(bt, bt.queries(4), causal=False)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_whole_prompt_of_many_key_tiles(d):
+    """One prompt, its last tiles over 130 key tiles."""
+    bt = Pool([8300], [8300], 2, d, seed=d)
+    _check(bt, bt.queries(4))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_prompt_tiles_in_long_parts(tmp_path, d):
+    """Parts of 60 key tiles and more, which start anywhere."""
+    bt = Pool([17000 - 150 * i for i in range(8)], [40] * 8, 4, d, seed=d)
+    q = bt.queries(8)
+    text = _launched(tmp_path, lambda: V.attention_fp8(q, bt.cache, **bt.args()))
+    assert "attn_prompt_kernel" in text and "attn_join_tiles_kernel" in text
+    _check(bt, q)
 
 
 @pytest.mark.parametrize("d,heads", [(64, 1), (128, 8), (64, 9), (128, 16)])
