@@ -311,14 +311,17 @@ voc_status encode_rows(CUtensorMap *map, const void *base, long long rows, long 
   return VOC_OK;
 }
 
-// Whether a product runs on 256 x 256 tiles of CTA pairs: above 128 tokens and with 32 such tiles or
-// more.  Measured (us, pairs / split K) at N x K = 12288 x 4096: 128 tokens 16.4 / 16.6, 256 tokens
-// 16.9 / 23.1; at 2048 x 8192: 400 tokens (16 tiles) 22.6 / 14.0; at 4096 x 4096: 400 tokens (32
-// tiles) 14.4 / 13.7.
+// Whether a product runs on 256 x 256 tiles of CTA pairs: above 128 tokens and with more than 32 such
+// tiles.  Measured (tokens x K x N, us, pairs / split K), 48 tiles: 144 x 4096 x 12288 16.6 / 17.2, 256 of
+// them 16.8 / 22.6, 700 x 4096 x 4096 15.1 / 19.3, 2000 x 1024 x 1536 8.1 / 10.6; 40: 1280 x 8192 x 2048
+// 23.5 / 32.5; 32: 300 x 4096 x 4096 14.5 / 11.6, 512 14.6 / 14.2, 1000 x 8192 x 2048 23.0 / 20.0, 144 x
+// 1024 x 8192 7.7 / 7.0, but 256 of them 7.9 / 9.7; 24: 700 x 8192 x 2048 22.9 / 18.6, but 1000 x 1024 x
+// 1536 7.6 / 9.1; 16: 256 x 4096 x 4096 14.2 / 11.3.  (With few chunks of K the pairs win from about 18
+// tiles on.)
 bool many_tokens(int M, int N) {
   const long long jobs = static_cast<long long>((M + voc::kManyTile - 1) / voc::kManyTile) *
                          ((N + voc::kManyTile - 1) / voc::kManyTile);
-  return M > 128 && jobs >= 32;
+  return M > 128 && jobs > 32;
 }
 
 template <typename T>
@@ -385,7 +388,7 @@ VOC_API voc_status vocoder_lm_linear_fp8(const void *x8, long long ldx, const fl
     if (e != cudaSuccess) return cuda_fail(e, "launch linear");
     return finish(*dev, stream, flags);
   }
-  // Equal tiles of up to 256 tokens (few: fewer than 32 of 256 x 256), down to 32 as long as all their
+  // Equal tiles of up to 256 tokens (few: up to 32 of 256 x 256), down to 32 as long as all their
   // parts of K have SMs: a tile's way out grows with its tokens.  Measured (tokens x K x N, us, as large
   // as they go / so): 444 x 592 x 65 8.9 / 4.3, 172 x 1536 x 694 8.0 / 5.7, 500 x 4096 x 256 10.5 / 6.5.
   const int n_tiles = (N + voc::kLinRows - 1) / voc::kLinRows;

@@ -55,9 +55,9 @@ def _operands(m, k, n, bias, seed):
 
 
 # 289 tiles on 76 pairs of SMs and 8 chunks of K, the last one ragged; 45 tiles and 13 chunks; 102
-# tiles of one chunk more than the ring holds; 32 tiles, the fewest, and one short chunk
+# tiles of two chunks more than the ring holds; 33 tiles, the fewest, and one short chunk
 MANY = [(4100, 1000, 4200, True), (2100, 1537, 1030, False), (4100, 900, 1300, True),
-        (2000, 70, 900, True)]
+        (2700, 70, 700, True)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
