@@ -21,8 +21,8 @@ constexpr int kPrRows = 256;      // rows of a tile of the prompt kernel
 constexpr int kFlatTiles = 512;   // sequences up to which its CTAs count through the tiles
 constexpr int kShareMin = 4;      // units of the smallest share
 // Units that a tile counts beside its blocks, for what its first and last steps take.  Measured with 0,
-// 4, 8 and 16: 16 sequences of 1 to 10012 tokens 61.2, 23.5, 20.7 and 20.9 us, 8 of 4000 with 16 rows
-// 31.0, 28.7, 26.1 and 27.1.
+// 4, 8 and 16: 16 sequences of 1 to 10012 tokens 61.5, 24.9, 22.2 and 22.5 us, 8 of 4000 with 16 rows
+// 32.0, 29.9, 27.4 and 28.2.
 constexpr int kTileCost = 8;
 
 struct LmAttnArgs {
@@ -161,8 +161,8 @@ struct Segment {
 // lengths, and a tile that several CTAs share is joined by attn_join_kernel.  Two CTAs per SM.
 //
 // Bound by the cache's bytes: 8 sequences of 15504 tokens, 8 key heads of 128 channels (254 MB), 4
-// queries a head: 46 us with the join, 5.5 TB/s; in its middle the kernel reads about 7, and some
-// 9 us are the launch, the first blocks' way in, CTAs that end at different times, and the join.  With
+// queries a head: 48 us with the join, 5.3 TB/s; in its middle the kernel reads about 7, and some
+// 11 us are the launch, the first blocks' way in, CTAs that end at different times, and the join.  With
 // 16-row tiles the same call took 59 us (twice the products and registers): 8 rows and fewer have
 // tiles of their own.  With the products the other way round and a fixed split of each tile it took
 // 76 us.  One sequence of 250 tokens: 4.2 us, latency.
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(const LmAttn
 }
 
 // Joins the parts of a row kernel's tile, one CTA of D threads per row, a channel each.  Bound by its
-// chain of reads: with barriers and the values read after the maxima it took 3 us more.
+// chain of reads, lengths, maxima and values: with barriers between the latter it took 3 us more.
 template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(D) attn_join_kernel(const LmAttnArgs p) {
   constexpr int kWarps = D / 32;

@@ -202,7 +202,7 @@ cudaError_t launch_rows_ch(int tpr, const voc::LmRowsArgs &a, voc_stream_t strea
 
 // As many vectors per thread as the row needs, up to kRowValues values, in steps of an eighth of these
 // (a vector where that is more; vectors that hold nothing cost instructions all the same: a row of 4100
-// takes 18.8 us with 5 vectors of 4 a thread, 19.3 with 6).  `d`: values that the vectors have to cover.
+// takes 19.3 us with 5 vectors of 4 a thread, 20.9 with 6).  `d`: values that the vectors have to cover.
 template <typename T, int MODE, int VB, bool ANY, int CH>
 cudaError_t launch_rows_need(int need, int tpr, const voc::LmRowsArgs &a, voc_stream_t stream) {
   constexpr int step = std::max(1, voc::kRowValues / (VB / static_cast<int>(sizeof(T))) / 8);
@@ -508,21 +508,21 @@ namespace {
 
 // From kPromptRows rows (queries that share a key head) of a sequence the attention runs on tiles of
 // 256 rows (prompt kernel), below on tiles of 8 or 16 (row kernel).  Measured, 8 sequences of 4000
-// tokens, 8 heads of 128 channels (us, row / prompt kernel): 16 rows 25.8 / 39.1, 32 rows 39.0 / 40.1,
-// 36 rows 49.3 / 40.3; 8 of 15504: 32 rows 104 / 125, 36 rows 144 / 125; one of 15504: 32 rows 23.8 /
-// 25.2, 36 rows 28.0 / 25.4.
+// tokens, 8 heads of 128 channels (us, row / prompt kernel): 16 rows 27.2 / 40.0, 32 rows 40.0 / 41.3,
+// 36 rows 51.2 / 41.4; 8 of 15504: 32 rows 105 / 126, 36 rows 145 / 127; one of 15504: 32 rows 25.6 /
+// 25.8, 36 rows 29.9 / 26.0.
 // Up to kShortBlocks blocks of keys the row kernel takes more rows too, as long as all its tiles run at
 // once: the prompt kernel has about 10 us before its first and after its last product.  Measured, 256
 // rows x 4 heads of 128 channels: 500 tokens 10.7 / 19.8, 1000 tokens 15.1 / 20.0; 64 rows x 16 heads:
-// 1000 tokens 15.1 / 13.0, 2000 tokens (beyond the limit) 17.9 / 15.2; tiles for two turns, 300 rows x
+// 1000 tokens 15.1 / 18.4, 2000 tokens (beyond the limit) 24.1 / 15.8; tiles for two turns, 300 rows x
 // 8 heads, 4 queries each, 1000 tokens: 34.2 / 25.0.
 constexpr int kPromptRows = 33;
 constexpr int kShortBlocks = 16;
 // A tile of the row kernel is a CTA's, unless equal shares of all units (kTileCost) spare the busiest
 // CTA this many: a share that starts inside a tile and the join of its parts cost about as much.
-// Measured (us, whole tiles / shares), 128 tiles of 64 channels: 16 blocks 7.9 / 10.7, 32 blocks 13.3 /
-// 13.2, 63 blocks 23.8 / 18.8; 16 tiles: 16 blocks 7.9 / 7.0, 32 blocks 12.8 / 7.5; 256 tiles of 128
-// channels: 16 blocks 15.8 / 21.5, 63 blocks 43.1 / 48.7; 16 sequences of 1 to 10012 tokens 65.5 / 20.7.
+// Measured (us, whole tiles / shares), 128 tiles of 64 channels: 16 blocks 8.0 / 11.6, 32 blocks 13.6 /
+// 14.2, 63 blocks 24.0 / 19.6; 16 tiles: 16 blocks 7.9 / 8.0, 32 blocks 12.8 / 8.3; 256 tiles of 128
+// channels: 16 blocks 15.9 / 23.1, 63 blocks 43.2 / 50.6; 16 sequences of 1 to 10012 tokens 65.4 / 22.2.
 constexpr int kShareGain = 20;
 
 struct AttnPlan {
@@ -542,9 +542,9 @@ size_t part_bytes(size_t slots, int head_dim) { return slots * (head_dim * sizeo
 // Row kernel: a CTA per tile, or equal shares for two CTAs per SM (kShareGain).  Prompt kernel: long
 // keys are split while there are fewer tiles than SMs, into parts of 4 blocks or more, and no more than
 // 1.5 sqrt(blocks) of them, beyond which the parts' join costs what the shorter parts save.  Measured,
-// 256 rows x 4 heads: 1100 tokens whole 27.9, 2 parts 24.9, 4 parts 20.4 us; 8000 tokens whole 124, 15
-// parts 26.4, 17 25.6; 64 rows, 16000 tokens: 23 parts 21.8, 31 22.4; 8 chunks over a window of 250 (8
-// blocks): whole 15.0, 2 parts 18.0.
+// 256 rows x 4 heads: 1100 tokens whole 28.1, 2 parts 25.4, 4 parts 20.9 us; 8000 tokens whole 123, 15
+// parts 27.0, 17 26.2; 64 rows, 16000 tokens: 23 parts 21.9, 31 22.1; 8 chunks over a window of 250 (8
+// blocks): whole 15.2, 2 parts 18.7.
 // Its CTAs look for their tiles, which n_tokens bounds, so that sequences with few new tokens cost
 // none (flat_tiles); splits grow as n_tokens falls, and parts are never more than one per SM.
 AttnPlan plan_attention(int sms, int n_seq, long long n_tokens, int max_q, int heads, int kv_heads,
