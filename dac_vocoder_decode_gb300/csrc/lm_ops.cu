@@ -14,38 +14,23 @@
 #include "vocoder.h"
 #include "lm_attention.cuh"
 #include "lm_cache.cuh"
+#include "lm_host.cuh"
 #include "lm_linear.cuh"
 #include "lm_prompt.cuh"
 #include "lm_rows.cuh"
-
-#define VOC_API extern "C" __attribute__((visibility("default")))
 
 namespace voc {
 std::string &last_error_slot();  // vocoder.cu: the thread's error without a context
 }
 
+using namespace voc::lm;
+
 namespace {
 
 constexpr long long kWaitBudget = 4000000000LL;  // cycles (~2 s) before a wait gives up
-constexpr int kMaxDevices = 64;
 
 // Set by a kernel that gave up a wait; read and cleared by calls with VOC_FLAG_SYNC.
 __device__ int g_timeout;
-
-voc_status fail(voc_status st, const char *msg) noexcept {
-  try {
-    voc::last_error_slot() = msg;
-  } catch (...) {
-  }
-  return st;
-}
-voc_status cuda_fail(cudaError_t e, const char *what) noexcept {
-  try {
-    voc::last_error_slot() = std::string(what) + ": " + cudaGetErrorString(e);
-  } catch (...) {
-  }
-  return e == cudaErrorMemoryAllocation ? VOC_OOM : VOC_CUDA_ERROR;
-}
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
@@ -60,21 +45,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-struct Device {
-  std::once_flag once;
-  cudaError_t err = cudaSuccess;
-  int sms = 0;
-  int *timeout = nullptr;
-  int clusters[9] = {};  // clusters of 1..8 CTAs of the split-K product that run at once
-};
 Device g_devices[kMaxDevices];
 
-template <typename K>
-void allow_smem(cudaError_t &e, K kernel, size_t bytes) {
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(bytes));
-}
 constexpr size_t kLinSmem = 220 * 1024;       // one CTA of the split-K product on an SM
 constexpr size_t kLinSmemTwo = 108 * 1024;    // two
 
@@ -95,7 +67,26 @@ cudaError_t count_clusters(int *out, K kernel, int threads, size_t smem, int siz
   return cudaOccupancyMaxActiveClusters(out, kernel, &cfg);
 }
 
-// The current device, set up on first use (shared-memory limits of the kernels, SM count).
+}  // namespace
+
+namespace voc {
+namespace lm {
+
+voc_status fail(voc_status st, const char *msg) noexcept {
+  try {
+    voc::last_error_slot() = msg;
+  } catch (...) {
+  }
+  return st;
+}
+voc_status cuda_fail(cudaError_t e, const char *what) noexcept {
+  try {
+    voc::last_error_slot() = std::string(what) + ": " + cudaGetErrorString(e);
+  } catch (...) {
+  }
+  return e == cudaErrorMemoryAllocation ? VOC_OOM : VOC_CUDA_ERROR;
+}
+
 voc_status device(Device **out) {
   int d = 0;
   cudaError_t e = cudaGetDevice(&d);
@@ -136,32 +127,6 @@ voc_status device(Device **out) {
   return VOC_OK;
 }
 
-// Launch with programmatic stream serialization (see pdl_wait), in clusters of `cluster` CTAs
-// along z where that is above 1.
-template <typename... KArgs, typename... Args>
-cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, int cluster,
-                   voc_stream_t stream, const Args &...args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cluster > 1) {
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 1;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = cluster;
-    cfg.numAttrs = 2;
-  }
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-// With VOC_FLAG_SYNC: wait for the stream and report a kernel that gave up a wait.
 voc_status finish(const Device &dev, voc_stream_t stream, unsigned flags) {
   if (!(flags & VOC_FLAG_SYNC)) return VOC_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -178,8 +143,10 @@ voc_status finish(const Device &dev, voc_stream_t stream, unsigned flags) {
   return VOC_OK;
 }
 
-bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-bool known_flags(unsigned f) { return (f & ~static_cast<unsigned>(VOC_FLAG_SYNC)) == 0; }
+}  // namespace lm
+}  // namespace voc
+
+namespace {
 
 // Threads of a row: as few as hold it in registers, and more of them while there are too few rows
 // to fill the GPU (up to a chunk of values per thread).  Measured, without / with more: 8 x 1024 2.8 /
