@@ -70,6 +70,7 @@ EXPORTED = [
     "vocoder_encoder_last_error", "vocoder_encoder_destroy",
     "vocoder_lm_rows_fp8", "vocoder_lm_linear_fp8", "vocoder_lm_kv_append",
     "vocoder_lm_attention_ws_bytes", "vocoder_lm_attention",
+    "vocoder_lm_rotate", "vocoder_lm_adapters", "vocoder_lm_logprobs",
 ]
 
 
@@ -240,6 +241,14 @@ def load_library():
     lib.vocoder_lm_attention.restype = I
     lib.vocoder_lm_attention.argtypes = [P, L, L, I, I, P, P, P, P, I, I, I, P, L, I, P, P, I, I,
                                          I, I, FL, I, I, P, L, L, P, Z, P, U]
+    lib.vocoder_lm_rotate.restype = I
+    lib.vocoder_lm_rotate.argtypes = [P, L, L, I, P, L, L, I, I, I, P, P, FL, P, L, I, P, P, I, I, L,
+                                      P, L, L, P, L, L, P, U]
+    lib.vocoder_lm_adapters.restype = I
+    lib.vocoder_lm_adapters.argtypes = [P, L, P, P, L, I, P, L, L, P, L, L, I, P, P, I, I, P, I, I, I,
+                                        P, L, P, U]
+    lib.vocoder_lm_logprobs.restype = I
+    lib.vocoder_lm_logprobs.argtypes = [P, L, I, L, I, FL, P, P, P, I, P, P, P, U]
     _lib = lib
     return lib
 
@@ -784,7 +793,8 @@ def _lm_compiled():
                       RuntimeWarning, stacklevel=2)
         return None
     fast.init(*(ctypes.cast(f, ctypes.c_void_p).value
-                for f in (_LM.rows, _LM.linear, _LM.append, _LM.attention, _LM.attention_ws)))
+                for f in (_LM.rows, _LM.linear, _LM.append, _LM.attention, _LM.attention_ws,
+                          _LM.rotate, _LM.adapters, _LM.logprobs)))
     return fast
 
 
@@ -792,12 +802,15 @@ def _lm_setup():
     import torch
     lib = load_library()
     _LM.torch, _LM.empty = torch, torch.empty
-    _LM.f8, _LM.f32, _LM.i32 = torch.float8_e4m3fn, torch.float32, torch.int32
+    _LM.f8, _LM.f32 = torch.float8_e4m3fn, torch.float32
+    _LM.i32, _LM.i64 = torch.int32, torch.int64
     _LM.types = {torch.bfloat16: VOC_LM_BF16, torch.float16: VOC_LM_F16,
                  torch.float32: VOC_LM_F32}
     _LM.rows, _LM.linear = lib.vocoder_lm_rows_fp8, lib.vocoder_lm_linear_fp8
     _LM.append, _LM.attention = lib.vocoder_lm_kv_append, lib.vocoder_lm_attention
     _LM.attention_ws = lib.vocoder_lm_attention_ws_bytes
+    _LM.rotate, _LM.adapters = lib.vocoder_lm_rotate, lib.vocoder_lm_adapters
+    _LM.logprobs = lib.vocoder_lm_logprobs
     # the current stream as an integer, without building a Stream object where torch allows it
     _LM.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                              lambda dev: torch.cuda.current_stream(dev).cuda_stream)
@@ -1112,3 +1125,173 @@ def attention_fp8(q, cache: KVCacheFP8, page_table, kv_lens, cu_q=None,
     if st:
         _check(st)
     return out
+
+
+def rotation_turns(rates):
+    """Rates in radians per position (a tensor or a sequence of them) as rotate_heads takes them: int64,
+    2^-64 of a turn, on the tensor's device.  Made once, like weights."""
+    import torch
+    r = rates.double() if torch.is_tensor(rates) else torch.tensor(rates, dtype=torch.float64)
+    r = r / (2 * np.pi)
+    r = r - r.round()  # whole turns do not count: [-1/2, 1/2]
+    return torch.where(r >= 0.5, r - 1, r).mul(2.0 ** 64).to(torch.int64)
+
+
+def _heads_ok(t, name, tokens, d, dtype, dev):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != d or t.dtype != dtype or stride[2] != 1 or \
+            t.get_device() != dev:
+        raise _bad(f"{name} must be {dtype} [{tokens}, heads, {d}] on q's device, head_dim contiguous")
+    return t.data_ptr(), stride[0], stride[1], shape[1]
+
+
+def rotate_heads(q, k, positions, turns, axis=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 neighbours: bool = False, q_out=None, k_out=None, stream=None, flags: int = 0):
+    """Queries q [tokens, heads, d] and keys k [tokens, kv_heads, d] (or None; bf16 or f16) with the RMS
+    norm of each head (where its weight [d] is given) and turned by position (see vocoder_lm_rotate in
+    include/vocoder.h).  positions int32 [tokens] or [axes, tokens]; turns int64 [pairs] from
+    rotation_turns; axis int32 [pairs], the position axis of each pair (None: all on the first).  Returns
+    (q_out, k_out), new tensors unless given; in place with q_out=q, k_out=k."""
+    if not _LM.ready:
+        _lm_setup()
+    if stream is None and _LM.fast is not None:
+        res = _LM.fast.rotate(q, k, positions, turns, axis, q_weight, k_weight, eps, neighbours, q_out,
+                              k_out, flags)
+        if res.__class__ is tuple:
+            return res
+        if res is not None:
+            _check(res)
+    dtype, shape = q.dtype, q.shape
+    code = _LM.types.get(dtype)
+    if code is None or len(shape) != 3:
+        raise _bad("q must be a bf16 or f16 tensor [tokens, heads, head_dim]")
+    tokens, _, d = shape
+    dev = _lm_device(q)
+    q_args = _heads_ok(q, "q", tokens, d, dtype, dev)
+    made_q = made_k = None
+    if q_out is None:
+        q_out = made_q = _LM.empty(shape, dtype=dtype, device=q.device)
+    elif q_out.shape != shape:
+        raise _bad("q_out must have q's shape")
+    qo_args = _heads_ok(q_out, "q_out", tokens, d, dtype, dev)
+    if k is None:
+        if k_weight is not None or k_out is not None:
+            raise _bad("k_weight or k_out without k")
+        k_args = ko_args = (None, 0, 0, 0)
+    else:
+        k_args = _heads_ok(k, "k", tokens, d, dtype, dev)
+        if k_out is None:
+            k_out = made_k = _LM.empty(k.shape, dtype=dtype, device=q.device)
+        elif k_out.shape != k.shape:
+            raise _bad("k_out must have k's shape")
+        ko_args = _heads_ok(k_out, "k_out", tokens, d, dtype, dev)
+    qw = None if q_weight is None else _vector_ok(q_weight, "q_weight", d, dtype, dev)
+    kw = None if k_weight is None else _vector_ok(k_weight, "k_weight", d, dtype, dev)
+    if positions.dim() == 1:
+        positions = positions[None]
+    axes = positions.shape[0]
+    ldp = _rows_strides(positions, "positions", axes, tokens, _LM.i32, dev)
+    pairs = turns.numel()
+    tp = _vector_ok(turns, "turns", pairs, _LM.i64, dev)
+    ap = None if axis is None else _vector_ok(axis, "axis", pairs, _LM.i32, dev)
+    st = _LM.rotate(*q_args, *k_args, d, code, qw, kw, eps, positions.data_ptr(), ldp, axes, tp, ap,
+                    pairs, 1 if neighbours else 0, tokens, *qo_args[:3], *ko_args[:3],
+                    _lm_stream(dev, stream, (made_q, made_k)), flags)
+    if st:
+        _check(st)
+    return q_out, k_out
+
+
+def _pool_ok(t, name, pool, rows, width, dtype, dev):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != pool or shape[1] != rows or shape[2] != width or \
+            t.dtype != dtype or (stride[2] != 1 and width > 1) or t.get_device() != dev:
+        raise _bad(f"{name} must be {dtype} [{pool}, {rows}, {width}] with contiguous rows on x's device")
+    ld = stride[1] if rows > 1 else (max(width, stride[1]) + 7) // 8 * 8
+    return t.data_ptr(), ld, stride[0] if pool > 1 else 0
+
+
+def adapters_fp8(y, x, x_scale, a, b, scale, ids, ranks=None, out=None, stream=None, flags: int = 0):
+    """The projection's output y [M, N] plus each token's own low-rank adapter's of its input x [M, K]
+    float8_e4m3fn with x_scale [M], as linear_fp8 took it (see vocoder_lm_adapters in include/vocoder.h).
+    a [pool, rank, K] and b [pool, N, rank] bf16 or f16, y in their type or f32, scale fp32 [pool], ids
+    int32 [M] (outside 0..pool-1: no adapter), ranks int32 [pool] or None.  In place with out=y."""
+    if not _LM.ready:
+        _lm_setup()
+    if stream is None and _LM.fast is not None:
+        res = _LM.fast.adapters(y, x, x_scale, a, b, scale, ids, ranks, out, flags)
+        if res.__class__ is int:
+            _check(res)
+        elif res is not None:
+            return res
+    if x.dim() != 2 or y.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise _bad("x and y must be 2-d, a and b 3-d tensors")
+    M, K = x.shape
+    N = y.shape[1]
+    pool, rank, _ = a.shape
+    dev = _lm_device(x)
+    code, y_code = _LM.types.get(a.dtype), _LM.types.get(y.dtype)
+    if code is None or y_code is None:
+        raise _bad("a and b are bf16 or f16, y of their type or f32")
+    ldx = _rows_strides(x, "x", M, K, _LM.f8, dev)
+    if M == 1:
+        ldx = (ldx + 15) // 16 * 16
+    xsp = _vector_ok(x_scale, "x_scale", M, _LM.f32, dev)
+    ldy = _rows_strides(y, "y", M, N, y.dtype, dev)
+    a_args = _pool_ok(a, "a", pool, rank, K, a.dtype, dev)
+    b_args = _pool_ok(b, "b", pool, N, rank, a.dtype, dev)
+    sp = _vector_ok(scale, "scale", pool, _LM.f32, dev)
+    ip = _vector_ok(ids, "ids", M, _LM.i32, dev)
+    rp = None if ranks is None else _vector_ok(ranks, "ranks", pool, _LM.i32, dev)
+    made = None
+    if out is None:
+        out = made = _LM.empty((M, N), dtype=y.dtype, device=x.device)
+        ldo = N
+    else:
+        ldo = _rows_strides(out, "out", M, N, y.dtype, dev)
+    st = _LM.adapters(x.data_ptr(), ldx, xsp, y.data_ptr(), ldy, y_code, *a_args, *b_args, code, sp, rp,
+                      rank, pool, ip, M, N, K, out.data_ptr(), ldo, _lm_stream(dev, stream, (made,)),
+                      flags)
+    if st:
+        _check(st)
+    return out
+
+
+def logprobs(logits, tokens=None, top: int = 0, temperature: float = 1.0, entropy: bool = True,
+             stream=None, flags: int = 0):
+    """Rows of logits [rows, vocab] (bf16, f16 or f32) -> (logprob, entropy, top_logprobs, top_tokens): log
+    probabilities of tokens int64 [rows] (None without tokens), the entropies (None with entropy=False), and
+    the `top` (up to 32) likeliest tokens of each row with their log probabilities, fp32 and int64
+    [rows, top] (None with top=0); see vocoder_lm_logprobs in include/vocoder.h."""
+    if not _LM.ready:
+        _lm_setup()
+    if stream is None and _LM.fast is not None:
+        res = _LM.fast.logprobs(logits, tokens, top, temperature, entropy, flags)
+        if res.__class__ is tuple:
+            return res
+        if res is not None:
+            _check(res)
+    code = _LM.types.get(logits.dtype)
+    if code is None or logits.dim() != 2:
+        raise _bad("logits must be a 2-d bf16, f16 or f32 tensor")
+    rows, vocab = logits.shape
+    dev = _lm_device(logits)
+    ldl = _rows_strides(logits, "logits", rows, vocab, logits.dtype, dev)
+    tp = None if tokens is None else _vector_ok(tokens, "tokens", rows, _LM.i64, dev)
+    if not 0 <= top <= vocab:
+        raise _bad(f"top must lie between 0 and the {vocab} tokens")
+
+    def new(wanted, shape, dtype):
+        return _LM.empty(shape, dtype=dtype, device=logits.device) if wanted else None
+
+    lp = new(tokens is not None, (rows,), _LM.f32)
+    ent = new(entropy, (rows,), _LM.f32)
+    best, best_tokens = new(top, (rows, top), _LM.f32), new(top, (rows, top), _LM.i64)
+    made = (lp, ent, best, best_tokens)
+    st = _LM.logprobs(logits.data_ptr(), ldl, code, rows, vocab, temperature, tp,
+                      *(None if t is None else t.data_ptr() for t in made[:2]), top,
+                      *(None if t is None else t.data_ptr() for t in made[2:]),
+                      _lm_stream(dev, stream, made), flags)
+    if st:
+        _check(st)
+    return made

@@ -24,6 +24,9 @@ decltype(&vocoder_lm_linear_fp8) g_linear;
 decltype(&vocoder_lm_kv_append) g_append;
 decltype(&vocoder_lm_attention) g_attention;
 decltype(&vocoder_lm_attention_ws_bytes) g_attention_ws;
+decltype(&vocoder_lm_rotate) g_rotate;
+decltype(&vocoder_lm_adapters) g_adapters;
+decltype(&vocoder_lm_logprobs) g_logprobs;
 
 constexpr at::ScalarType kF8 = at::kFloat8_e4m3fn;
 
@@ -318,14 +321,162 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// init(addresses of rows, linear, append, attention, attention_ws)
+// One of the tensors of rotate: [tokens][heads][d] with head_dim contiguous.
+bool heads_of(const at::Tensor &t, int64_t tokens, int64_t d, at::ScalarType type, int dev) {
+  return t.dim() == 3 && t.scalar_type() == type && t.size(0) == tokens && t.size(2) == d && on(t, dev) &&
+         t.stride(2) == 1 && t.size(1) <= 65536;
+}
+
+// rotate(q, k, positions, turns, axis, q_weight, k_weight, eps, neighbours, q_out, k_out, flags)
+PyObject *rotate(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 12) Py_RETURN_NONE;
+  const at::Tensor *q = tensor(a[0]), *k = tensor(a[1]), *pos = tensor(a[2]), *turns = tensor(a[3]),
+                   *axis = tensor(a[4]), *qw = tensor(a[5]), *kw = tensor(a[6]), *qo = tensor(a[9]),
+                   *ko = tensor(a[10]);
+  const double eps = PyFloat_AsDouble(a[7]);
+  const int near = PyObject_IsTrue(a[8]);
+  const long flags = PyLong_AsLong(a[11]);
+  if (PyErr_Occurred()) return nullptr;
+  if (!q || !pos || !turns || (!k && !none(a[1])) || (!axis && !none(a[4])) || (!qw && !none(a[5])) ||
+      (!kw && !none(a[6])) || (!qo && !none(a[9])) || (!ko && !none(a[10])) || q->dim() != 3 ||
+      !q->is_cuda() || (!k && (kw || ko)) || pos->dim() < 1 || pos->dim() > 2 || turns->dim() != 1)
+    Py_RETURN_NONE;
+  const int dev = q->get_device(), code = code_of(q->scalar_type());
+  const at::ScalarType type = q->scalar_type();
+  const int64_t tokens = q->size(0), d = q->size(2), pairs = turns->size(0);
+  const int64_t axes = pos->dim() == 2 ? pos->size(0) : 1;
+  if (dev != current() || code < 0 || d > 65536 || pairs > 65536 || axes > 65536 ||
+      !heads_of(*q, tokens, d, type, dev) || (k && !heads_of(*k, tokens, d, type, dev)) ||
+      (qo && (qo->sizes() != q->sizes() || !heads_of(*qo, tokens, d, type, dev))) ||
+      (ko && (ko->sizes() != k->sizes() || !heads_of(*ko, tokens, d, type, dev))) ||
+      (qw && !vector_of(*qw, d, type, dev)) || (kw && !vector_of(*kw, d, type, dev)) ||
+      !vector_of(*turns, pairs, at::kLong, dev) || (axis && !vector_of(*axis, pairs, at::kInt, dev)))
+    Py_RETURN_NONE;
+  long long ldp = tokens;
+  if (pos->dim() == 1 ? !vector_of(*pos, tokens, at::kInt, dev)
+                      : (ldp = rows_of(*pos, axes, tokens, at::kInt, dev)) < 0)
+    Py_RETURN_NONE;
+  at::Tensor q_made, k_made;
+  if (!qo) q_made = make(q->sizes(), type, dev);
+  if (k && !ko) k_made = make(k->sizes(), type, dev);
+  const at::Tensor &qd = qo ? *qo : q_made, &kd = !k ? *q : ko ? *ko : k_made, &ks = k ? *k : *q;
+  const voc_status st = unlocked(
+      g_rotate, q->data_ptr(), q->stride(0), q->stride(1), static_cast<int>(q->size(1)),
+      k ? k->data_ptr() : nullptr, k ? ks.stride(0) : 0, k ? ks.stride(1) : 0,
+      k ? static_cast<int>(k->size(1)) : 0, static_cast<int>(d), code, qw ? qw->data_ptr() : nullptr,
+      kw ? kw->data_ptr() : nullptr, static_cast<float>(eps), static_cast<const int *>(pos->data_ptr()),
+      ldp, static_cast<int>(axes), static_cast<const long long *>(turns->data_ptr()),
+      axis ? static_cast<const int *>(axis->data_ptr()) : nullptr, static_cast<int>(pairs), near, tokens,
+      qd.data_ptr(), qd.stride(0), qd.stride(1), k ? kd.data_ptr() : nullptr, k ? kd.stride(0) : 0,
+      k ? kd.stride(1) : 0, stream_of(dev), static_cast<unsigned>(flags));
+  if (st != VOC_OK) return status(st);
+  PyObject *res = PyTuple_New(2);
+  if (!res) return nullptr;
+  PyTuple_SET_ITEM(res, 0, wrap(a[9], q_made));
+  PyTuple_SET_ITEM(res, 1, k ? wrap(a[10], k_made) : Py_NewRef(Py_None));
+  return res;
+  END_HANDLE_TH_ERRORS
+}
+
+// A pool of adapters' matrices [pool][rows][width], rows contiguous: its row stride, or -1.
+long long pool_of(const at::Tensor &t, int64_t pool, int64_t rows, int64_t width, at::ScalarType type,
+                  int dev) {
+  if (t.dim() != 3 || t.scalar_type() != type || t.size(0) != pool || t.size(1) != rows ||
+      t.size(2) != width || !on(t, dev) || (width > 1 && t.stride(2) != 1))
+    return -1;
+  return rows > 1 ? t.stride(1) : (std::max<int64_t>(width, t.stride(1)) + 7) / 8 * 8;
+}
+
+// adapters(y, x, x_scale, a, b, scale, ids, ranks, out, flags)
+PyObject *adapters(PyObject *, PyObject *const *o, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 10) Py_RETURN_NONE;
+  const at::Tensor *y = tensor(o[0]), *x = tensor(o[1]), *xs = tensor(o[2]), *a = tensor(o[3]),
+                   *b = tensor(o[4]), *scale = tensor(o[5]), *ids = tensor(o[6]), *ranks = tensor(o[7]),
+                   *out = tensor(o[8]);
+  const long flags = PyLong_AsLong(o[9]);
+  if (PyErr_Occurred()) return nullptr;
+  if (!y || !x || !xs || !a || !b || !scale || !ids || (!ranks && !none(o[7])) ||
+      (!out && !none(o[8])) || x->dim() != 2 || y->dim() != 2 || a->dim() != 3 || !x->is_cuda())
+    Py_RETURN_NONE;
+  const int dev = x->get_device();
+  const int64_t M = x->size(0), K = x->size(1), N = y->size(1), pool = a->size(0), rank = a->size(1);
+  const at::ScalarType type = a->scalar_type();
+  const int code = code_of(type), y_code = code_of(y->scalar_type());
+  constexpr int64_t kMost = 1 << 28;
+  if (dev != current() || code < 0 || y_code < 0 || M > kMost || N > kMost || K > kMost ||
+      pool > kMost || rank > kMost)
+    Py_RETURN_NONE;
+  long long ldx = rows_of(*x, M, K, kF8, dev);
+  const long long ldy = rows_of(*y, M, N, y->scalar_type(), dev);
+  const long long lda = pool_of(*a, pool, rank, K, type, dev), ldb = pool_of(*b, pool, N, rank, type, dev);
+  const long long ldo = out ? rows_of(*out, M, N, y->scalar_type(), dev) : N;
+  if (ldx < 0 || ldy < 0 || lda < 0 || ldb < 0 || ldo < 0 || !vector_of(*xs, M, at::kFloat, dev) ||
+      !vector_of(*scale, pool, at::kFloat, dev) || !vector_of(*ids, M, at::kInt, dev) ||
+      (ranks && !vector_of(*ranks, pool, at::kInt, dev)))
+    Py_RETURN_NONE;
+  if (M == 1) ldx = (ldx + 15) / 16 * 16;
+  at::Tensor made;
+  if (!out) made = make({M, N}, y->scalar_type(), dev);
+  const voc_status st = unlocked(
+      g_adapters, x->data_ptr(), ldx, static_cast<const float *>(xs->data_ptr()), y->data_ptr(), ldy,
+      y_code, a->data_ptr(), lda, pool > 1 ? a->stride(0) : 0, b->data_ptr(), ldb,
+      pool > 1 ? b->stride(0) : 0, code, static_cast<const float *>(scale->data_ptr()),
+      ranks ? static_cast<const int *>(ranks->data_ptr()) : nullptr, static_cast<int>(rank),
+      static_cast<int>(pool), static_cast<const int *>(ids->data_ptr()), static_cast<int>(M),
+      static_cast<int>(N), static_cast<int>(K), out ? out->data_ptr() : made.data_ptr(), ldo,
+      stream_of(dev), static_cast<unsigned>(flags));
+  if (st != VOC_OK) return status(st);
+  return wrap(o[8], made);
+  END_HANDLE_TH_ERRORS
+}
+
+// logprobs(logits, tokens, top, temperature, entropy, flags)
+PyObject *logprobs(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 6) Py_RETURN_NONE;
+  const at::Tensor *x = tensor(a[0]), *tokens = tensor(a[1]);
+  const long top = PyLong_AsLong(a[2]);
+  const double temperature = PyFloat_AsDouble(a[3]);
+  const int entropy = PyObject_IsTrue(a[4]);
+  const long flags = PyLong_AsLong(a[5]);
+  if (PyErr_Occurred()) return nullptr;
+  if (!x || (!tokens && !none(a[1])) || x->dim() != 2 || !x->is_cuda() || top < 0 ||
+      top > x->size(1))
+    Py_RETURN_NONE;
+  const int dev = x->get_device(), code = code_of(x->scalar_type());
+  const int64_t rows = x->size(0), vocab = x->size(1);
+  if (dev != current() || code < 0 || vocab > 0x7fffffff) Py_RETURN_NONE;
+  const long long ldl = rows_of(*x, rows, vocab, x->scalar_type(), dev);
+  if (ldl < 0 || (tokens && !vector_of(*tokens, rows, at::kLong, dev))) Py_RETURN_NONE;
+  at::Tensor made[4];
+  if (tokens) made[0] = make({rows}, at::kFloat, dev);
+  if (entropy) made[1] = make({rows}, at::kFloat, dev);
+  if (top) made[2] = make({rows, top}, at::kFloat, dev), made[3] = make({rows, top}, at::kLong, dev);
+  auto at = [&](int i) { return made[i].defined() ? made[i].data_ptr() : nullptr; };
+  const voc_status st = unlocked(
+      g_logprobs, x->data_ptr(), ldl, code, rows, static_cast<int>(vocab), static_cast<float>(temperature),
+      tokens ? static_cast<const long long *>(tokens->data_ptr()) : nullptr, static_cast<float *>(at(0)),
+      static_cast<float *>(at(1)), static_cast<int>(top), static_cast<float *>(at(2)),
+      static_cast<long long *>(at(3)), stream_of(dev), static_cast<unsigned>(flags));
+  if (st != VOC_OK) return status(st);
+  PyObject *res = PyTuple_New(4);
+  if (!res) return nullptr;
+  for (int i = 0; i < 4; ++i)
+    PyTuple_SET_ITEM(res, i, made[i].defined() ? THPVariable_Wrap(made[i]) : Py_NewRef(Py_None));
+  return res;
+  END_HANDLE_TH_ERRORS
+}
+
+// init(addresses of rows, linear, append, attention, attention_ws, rotate, adapters, logprobs)
 PyObject *init(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  if (n != 5) {
-    PyErr_SetString(PyExc_TypeError, "init takes five addresses");
+  if (n != 8) {
+    PyErr_SetString(PyExc_TypeError, "init takes eight addresses");
     return nullptr;
   }
-  void *p[5];
-  for (int i = 0; i < 5; ++i) {
+  void *p[8];
+  for (int i = 0; i < 8; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (!p[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a null address");
@@ -337,6 +488,9 @@ PyObject *init(PyObject *, PyObject *const *a, Py_ssize_t n) {
   g_append = reinterpret_cast<decltype(g_append)>(p[2]);
   g_attention = reinterpret_cast<decltype(g_attention)>(p[3]);
   g_attention_ws = reinterpret_cast<decltype(g_attention_ws)>(p[4]);
+  g_rotate = reinterpret_cast<decltype(g_rotate)>(p[5]);
+  g_adapters = reinterpret_cast<decltype(g_adapters)>(p[6]);
+  g_logprobs = reinterpret_cast<decltype(g_logprobs)>(p[7]);
   Py_RETURN_NONE;
 }
 
@@ -347,7 +501,8 @@ PyMethodDef method(const char *name, F f) {
 PyMethodDef g_methods[] = {method("init", init),         method("rows", rows),
                            method("linear", linear),     method("cache", cache),
                            method("append", append),     method("attention", attention),
-                           {nullptr, nullptr, 0, nullptr}};
+                           method("rotate", rotate),     method("adapters", adapters),
+                           method("logprobs", logprobs), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "lm_torch", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};
 

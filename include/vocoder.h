@@ -592,6 +592,59 @@ voc_status vocoder_lm_attention(const void *q, long long ldq, long long hsq, int
                                 void *out, long long ldo, long long hso, void *ws,
                                 size_t ws_bytes, voc_stream_t stream, unsigned flags);
 
+/* Three operators that a token model runs beside the four above, with their streams, errors and flags. */
+
+/* Queries q [n_tokens][heads][head_dim] and keys k [n_tokens][kv_heads][head_dim] (bf16 or f16) between
+ * the product that makes them and the cache.  For each head
+ *   n = x / sqrt(mean(x^2) + eps) * weight[i]   over its head_dim channels (weight NULL: n = x), then
+ *   (n_a, n_b) -> (n_a cos - n_b sin, n_a sin + n_b cos)   for the channels a, b of pair p,
+ * rounded once.  Pair p < pairs is channels (p, p + pairs) with neighbours = 0, (2p, 2p + 1) with 1; the
+ * channels behind the first 2 * pairs are not turned.  The angle is positions[axis[p]][token] * turns[p] in
+ * units of 2^-64 of a turn, whole turns dropped: turns[p] = rate / (2 pi) * 2^64 modulo 2^64 for a rate in
+ * radians, so that no position is too far for an exact angle.  positions int32 [axes][n_tokens] (row
+ * stride ldp), axis int32 [pairs] or NULL (all pairs on axis 0); a pair with an axis outside 0..axes-1 is
+ * not turned.  q or k may be absent (heads or kv_heads 0, NULL).  q_out and k_out may be the buffers of q
+ * and k with their strides; otherwise they do not overlap with them.  head_dim a multiple of 16 up to 256,
+ * pairs one of 8; heads, outputs and weights (of the same type) 16-byte aligned, strides multiples of 8.
+ * A head with a NaN or an infinity does not touch others. */
+voc_status vocoder_lm_rotate(const void *q, long long ldq, long long hsq, int heads, const void *k,
+                             long long ldk, long long hsk, int kv_heads, int head_dim, int dtype,
+                             const void *q_weight, const void *k_weight, float eps,
+                             const int *positions, long long ldp, int axes, const long long *turns,
+                             const int *axis, int pairs, int neighbours, long long n_tokens,
+                             void *q_out, long long ldqo, long long hsqo, void *k_out,
+                             long long ldko, long long hsko, voc_stream_t stream, unsigned flags);
+
+/* Low-rank adapters of many requests at once beside a shared projection (vocoder_lm_linear_fp8):
+ *   out[m][n] = y[m][n] + scale[i] * x_scale[m] * sum_r b[i][n][r] sum_k a[i][r][k] x8[m][k],  i = ids[m],
+ * rounded once; out[m] = y[m] for a token whose id is outside 0..pool-1 or whose adapter has rank 0.  x8
+ * [M][K] as the projection takes it; a [pool][rank][K] (row stride lda, sa from one adapter to the next) and
+ * b [pool][N][rank] (ldb, sb) bf16 or f16 (dtype), 16-byte aligned, strides multiples of 8; y and out [M][N]
+ * in the adapters' type or f32, out may be y (same stride) and otherwise does not overlap with it; scale
+ * fp32 [pool]; ids int32 [M] in any order.  rank: a multiple of 8 up to 128; ranks int32 [pool] or NULL: the
+ * rank of each adapter (0 to rank), what lies behind it in a and b is not used.  Sums are 32-bit; the
+ * low-rank values keep 16 (bf16) or 22 (f16) bits between the products. */
+voc_status vocoder_lm_adapters(const void *x8, long long ldx, const float *x_scale, const void *y,
+                               long long ldy, int y_dtype, const void *a, long long lda, long long sa,
+                               const void *b, long long ldb, long long sb, int dtype,
+                               const float *scale, const int *ranks, int rank, int pool,
+                               const int *ids, int M, int N, int K, void *out, long long ldo,
+                               voc_stream_t stream, unsigned flags);
+
+/* Rows of logits [rows][vocab] (bf16, f16 or f32, row stride ldl >= vocab, any alignment of the type).  With
+ * z = logits / temperature and lse = log sum exp z:
+ *   logprob[row] = z[tokens[row]] - lse      (tokens int64 [rows]; both NULL: not wanted)
+ *   entropy[row] = lse - sum_i exp(z_i - lse) z_i   (NULL: not wanted)
+ *   top_tokens[row][0..top-1], top_logprobs: the top (0 to 32) largest logits in falling order, equal ones by
+ *   their index (of a row with a NaN: some of its tokens).
+ * -infinity closes a token; a row of nothing else has logprob and top_logprobs -infinity and entropy 0.  A
+ * token outside 0..vocab-1 has -infinity.  A row with a NaN or +infinity gives NaN; other rows are not
+ * touched by it. */
+voc_status vocoder_lm_logprobs(const void *logits, long long ldl, int dtype, long long rows, int vocab,
+                               float temperature, const long long *tokens, float *logprob,
+                               float *entropy, int top, float *top_logprobs, long long *top_tokens,
+                               voc_stream_t stream, unsigned flags);
+
 #ifdef __cplusplus
 }
 #endif
