@@ -7,6 +7,7 @@
 // 22 (f16) bits together, so that only the output is rounded.
 #pragma once
 #include "lm_common.cuh"
+#include "lm_rows.cuh"
 
 namespace voc {
 
@@ -90,36 +91,87 @@ __device__ __forceinline__ void cut_words(uint32_t (&w)[WORDS], int left) {
     w[i] = left >= 2 * i + 2 ? w[i] : left == 2 * i + 1 ? w[i] & 0xffffu : 0u;
 }
 
-// Eight values of a row of y or out, at `p`, of which `left` lie in the row.
+// Eight values of a row of y or out, at `p`, of which `left` lie in the row, in the widest accesses that
+// `start` (what all rows of both start on, in bytes) allows.
 template <typename Y>
-__device__ __forceinline__ void load8(const Y *p, int left, bool vec, float (&f)[8]) {
-  if (vec && left >= 8) {
-    if constexpr (sizeof(Y) == 4) {
-      const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-      f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-    } else {
-      Vec16<Y>::unpack(*reinterpret_cast<const uint4 *>(p), f);
-    }
-  } else {
+struct Eight {
+  static constexpr int kWords = 2 * static_cast<int>(sizeof(Y));
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const Y *p, int left, int start) {
+    if (left < 8) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = i < left ? to_f32(p[i]) : 0.f;
-  }
-}
-template <typename Y>
-__device__ __forceinline__ void store8(Y *p, int left, bool vec, const float (&f)[8]) {
-  if (vec && left >= 8) {
-    if constexpr (sizeof(Y) == 4) {
-      reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-      reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-    } else {
-      *reinterpret_cast<uint4 *>(p) = Vec16<Y>::pack(f);
-    }
-  } else {
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (sizeof(Y) == 4) {
+          w[i] = i < left ? reinterpret_cast<const uint32_t *>(p)[i] : 0u;
+        } else {
+          const uint32_t h = i < left ? reinterpret_cast<const uint16_t *>(p)[i] : 0u;
+          w[i / 2] = i % 2 ? w[i / 2] | h << 16 : h;
+        }
+      }
+    } else if (start % 16 == 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < left) p[i] = from_f32<Y>(f[i]);
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint32_t *>(p) + i);
+        w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+      }
+    } else if (start % 8 == 0) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 2) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint32_t *>(p) + i);
+        w[i] = v.x, w[i + 1] = v.y;
+      }
+    } else if (sizeof(Y) == 4 || start % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const uint32_t *>(p)[i];
+    } else if constexpr (sizeof(Y) == 2) {
+      RowVec<Y, 16>::load_any(p, w);
+    }
   }
-}
+  __device__ __forceinline__ void store(Y *p, int left, int start) const {
+    if (left < 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < left) {
+          if constexpr (sizeof(Y) == 4)
+            reinterpret_cast<uint32_t *>(p)[i] = w[i];
+          else
+            reinterpret_cast<uint16_t *>(p)[i] = static_cast<uint16_t>(w[i / 2] >> 16 * (i % 2));
+        }
+    } else if (start % 16 == 0) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4)
+        *reinterpret_cast<uint4 *>(reinterpret_cast<uint32_t *>(p) + i) =
+            make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    } else if (start % 8 == 0) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 2)
+        *reinterpret_cast<uint2 *>(reinterpret_cast<uint32_t *>(p) + i) = make_uint2(w[i], w[i + 1]);
+    } else if (sizeof(Y) == 4 || start % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) reinterpret_cast<uint32_t *>(p)[i] = w[i];
+    } else if constexpr (sizeof(Y) == 2) {
+      RowVec<Y, 16>::store_any(p, w);
+    }
+  }
+  __device__ __forceinline__ void unpack(float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(Y) == 4)
+        f[i] = __uint_as_float(w[i]);
+      else
+        unpack2<Y>(w[i], f[2 * i], f[2 * i + 1]);
+    }
+  }
+  __device__ __forceinline__ void pack(const float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(Y) == 4)
+        w[i] = __float_as_uint(f[i]);
+      else
+        w[i] = pack2<Y>(f[2 * i], f[2 * i + 1]);
+    }
+  }
+};
 
 // A cluster of CTAs (along z) takes those of the adapters that the 64 tokens of tile blockIdx.x use whose
 // turn it is (every gridDim.y-th, in the order in which they first occur), one after the other, with all
@@ -187,21 +239,26 @@ __global__ void __launch_bounds__(kAdThreads) adapters_kernel(const LmAdaptersAr
     const int g1 = static_cast<int>(static_cast<long long>(groups) * (part + 1) / split);
     const Y *y = static_cast<const Y *>(p.y);
     Y *out = static_cast<Y *>(p.out);
-    const bool vec = ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(out) |
-                       (p.ldy * sizeof(Y)) | (p.ldo * sizeof(Y))) % 16) == 0;
+    const int start = static_cast<int>((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(out) |
+                                        (p.ldy * sizeof(Y)) | (p.ldo * sizeof(Y))) & 15);
     if (rank == 0) {  // uniform in the cluster
       if (p.out != p.y)
         for (int i = tid; i < count * (g1 - g0) * 4; i += kAdThreads) {
           const int r = i / ((g1 - g0) * 4), n = 32 * g0 + i % ((g1 - g0) * 4) * 8;
           const long long m = m0 + rows[r];
-          float f[8];
-          load8(y + m * p.ldy + n, p.N - n, vec, f);
-          store8(out + m * p.ldo + n, p.N - n, vec, f);
+          Eight<Y> v;
+          v.load(y + m * p.ldy + n, p.N - n, start);
+          v.store(out + m * p.ldo + n, p.N - n, start);
         }
       __syncthreads();  // rows are read
       continue;
     }
 
+    const W *b = static_cast<const W *>(p.b) + which * p.sb;
+    if (count <= 16 && tid == 0 && g0 < g1 && p.ldb <= 2 * p.rank) {  // the second product's rows meanwhile to L2
+      const int n0 = 32 * g0, n1 = min(p.N, 32 * g1);
+      bulk_prefetch_l2(b + n0 * p.ldb, static_cast<uint32_t>(((n1 - 1 - n0) * p.ldb + p.rank) * 2));
+    }
     // ---------------------------------------------------------------- A x, this CTA's part of K
     const W *a = static_cast<const W *>(p.a) + which * p.sa;
     const int segs = (p.K + kAdSeg - 1) / kAdSeg;
@@ -337,7 +394,6 @@ __global__ void __launch_bounds__(kAdThreads) adapters_kernel(const LmAdaptersAr
       __syncthreads();
 
     // ---------------------------------------------------------------- B v, this CTA's channels
-    const W *b = static_cast<const W *>(p.b) + which * p.sb;
     constexpr int kWords = R >= 32 ? 4 : 2;  // a lane's words of a row of B: 8 (4) ranks in a row
     constexpr int kBlocks = R >= 32 ? R / 32 : 1;
     for (int gr = g0 + warp; gr < g1; gr += 8) {
@@ -364,50 +420,65 @@ __global__ void __launch_bounds__(kAdThreads) adapters_kernel(const LmAdaptersAr
         }
       }
       const int n = 32 * gr + 8 * t, left = p.N - n;
-      for (int m = 0; m < (count + 15) / 16; ++m) {
-        float o[4][4];
+      constexpr int kTogether = sizeof(Y) == 4 ? 2 : 4;  // sixteens of tokens whose y is under way together
+      const int sixteens = (count + 15) / 16;
+      for (int first16 = 0; first16 < sixteens; first16 += kTogether) {
+        Eight<Y> yw[kTogether][2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int m = 0; m < kTogether; ++m)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
+          for (int h = 0; h < 2; ++h) {
+            const int r = (first16 + m) * 16 + g + 8 * h;
+            if (r < count && left > 0) yw[m][h].load(y + (m0 + rows[r]) * p.ldy + n, left, start);
+          }
 #pragma unroll
-        for (int part_of = 0; part_of < 2; ++part_of) {
-          const uint8_t *from = half + part_of * Smem::kHalf + (m * 16 + g) * Smem::kRow + 4 * kWords * t;
+        for (int m = 0; m < kTogether; ++m) {
+          if (first16 + m >= sixteens) break;
+          float o[4][4];
 #pragma unroll
-          for (int i = 0; i < kBlocks; ++i) {
-            uint32_t va[kWords / 2][4];
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint8_t *at = from + h * 8 * Smem::kRow + 64 * i;
-              if constexpr (kWords == 4) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(at);
-                va[0][h] = v.x, va[0][2 + h] = v.y, va[1][h] = v.z, va[1][2 + h] = v.w;
-              } else {
-                const uint2 v = *reinterpret_cast<const uint2 *>(at);
-                va[0][h] = v.x, va[0][2 + h] = v.y;
+            for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
+#pragma unroll
+          for (int part_of = 0; part_of < 2; ++part_of) {
+            const uint8_t *from = half + part_of * Smem::kHalf + ((first16 + m) * 16 + g) * Smem::kRow +
+                                  4 * kWords * t;
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) {
+              uint32_t va[kWords / 2][4];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint8_t *at = from + h * 8 * Smem::kRow + 64 * i;
+                if constexpr (kWords == 4) {
+                  const uint4 v = *reinterpret_cast<const uint4 *>(at);
+                  va[0][h] = v.x, va[0][2 + h] = v.y, va[1][h] = v.z, va[1][2 + h] = v.w;
+                } else {
+                  const uint2 v = *reinterpret_cast<const uint2 *>(at);
+                  va[0][h] = v.x, va[0][2 + h] = v.y;
+                }
               }
+#pragma unroll
+              for (int s = 0; s < kWords / 2; ++s)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  mma16(o[j], va[s], bw[j][i][2 * s], bw[j][i][2 * s + 1], W());
             }
-#pragma unroll
-            for (int s = 0; s < kWords / 2; ++s)
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                mma16(o[j], va[s], bw[j][i][2 * s], bw[j][i][2 * s + 1], W());
           }
-        }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = m * 16 + g + 8 * h;
-          if (r >= count || left <= 0) continue;
-          const long long token = m0 + rows[r];
-          const float by = factor[r];
-          float f[8];
-          load8(y + token * p.ldy + n, left, vec, f);
+          for (int h = 0; h < 2; ++h) {
+            const int r = (first16 + m) * 16 + g + 8 * h;
+            if (r >= count || left <= 0) continue;
+            const float by = factor[r];
+            float f[8];
+            yw[m][h].unpack(f);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            f[2 * j] = fmaf(o[j][2 * h], by, f[2 * j]);
-            f[2 * j + 1] = fmaf(o[j][2 * h + 1], by, f[2 * j + 1]);
+            for (int j = 0; j < 4; ++j) {
+              f[2 * j] = fmaf(o[j][2 * h], by, f[2 * j]);
+              f[2 * j + 1] = fmaf(o[j][2 * h + 1], by, f[2 * j + 1]);
+            }
+            yw[m][h].pack(f);
+            yw[m][h].store(out + (m0 + rows[r]) * p.ldo + n, left, start);
           }
-          store8(out + token * p.ldo + n, left, vec, f);
         }
       }
     }

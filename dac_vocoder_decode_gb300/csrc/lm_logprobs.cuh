@@ -59,6 +59,23 @@ __device__ __forceinline__ LpPart lp_join(const LpPart &a, const LpPart &b, floa
   return r;
 }
 
+// The parts of a warp's lanes, in a fixed order, to all of them.
+__device__ __forceinline__ LpPart lp_join_warp(const LpPart &a, float c) {
+  LpPart r;
+  r.m = a.m;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) r.m = fmaxf(r.m, __shfl_xor_sync(0xffffffffu, r.m, o));
+  const float d = a.m == -INFINITY ? 0.f : (a.m - r.m) * c, f = ex2(d);
+  r.s = a.s * f;
+  r.t = f > 0.f ? f * fmaf(a.s, d, a.t) : a.s * 0.f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    r.s += __shfl_xor_sync(0xffffffffu, r.s, o);
+    r.t += __shfl_xor_sync(0xffffffffu, r.t, o);
+  }
+  return r;
+}
+
 // The larger ones of two pairs of 16-bit values (a number before NaN).
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, __half) {
   __half2 x, y;
@@ -77,6 +94,11 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, __nv_bfloat16) 
 
 // A row in 16-byte vectors that lie on the 16-byte grid, whatever the row starts on: those at its ends
 // that it covers only in part are read value by value, with -infinity in the places outside of it.
+template <int N>
+struct LpCount {
+  static constexpr int value = N;
+};
+
 template <typename T>
 struct LpRow {
   static constexpr int N = 16 / static_cast<int>(sizeof(T));
@@ -115,6 +137,12 @@ struct LpRow {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
+  // Vectors v, v + step, ..., all of them whole.
+  __device__ __forceinline__ void load_batch(int v, int step, uint4 (&u)[kBatch]) const {
+    const uint4 *at = reinterpret_cast<const uint4 *>(row + index(v, 0));
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) u[b] = at[b * step];
+  }
   // Values 2i and 2i + 1 of a vector.
   static __device__ __forceinline__ float2 pair(const uint4 &u, int i) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -129,23 +157,22 @@ struct LpRow {
     const float2 f = pair(u, j / 2);
     return j % 2 ? f.y : f.x;
   }
-  // Largest of a batch (of NaN only: NaN or -infinity).
-  static __device__ __forceinline__ float largest(const uint4 (&u)[kBatch]) {
+  // Largest of V vectors (of NaN only: NaN or -infinity).
+  template <int V>
+  static __device__ __forceinline__ float largest(const uint4 *u) {
     if constexpr (sizeof(T) == 4) {
       float m[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b)
+      for (int b = 0; b < V; ++b)
 #pragma unroll
         for (int i = 0; i < 4; ++i) m[i % 2] = fmaxf(m[i % 2], value(u[b], i));
       return fmaxf(m[0], m[1]);
     } else {
-      uint32_t m[2] = {u[0].x, u[0].y};
+      uint32_t m[2] = {max2(u[0].x, u[0].z, T()), max2(u[0].y, u[0].w, T())};
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        m[0] = max2(m[0], u[b].x, T());
-        m[1] = max2(m[1], u[b].y, T());
-        m[0] = max2(m[0], u[b].z, T());
-        m[1] = max2(m[1], u[b].w, T());
+      for (int b = 1; b < V; ++b) {
+        m[0] = max2(max2(m[0], u[b].x, T()), u[b].z, T());
+        m[1] = max2(max2(m[1], u[b].y, T()), u[b].w, T());
       }
       float a, b;
       unpack2<T>(max2(m[0], m[1], T()), a, b);
@@ -236,11 +263,10 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kLpWarps : kLpWide)
   int best = v0 + tid;  // first vector of the batch that holds this thread's maximum first
   {
     float2 s = {0.f, 0.f}, t = {0.f, 0.f};
-    for (int v = v0 + tid; v < v1; v += B * TPR) {
-      uint4 u[B];
-#pragma unroll
-      for (int b = 0; b < B; ++b) u[b] = v + b * TPR < v1 ? row.load(v + b * TPR) : Row::nothing();
-      const float m = Row::largest(u);
+    // Adds V vectors, the first of them number v.
+    auto add = [&](const uint4 *u, auto count, int v) {
+      constexpr int kVectors = decltype(count)::value;
+      const float m = Row::template largest<kVectors>(u);
       if (m > mine.m) {
         const float d = (mine.m - m) * c, f = mine.m == -INFINITY ? 0.f : ex2(d);
         if (f > 0.f)
@@ -252,29 +278,44 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kLpWarps : kLpWide)
         best = v;
       }
       const float neg = mine.m == -INFINITY ? 0.f : -mine.m;
-      const float2 from = {neg, neg}, by = {c, c}, zero = {0.f, 0.f};
+      const float2 from = {neg, neg}, by = {c, c};
 #pragma unroll
-      for (int b = 0; b < B; ++b)
+      for (int b = 0; b < kVectors; ++b)
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
-          float2 d = fma2(add2(Row::pair(u[b], i), from), by, zero);
+          float2 d = mul2(add2(Row::pair(u[b], i), from), by);
           d.x = max_nan(d.x, -200.f), d.y = max_nan(d.y, -200.f);  // -infinity weighs 0, and 0 times it is 0
           const float2 e = {ex2(d.x), ex2(d.y)};
           s = add2(s, e);
           t = fma2(e, d, t);
         }
+    };
+    int v = v0 + tid;
+    const int whole = min(v1, row.hi) - (B - 1) * TPR;  // batches that start below it are whole
+    if (v < row.lo) {  // the row's first vector, covered in part
+      const uint4 u = row.load(v);
+      add(&u, LpCount<1>(), v);
+      v += TPR;
+    }
+    if (v < whole) {
+      uint4 u[B];
+      row.load_batch(v, TPR, u);
+      for (; v < whole; v += B * TPR) {
+        uint4 now[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) now[b] = u[b];
+        if (v + B * TPR < whole) row.load_batch(v + B * TPR, TPR, u);
+        add(now, LpCount<B>(), v);
+      }
+    }
+    for (; v < v1; v += TPR) {
+      const uint4 u = row.load(v);
+      add(&u, LpCount<1>(), v);
     }
     mine.s = s.x + s.y, mine.t = t.x + t.y;
   }
   const float top_value = mine.m;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    LpPart other;
-    other.m = __shfl_xor_sync(0xffffffffu, mine.m, o);
-    other.s = __shfl_xor_sync(0xffffffffu, mine.s, o);
-    other.t = __shfl_xor_sync(0xffffffffu, mine.t, o);
-    mine = lane & o ? lp_join(other, mine, c) : lp_join(mine, other, c);
-  }
+  mine = lp_join_warp(mine, c);
   if (TPR > 32 && lane == 0) parts[warp] = mine;
 
   if constexpr (TOP) {

@@ -56,12 +56,20 @@ __global__ void __launch_bounds__(kRotThreads) rotate_kernel(const LmRotateArgs 
   const int first = static_cast<int>(task % p.parts) * p.per;
   const int last = min(first + p.per, p.groups[0] + p.groups[1]);
   const int blocks = p.pairs / 8;  // lanes that turn pairs
+  auto unpack8 = [](const uint4 &u, float2 *f) {
+    unpack2<T>(u.x, f[0].x, f[0].y), unpack2<T>(u.y, f[1].x, f[1].y);
+    unpack2<T>(u.z, f[2].x, f[2].y), unpack2<T>(u.w, f[3].x, f[3].y);
+  };
+  auto pack8 = [](const float2 *f) {
+    return make_uint4(pack2<T>(f[0].x, f[0].y), pack2<T>(f[1].x, f[1].y), pack2<T>(f[2].x, f[2].y),
+                      pack2<T>(f[3].x, f[3].y));
+  };
   const bool turns = unit < blocks, channels = unit < p.d / 16;
   const int c0 = 8 * (turns && !NEAR ? unit : 2 * unit);
   const int c1 = turns && !NEAR ? c0 + p.pairs : c0 + 8;
-  float co[8], si[8];
+  float2 co[4], si[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) co[i] = 1.f, si[i] = 0.f;
+  for (int i = 0; i < 4; ++i) co[i] = {1.f, 1.f}, si[i] = {0.f, 0.f};
   if (turns) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -69,15 +77,33 @@ __global__ void __launch_bounds__(kRotThreads) rotate_kernel(const LmRotateArgs 
       const int axis = p.axis ? p.axis[pair] : 0;
       if (axis >= 0 && axis < p.axes) {
         const float2 cs = turn_cos_sin(p.pos[axis * p.ldp + token], p.turns[pair]);
-        co[i] = cs.x, si[i] = cs.y;
+        if (i % 2)
+          co[i / 2].y = cs.x, si[i / 2].y = cs.y;
+        else
+          co[i / 2].x = cs.x, si[i / 2].x = cs.y;
       }
     }
   }
+  const float inv_d = 1.f / static_cast<float>(p.d);
+  // A turn of the warp: its head, whether this lane has channels of it, and where they are.
+  auto head_of = [&](int g, int which) {
+    return (g - (which ? p.groups[0] : 0)) * kAtOnce + lane / L;
+  };
+  auto load = [&](int g, uint4 &a, uint4 &b) {
+    const int which = g >= p.groups[0], head = head_of(g, which);
+    a = b = make_uint4(0, 0, 0, 0);
+    if (channels && g < last && head < p.heads[which]) {
+      const T *x = static_cast<const T *>(p.x[which]) + token * p.ldx[which] + head * p.hsx[which];
+      a = *reinterpret_cast<const uint4 *>(x + c0);
+      b = *reinterpret_cast<const uint4 *>(x + c1);
+    }
+  };
   int of = -1;  // whose weights are at hand
-  uint4 w0 = {}, w1 = {};
+  uint4 w0 = {}, w1 = {}, a, b;
+  load(first, a, b);
   for (int g = first; g < last; ++g) {
     const int which = g >= p.groups[0];
-    const int head = (g - (which ? p.groups[0] : 0)) * kAtOnce + lane / L;
+    const int head = head_of(g, which);
     const bool live = channels && head < p.heads[which];
     const T *w = static_cast<const T *>(p.w[which]);
     if (which != of && w && channels) {
@@ -85,75 +111,59 @@ __global__ void __launch_bounds__(kRotThreads) rotate_kernel(const LmRotateArgs 
       w1 = *reinterpret_cast<const uint4 *>(w + c1);
     }
     of = which;
-    uint4 a = {}, b = {};
-    if (live) {
-      const T *x = static_cast<const T *>(p.x[which]) + token * p.ldx[which] + head * p.hsx[which];
-      a = *reinterpret_cast<const uint4 *>(x + c0);
-      b = *reinterpret_cast<const uint4 *>(x + c1);
-    }
-    float h[16];
-    {
-      float f[8];
-      Vec16<T>::unpack(a, f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] = f[i];
-      Vec16<T>::unpack(b, f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[8 + i] = f[i];
-    }
+    float2 h[8];
+    unpack8(a, h), unpack8(b, h + 4);
+    load(g + 1, a, b);  // in flight meanwhile; an output in the input's place is another head's
     if (w) {
-      float ss = 0.f;
+      float2 sq = {0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 16; ++i) ss = fmaf(h[i], h[i], ss);
+      for (int i = 0; i < 8; ++i) sq = fma2(h[i], h[i], sq);
+      float ss = sq.x + sq.y;
 #pragma unroll
       for (int o = 1; o < L; o *= 2) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      float pre = 1.f;
       const bool holds = rms_sum_holds(ss) || head >= p.heads[which];
+      float rs = rsqrtf(fmaf(ss, inv_d, p.eps));
       if (__any_sync(0xffffffffu, !holds)) {  // rare: squares that overflowed or vanished
         float m = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) m = max_abs(m, h[i]);
+        for (int i = 0; i < 8; ++i) m = max_abs(max_abs(m, h[i].x), h[i].y);
         uint32_t top = abs_bits(m);
 #pragma unroll
         for (int o = 1; o < L; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (!holds && rms_needs_scaling(top)) pre = rms_prescale(top);
+        const float pre = !holds && rms_needs_scaling(top) ? rms_prescale(top) : 1.f;
         float again = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          h[i] *= pre;
-          again = fmaf(h[i], h[i], again);
+        for (int i = 0; i < 8; ++i) {
+          h[i].x *= pre, h[i].y *= pre;
+          again = fmaf(h[i].x, h[i].x, fmaf(h[i].y, h[i].y, again));
         }
 #pragma unroll
         for (int o = 1; o < L; o *= 2) again += __shfl_xor_sync(0xffffffffu, again, o);
-        ss = again;
+        if (!holds) rs = rms_factor(again, p.d, p.eps, pre);
       }
-      const float rs = rms_factor(ss, p.d, p.eps, pre);
-      float f[8];
-      Vec16<T>::unpack(w0, f);
+      float2 f[8];
+      unpack8(w0, f), unpack8(w1, f + 4);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] = h[i] * rs * f[i];
-      Vec16<T>::unpack(w1, f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[8 + i] = h[8 + i] * rs * f[i];
+      for (int i = 0; i < 8; ++i) h[i] = mul2(mul2(h[i], {rs, rs}), f[i]);
     }
     if (turns) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int ia = NEAR ? 2 * i : i, ib = NEAR ? 2 * i + 1 : 8 + i;
-        const float u = h[ia], v = h[ib];
-        h[ia] = u * co[i] - v * si[i];
-        h[ib] = u * si[i] + v * co[i];
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (NEAR) {
+          const float2 u = h[2 * i], v = h[2 * i + 1];
+          h[2 * i] = {u.x * co[i].x - u.y * si[i].x, u.x * si[i].x + u.y * co[i].x};
+          h[2 * i + 1] = {v.x * co[i].y - v.y * si[i].y, v.x * si[i].y + v.y * co[i].y};
+        } else {
+          const float2 u = h[i], v = h[4 + i], less = {-v.x, -v.y};
+          h[i] = fma2(less, si[i], mul2(u, co[i]));
+          h[4 + i] = fma2(u, si[i], mul2(v, co[i]));
+        }
       }
     }
     if (live) {
-      float f[8];
       T *o = static_cast<T *>(p.out[which]) + token * p.ldo[which] + head * p.hso[which];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = h[i];
-      *reinterpret_cast<uint4 *>(o + c0) = Vec16<T>::pack(f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = h[8 + i];
-      *reinterpret_cast<uint4 *>(o + c1) = Vec16<T>::pack(f);
+      *reinterpret_cast<uint4 *>(o + c0) = pack8(h);
+      *reinterpret_cast<uint4 *>(o + c1) = pack8(h + 4);
     }
   }
 }
