@@ -45,21 +45,9 @@ __device__ __forceinline__ int key_index(unsigned long long key) {
 struct LpPart {
   float m, s, t;
 };
-__device__ __forceinline__ LpPart lp_join(const LpPart &a, const LpPart &b, float c) {
-  LpPart r;
-  r.m = fmaxf(a.m, b.m);
-  // a part without weight (nothing but -infinity) stays out: its maximum has no difference to another
-  const float da = a.m == -INFINITY ? 0.f : (a.m - r.m) * c, db = b.m == -INFINITY ? 0.f : (b.m - r.m) * c;
-  const float fa = ex2(da), fb = ex2(db);
-  // parts too far below for their weight to count: 0, and not 0 times a difference that left 32 bits
-  const float ta = fa > 0.f ? fa * fmaf(a.s, da, a.t) : a.s * 0.f;
-  const float tb = fb > 0.f ? fb * fmaf(b.s, db, b.t) : b.s * 0.f;
-  r.s = fmaf(a.s, fa, b.s * fb);
-  r.t = ta + tb;
-  return r;
-}
-
-// The parts of a warp's lanes, in a fixed order, to all of them.
+// The parts of a warp's lanes, in a fixed order, to all of them.  A part without weight (nothing but
+// -infinity) stays out, and one too far below for its weight to count adds 0, not 0 times a difference that
+// left 32 bits; NaN stays.
 __device__ __forceinline__ LpPart lp_join_warp(const LpPart &a, float c) {
   LpPart r;
   r.m = a.m;
@@ -205,9 +193,9 @@ template <int TPR>
 struct LpShared {
   static constexpr int kSubs = TPR == 32 ? 32 : 128;  // parts of a row, for its alternatives
   static constexpr int kRoom = TPR == 32 ? 256 : 1024;
-  unsigned long long sub[kSubs], cand[kRoom], top[kLpMaxTop];
-  int winner[kLpMaxTop];
-  int count;
+  unsigned long long sub[kSubs], cand[kRoom], top[kLpMaxTop], bound;
+  int reach[kSubs];  // subsets that reach the bound
+  int reached, count;
 };
 
 // The n numbers of `cand` (n <= room; all different but for zeros, which do not count): the k largest, in
@@ -223,13 +211,61 @@ __device__ __forceinline__ void lp_rank(const unsigned long long *cand, int n, i
   }
 }
 
+// One warp: a lower bound of the k-th largest number of a row from the largest of each subset (0: nothing in
+// it), and the subsets that reach it.  The lanes' heads are compared k times, by their 32 - log2(kSubs) first
+// bits; the smallest of the k winners' whole numbers is the bound.  (What those bits do not tell apart may
+// pass a larger one over; that makes the bound lower, and the subsets that reach it are looked up anew.)
+template <int TPR>
+__device__ __forceinline__ void lp_bound(LpShared<TPR> &sh, int k, int lane) {
+  constexpr int kSubs = LpShared<TPR>::kSubs, kOwn = kSubs / 32;
+  uint32_t own[kOwn];
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const uint32_t v = static_cast<uint32_t>(sh.sub[lane + 32 * i] >> 32);
+    own[i] = v ? (v & ~(kSubs - 1u)) | (lane + 32 * i) : 0;
+  }
+  auto order = [&](int i, int j) {
+    const uint32_t hi = max(own[i], own[j]), lo = min(own[i], own[j]);
+    own[i] = hi, own[j] = lo;
+  };
+  if constexpr (kOwn == 4) {
+    order(0, 1), order(2, 3), order(0, 2), order(1, 3), order(1, 2);
+  }
+  uint32_t mine = 0;  // the k-th turn's winner in lane k
+  for (int i = 0; i < k; ++i) {
+    const uint32_t top = __reduce_max_sync(0xffffffffu, own[0]);
+    if (lane == i) mine = top;
+    if (own[0] == top) {
+#pragma unroll
+      for (int n = 0; n + 1 < kOwn; ++n) own[n] = own[n + 1];
+      own[kOwn - 1] = 0;
+    }
+  }
+  unsigned long long key = ~0ull;
+  if (lane < k) key = mine ? sh.sub[mine & (kSubs - 1)] : 0;  // fewer subsets than k hold anything: all of them
+  const uint32_t hi = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(key >> 32));
+  const uint32_t lo = __reduce_min_sync(
+      0xffffffffu, static_cast<uint32_t>(key >> 32) == hi ? static_cast<uint32_t>(key) : 0xffffffffu);
+  const unsigned long long bound = static_cast<unsigned long long>(hi) << 32 | lo;
+  int reached = 0;
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const unsigned long long s = sh.sub[lane + 32 * i];
+    const bool in = s && s >= bound;
+    const uint32_t all = __ballot_sync(0xffffffffu, in);
+    if (in) sh.reach[reached + __popc(all & ((1u << lane) - 1u))] = lane + 32 * i;
+    reached += __popc(all);
+  }
+  if (lane == 0) sh.bound = bound, sh.reached = reached, sh.count = 0;
+}
+
 // TPR threads take a row, or with a cluster of several CTAs (along z) a part of it each.
 //
-// Top: the row falls into subsets (kSubs lanes or pairs of lanes).  The k-th largest of their maxima is a
-// lower bound of the k-th largest value, which only the k subsets with the largest maxima can reach: these
-// are read again (from cache), what reaches the bound is gathered, some k to 2k numbers for logits in no
-// order, and ranked by counting.  Where more of them come together than there is room for, the k-th
-// largest of those at hand is a higher bound, and they are gathered again.
+// Top: the row falls into subsets (of a lane or a pair of lanes).  The k-th largest of their maxima is a
+// lower bound of the k-th largest value, and few subsets reach it: these are read again (from cache), what
+// reaches the bound is gathered, some k to 2k numbers for logits in no order, and ranked by counting.  Where
+// more of them come together than there is room for, the k-th largest of those at hand is a higher bound,
+// and they are gathered again.
 template <typename T, int TPR, bool TOP>
 __global__ void __launch_bounds__(TPR == 32 ? 32 * kLpWarps : kLpWide)
     logprobs_kernel(const LmLogprobsArgs p) {
@@ -322,63 +358,51 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kLpWarps : kLpWide)
     constexpr int kEach = TPR / Shared::kSubs;  // lanes of a subset
     unsigned long long key = 0;
     if (v0 + tid < v1) {
-      int index = -1, any = -1;
-      for (int b = 0; b < B; ++b) {
-        const int v = best + b * TPR;
-        if (v >= v1) break;
-        const uint4 u = row.load(v);
+      // the vector that holds the maximum first; its last index stands for the value's, which is no larger
+      int at_vector = best;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const int i = row.index(v, j);
-          if (i < 0 || i >= p.vocab) continue;
-          if (any < 0) any = i;
-          if (index < 0 && Row::value(u, j) == top_value) index = i;
+      for (int b = B - 1; b >= 0; --b) {
+        const int v = best + b * TPR;
+        if (v < v1) {
+          const uint4 u = row.load(v);
+          if (Row::template largest<1>(&u) == top_value) at_vector = v;
         }
       }
-      key = order_key(top_value, index >= 0 ? index : any);  // without a number in it: any of them
+      key = order_key(top_value, row.index(at_vector, N - 1));
     }
     if (kEach == 2) {
       const unsigned long long other = __shfl_xor_sync(0xffffffffu, key, 1);
       key = other > key ? other : key;
     }
     if (tid % kEach == 0) sh.sub[tid / kEach] = key;
-    if (tid < kLpMaxTop) sh.top[tid] = 0, sh.winner[tid] = -1;
-    if (tid == 0) sh.count = 0;
+    if (tid < kLpMaxTop) sh.top[tid] = 0;
     sync();
-    if (tid < Shared::kSubs) {
-      const unsigned long long own = sh.sub[tid];
-      int above = 0;
-#pragma unroll 8
-      for (int j = 0; j < Shared::kSubs; ++j) above += sh.sub[j] > own;
-      if (own && above < p.k) {
-        sh.winner[above] = tid;
-        sh.top[above] = own;
-      }
-    }
+    if (tid < 32) lp_bound<TPR>(sh, p.k, lane);
     sync();
-    unsigned long long bound = sh.top[p.k - 1];  // 0: fewer subsets than k hold anything
-    int n;
+    unsigned long long bound = sh.bound;
+    const int each = (v1 - v0 + TPR - 1) / TPR * kEach;  // vectors of a subset, at most
+    const int items = sh.reached * each;
     while (true) {
       const float least = bound ? key_value(bound) : -INFINITY;
-      for (int w = TPR == 32 ? 0 : warp; w < p.k; w += kWarps) {
-        const int g = sh.winner[w];
-        if (g < 0) break;
-        for (int v = v0 + g * kEach + lane % kEach + lane / kEach * TPR; v < v1; v += 32 / kEach * TPR) {
-          const uint4 u = row.load(v);
+      for (int i = tid; i < items; i += TPR) {
+        const int w = i / each, r = i % each;
+        const int v = v0 + sh.reach[w] * kEach + r % kEach + r / kEach * TPR;
+        if (v >= v1) continue;
+        const uint4 u = row.load(v);
+        if (Row::template largest<1>(&u) < least) continue;
 #pragma unroll
-          for (int j = 0; j < N; ++j) {
-            const float x = Row::value(u, j);
-            const int i = row.index(v, j);
-            if (x < least || i < 0 || i >= p.vocab) continue;
-            const unsigned long long k = order_key(x, i);
-            if (k < bound) continue;
-            const int to = atomicAdd(&sh.count, 1);  // in any order: they are ranked
-            if (to < Shared::kRoom) sh.cand[to] = k;
-          }
+        for (int j = 0; j < N; ++j) {
+          const float x = Row::value(u, j);
+          const int at_index = row.index(v, j);
+          if (x < least || at_index < 0 || at_index >= p.vocab) continue;
+          const unsigned long long one = order_key(x, at_index);
+          if (one < bound) continue;
+          const int to = atomicAdd(&sh.count, 1);  // in any order: they are ranked
+          if (to < Shared::kRoom) sh.cand[to] = one;
         }
       }
       sync();
-      n = sh.count;
+      const int n = sh.count;
       lp_rank<TPR>(sh.cand, min(n, Shared::kRoom), p.k, sh.top, tid);
       sync();
       if (n <= Shared::kRoom) break;
@@ -389,25 +413,22 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kLpWarps : kLpWide)
   } else if (TPR > 32) {
     __syncthreads();
   }
-
-  if (TPR > 32) {
-    mine = parts[0];
-    for (int w = 1; w < kWarps; ++w) mine = lp_join(mine, parts[w], c);
-  }
+  if (TPR > 32 && warp == 0)  // the first warp's from here on
+    mine = lp_join_warp(lane < kWarps ? parts[lane] : LpPart{-INFINITY, 0.f, 0.f}, c);
   if (TPR > 32 && split > 1) {
     if (tid == 0) parts[kWarps] = mine;
     cluster_sync();
     if (rank == 0) {
-      for (int q = 1; q < split; ++q) {
-        const uint32_t from = mapa_shared(smem_u32(&parts[kWarps]), q);
-        LpPart other;
-        other.m = ld_cluster_f32(from);
-        other.s = ld_cluster_f32(from + 4);
-        other.t = ld_cluster_f32(from + 8);
-        mine = lp_join(mine, other, c);
+      if (warp == 0) {
+        LpPart other{-INFINITY, 0.f, 0.f};
+        if (lane < split) {
+          const uint32_t from = mapa_shared(smem_u32(&parts[kWarps]), lane);
+          other = {ld_cluster_f32(from), ld_cluster_f32(from + 4), ld_cluster_f32(from + 8)};
+        }
+        mine = lp_join_warp(other, c);
       }
       if constexpr (TOP) {
-        const int n = split * p.k;  // at most 256
+        const int n = split * p.k;  // no more than there is room for
         for (int i = tid; i < n; i += TPR)
           sh.cand[i] = ld_cluster_u64(mapa_shared(smem_u32(&sh.top[i % p.k]), i / p.k));
         __syncthreads();
@@ -416,7 +437,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kLpWarps : kLpWide)
       }
     }
   }
-  if (rank == 0) {
+  if (rank == 0 && (TPR == 32 || warp == 0)) {
     constexpr float kLn2 = 0.693147181f;
     const float log2s = log2f(mine.s);
     const bool none = mine.s == 0.f;  // nothing but -infinity: no token has any weight
@@ -429,10 +450,10 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kLpWarps : kLpWide)
       }
     }
     if constexpr (TOP) {
-      for (int i = tid; i < p.k; i += TPR) {
-        const unsigned long long key = sh.top[i];
-        p.top[at * p.k + i] = none ? -INFINITY : ((key_value(key) - mine.m) * c - log2s) * kLn2;
-        p.top_tokens[at * p.k + i] = key_index(key);
+      if (lane < p.k) {
+        const unsigned long long key = sh.top[lane];
+        p.top[at * p.k + lane] = none ? -INFINITY : ((key_value(key) - mine.m) * c - log2s) * kLn2;
+        p.top_tokens[at * p.k + lane] = key_index(key);
       }
     }
   }

@@ -23,11 +23,11 @@ cudaError_t launch_rotate(int sms, voc::LmRotateArgs &a, voc_stream_t stream) {
   for (int i = 0; i < 2; ++i) turns += a.groups[i] = (a.heads[i] + at_once - 1) / at_once;
   // A warp takes all heads of a token, whose angles it then computes once, or as few as fill the GPU.
   const long long want = std::max<long long>(1, sms * 32ll / a.tokens);
-  a.parts = static_cast<int>(std::min<long long>(want, turns));
-  a.per = (turns + a.parts - 1) / a.parts;
-  a.parts = (turns + a.per - 1) / a.per;
-  const long long tasks = a.tokens * a.parts;
-  return launch(voc::rotate_kernel<T, L, NEAR>, dim3(static_cast<unsigned>((tasks + warps - 1) / warps)),
+  int parts = static_cast<int>(std::min<long long>({want, turns, 65535}));
+  a.per = (turns + parts - 1) / parts;
+  parts = (turns + a.per - 1) / a.per;
+  return launch(voc::rotate_kernel<T, L, NEAR>,
+                dim3(static_cast<unsigned>((a.tokens + warps - 1) / warps), static_cast<unsigned>(parts)),
                 dim3(voc::kRotThreads), 0, 1, stream, a);
 }
 template <typename T, bool NEAR>
@@ -73,8 +73,8 @@ VOC_API voc_status vocoder_lm_rotate(const void *q, long long ldq, long long hsq
       ldqo % 8 || hsqo % 8 || ldko % 8 || hsko % 8)
     return fail(VOC_INVALID_ARG,
                 "rotate: heads and weights must be 16-byte aligned, strides multiples of 8");
-  if (!aligned(positions, 4) || !aligned(axis, 4) || !aligned(turns, 8))
-    return fail(VOC_INVALID_ARG, "rotate: a buffer is not aligned to its type");
+  if (!aligned(positions, 4) || !aligned(axis, 8) || !aligned(turns, 16))
+    return fail(VOC_INVALID_ARG, "rotate: positions, axis (8 bytes) or turns (16) are not aligned");
   Device *dev;
   if (voc_status st = device(&dev); st != VOC_OK) return st;
   if (n_tokens == 0) return finish(*dev, stream, flags);
@@ -203,9 +203,9 @@ namespace {
 
 template <typename T, bool TOP>
 cudaError_t launch_logprobs(int sms, const voc::LmLogprobsArgs &a, voc_stream_t stream) {
-  // A warp has a row of up to 4096 values, a CTA a longer one, several CTAs while there are SMs for them
-  // and a CTA keeps 4096 values.
-  if (a.vocab <= 4096)
+  // A warp has a row of up to 4096 values where there are rows enough, a CTA another, several CTAs while there
+  // are SMs for them and a CTA keeps 4096 values.
+  if (a.vocab <= 4096 && a.rows > 4 * sms)
     return launch(voc::logprobs_kernel<T, 32, TOP>,
                   dim3(static_cast<unsigned>((a.rows + voc::kLpWarps - 1) / voc::kLpWarps)),
                   dim3(32 * voc::kLpWarps), 0, 1, stream, a);

@@ -605,7 +605,8 @@ voc_status vocoder_lm_attention(const void *q, long long ldq, long long hsq, int
  * stride ldp), axis int32 [pairs] or NULL (all pairs on axis 0); a pair with an axis outside 0..axes-1 is
  * not turned.  q or k may be absent (heads or kv_heads 0, NULL).  q_out and k_out may be the buffers of q
  * and k with their strides; otherwise they do not overlap with them.  head_dim a multiple of 16 up to 256,
- * pairs one of 8; heads, outputs and weights (of the same type) 16-byte aligned, strides multiples of 8.
+ * pairs one of 8; heads, outputs, weights (of the same type) and turns 16-byte aligned, axis 8-byte, strides
+ * multiples of 8.
  * A head with a NaN or an infinity does not touch others. */
 voc_status vocoder_lm_rotate(const void *q, long long ldq, long long hsq, int heads, const void *k,
                              long long ldk, long long hsk, int kv_heads, int head_dim, int dtype,
