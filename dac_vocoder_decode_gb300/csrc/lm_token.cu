@@ -167,6 +167,8 @@ VOC_API voc_status vocoder_lm_adapters(const void *x8, long long ldx, const floa
   if (!known_flags(flags)) return fail(VOC_INVALID_ARG, "adapters: flags");
   if (ldx < K || ldy < N || ldo < N || lda < K || ldb < rank)
     return fail(VOC_INVALID_ARG, "adapters: a row stride is below the width");
+  if (ldx > 0x7fffffff || ldy > 0x7fffffff || ldo > 0x7fffffff || lda > 0x7fffffff || ldb > 0x7fffffff)
+    return fail(VOC_UNSUPPORTED, "adapters: a row stride above 2^31 - 1");
   if (ldx % 16) return fail(VOC_INVALID_ARG, "adapters: the row stride of x8 must be a multiple of 16");
   if (lda % 8 || ldb % 8 || sa % 8 || sb % 8)
     return fail(VOC_INVALID_ARG, "adapters: strides of a and b must be multiples of 8");
