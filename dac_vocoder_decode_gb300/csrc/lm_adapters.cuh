@@ -83,7 +83,7 @@ __device__ __forceinline__ int binade(uint32_t amax) {
   return amax == 0 || amax >= kInfBits ? 0 : max(-126, min(126, e));
 }
 
-// The words of 8 (4) values of which the first `left` count, zeros for the others.
+// The words of 8 (4) values of which the first `left` (any number) count, zeros for the others.
 template <int WORDS>
 __device__ __forceinline__ void cut_words(uint32_t (&w)[WORDS], int left) {
 #pragma unroll
@@ -181,7 +181,7 @@ struct Eight {
 // y on the way.  So a few tokens keep 8 CTAs busy, and many tokens read every adapter once a tile, from
 // cache.
 template <typename W, typename Y, int R>
-__global__ void __launch_bounds__(kAdThreads) adapters_kernel(const LmAdaptersArgs p) {
+__global__ void __launch_bounds__(kAdThreads, R <= 64 ? 2 : 1) adapters_kernel(const LmAdaptersArgs p) {
   using Smem = AdapterSmem<R>;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ int rows[kAdTokens];
@@ -208,25 +208,22 @@ __global__ void __launch_bounds__(kAdThreads) adapters_kernel(const LmAdaptersAr
     same[h] = __match_any_sync(0xffffffffu, v);
   }
   bool repeated = false;  // the second half's id occurs in the first
-  for (int i = 0; i < 32; ++i) repeated |= __shfl_sync(0xffffffffu, id[0], i) == id[1];
-  const uint32_t first0 =
-      __ballot_sync(0xffffffffu, id[0] != -2 && __ffs(same[0]) - 1 == lane);
-  const uint32_t first1 =
-      __ballot_sync(0xffffffffu, id[1] != -2 && __ffs(same[1]) - 1 == lane && !repeated);
-  const int distinct = __popc(first0) + __popc(first1);
+  if (m0 + 32 < p.M)
+    for (int i = 0; i < 32; ++i) repeated |= __shfl_sync(0xffffffffu, id[0], i) == id[1];
+  const uint32_t below = (1u << lane) - 1u;
+  const bool leads0 = id[0] != -2 && __ffs(same[0]) - 1 == lane;
+  const bool leads1 = id[1] != -2 && __ffs(same[1]) - 1 == lane && !repeated;
+  const uint32_t first0 = __ballot_sync(0xffffffffu, leads0), first1 = __ballot_sync(0xffffffffu, leads1);
+  const int here = __popc(first0), distinct = here + __popc(first1);
 
   for (int turn = blockIdx.y; turn < distinct; turn += gridDim.y) {
-    const int here = __popc(first0);
-    int which;
-    if (turn < here)
-      which = __shfl_sync(0xffffffffu, id[0], __fns(first0, 0, turn + 1));
-    else
-      which = __shfl_sync(0xffffffffu, id[1], __fns(first1, 0, turn - here + 1));
+    const uint32_t at0 = __ballot_sync(0xffffffffu, leads0 && __popc(first0 & below) == turn);
+    const uint32_t at1 = __ballot_sync(0xffffffffu, leads1 && here + __popc(first1 & below) == turn);
+    const int which = __shfl_sync(0xffffffffu, at0 ? id[0] : id[1], __ffs(at0 | at1) - 1);
     const uint32_t use0 = __ballot_sync(0xffffffffu, id[0] == which);
     const uint32_t use1 = __ballot_sync(0xffffffffu, id[1] == which);
     const int count = __popc(use0) + __popc(use1);
     if (warp == 0) {
-      const uint32_t below = (1u << lane) - 1u;
       if (use0 >> lane & 1) rows[__popc(use0 & below)] = lane;
       if (use1 >> lane & 1) rows[__popc(use0) + __popc(use1 & below)] = 32 + lane;
     }
@@ -304,15 +301,15 @@ __global__ void __launch_bounds__(kAdThreads) adapters_kernel(const LmAdaptersAr
       __syncthreads();  // stage c has landed for all, and the stage before it has been read
       if (c + Smem::kStages - 1 < chunks) load(c + Smem::kStages - 1);
       copy_commit();
-      const uint8_t *xs = ring + (c % Smem::kStages) * Smem::kStage, *as = xs + Smem::kX;
+      const uint8_t *xs = ring + (c % Smem::kStages) * Smem::kStage + (mt * 16 + g) * kAdK + 8 * (t & 1);
+      const uint8_t *as = ring + (c % Smem::kStages) * Smem::kStage + Smem::kX + g * (2 * kAdK);
       for (int seg = share; seg < 8; seg += shares) {
         // lane t takes channels 8t to 8t + 7 of the segment in both operands
         uint32_t xa[2][4];
+        const int x_at = ((2 * seg + t / 2) ^ (g & 3) << 1) << 4, a_at = ((4 * seg + t) ^ (g & 1) << 2) << 4;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int r = mt * 16 + g + 8 * h;
-          const uint2 v = *reinterpret_cast<const uint2 *>(
-              xs + r * kAdK + (((2 * seg + t / 2) ^ (r & 3) << 1) << 4) + 8 * (t & 1));
+          const uint2 v = *reinterpret_cast<const uint2 *>(xs + 8 * h * kAdK + x_at);
           xa[0][h] = e4m3x2_to(v.x & 0xffffu, W());
           xa[0][2 + h] = e4m3x2_to(v.x >> 16, W());
           xa[1][h] = e4m3x2_to(v.y & 0xffffu, W());
@@ -321,9 +318,7 @@ __global__ void __launch_bounds__(kAdThreads) adapters_kernel(const LmAdaptersAr
 #pragma unroll
         for (int j = 0; j < R / 8; ++j) {
           if (j >= tiles8) break;
-          const int r = 8 * j + g;
-          const uint4 w = *reinterpret_cast<const uint4 *>(
-              as + r * (2 * kAdK) + (((4 * seg + t) ^ (r & 1) << 2) << 4));
+          const uint4 w = *reinterpret_cast<const uint4 *>(as + 8 * j * (2 * kAdK) + a_at);
           mma16(acc[j], xa[0], w.x, w.y, W());
           mma16(acc[j], xa[1], w.z, w.w, W());
         }
@@ -362,12 +357,15 @@ __global__ void __launch_bounds__(kAdThreads) adapters_kernel(const LmAdaptersAr
     const float scale = p.scale[which];
     for (int r0 = 0; r0 < count; r0 += kAdThreads / kQuads) {  // whole warps: they exchange maxima
       const int r = r0 + tid / kQuads;
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      if (r < count)
-        for (int q = 0; q < split; ++q) {
-          const float4 o = ld_cluster_f32x4(mapa_shared(sums_at + r * (R * 4), q));
-          v[0] += o.x, v[1] += o.y, v[2] += o.z, v[3] += o.w;
-        }
+      float4 all[8];  // read together, added in the CTAs' order
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        all[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < count && q < split) all[q] = ld_cluster_f32x4(mapa_shared(sums_at + r * (R * 4), q));
+      }
+      float v[4] = {all[0].x, all[0].y, all[0].z, all[0].w};
+#pragma unroll
+      for (int q = 1; q < 8; ++q) v[0] += all[q].x, v[1] += all[q].y, v[2] += all[q].z, v[3] += all[q].w;
       uint32_t top = max(max(abs_bits(v[0]), abs_bits(v[1])), max(abs_bits(v[2]), abs_bits(v[3])));
 #pragma unroll
       for (int o = 1; o < kQuads; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -388,12 +386,13 @@ __global__ void __launch_bounds__(kAdThreads) adapters_kernel(const LmAdaptersAr
         if (col == 0) factor[r] = p.xs[m0 + rows[r]] * pow2(e) * scale;
       }
     }
-    if (split > 1)
-      cluster_sync();  // every CTA has read the sums, and the ring may be written again
-    else
-      __syncthreads();
+    if (split > 1) cluster_arrive();  // has read the others' sums
+    __syncthreads();
 
     // ---------------------------------------------------------------- B v, this CTA's channels
+    const Y *y_tile = y + m0 * p.ldy;
+    Y *out_tile = out + m0 * p.ldo;
+    const int ldy = static_cast<int>(p.ldy), ldo = static_cast<int>(p.ldo), ldb = static_cast<int>(p.ldb);
     constexpr int kWords = R >= 32 ? 4 : 2;  // a lane's words of a row of B: 8 (4) ranks in a row
     constexpr int kBlocks = R >= 32 ? R / 32 : 1;
     for (int gr = g0 + warp; gr < g1; gr += 8) {
@@ -407,7 +406,7 @@ __global__ void __launch_bounds__(kAdThreads) adapters_kernel(const LmAdaptersAr
 #pragma unroll
           for (int w = 0; w < kWords; ++w) bw[j][i][w] = 0;
           if (left > 0) {
-            const W *from = b + n * p.ldb + k;
+            const W *from = b + static_cast<long long>(n) * ldb + k;
             if constexpr (kWords == 4) {
               const uint4 v = *reinterpret_cast<const uint4 *>(from);
               bw[j][i][0] = v.x, bw[j][i][1] = v.y, bw[j][i][2] = v.z, bw[j][i][3] = v.w;
@@ -415,9 +414,14 @@ __global__ void __launch_bounds__(kAdThreads) adapters_kernel(const LmAdaptersAr
               const uint2 v = *reinterpret_cast<const uint2 *>(from);
               bw[j][i][0] = v.x, bw[j][i][1] = v.y;
             }
-            if (left < 2 * kWords) cut_words(bw[j][i], left);
           }
         }
+      }
+      if (rank % (2 * kWords)) {  // behind all loads: a look at one value would wait for it
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < kBlocks; ++i) cut_words(bw[j][i], rank - 32 * i - 2 * kWords * t);
       }
       const int n = 32 * gr + 8 * t, left = p.N - n;
       constexpr int kTogether = sizeof(Y) == 4 ? 2 : 4;  // sixteens of tokens whose y is under way together
@@ -429,7 +433,7 @@ __global__ void __launch_bounds__(kAdThreads) adapters_kernel(const LmAdaptersAr
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int r = (first16 + m) * 16 + g + 8 * h;
-            if (r < count && left > 0) yw[m][h].load(y + (m0 + rows[r]) * p.ldy + n, left, start);
+            if (r < count && left > 0) yw[m][h].load(y_tile + static_cast<long long>(rows[r]) * ldy + n, left, start);
           }
 #pragma unroll
         for (int m = 0; m < kTogether; ++m) {
@@ -477,12 +481,13 @@ __global__ void __launch_bounds__(kAdThreads) adapters_kernel(const LmAdaptersAr
               f[2 * j + 1] = fmaf(o[j][2 * h + 1], by, f[2 * j + 1]);
             }
             yw[m][h].pack(f);
-            yw[m][h].store(out + (m0 + rows[r]) * p.ldo + n, left, start);
+            yw[m][h].store(out_tile + static_cast<long long>(rows[r]) * ldo + n, left, start);
           }
         }
       }
     }
-    __syncthreads();  // rows, factors and halves are read
+    if (split > 1) cluster_wait();  // nobody leaves or writes its sums' place while they are being read
+    __syncthreads();                // rows, factors and halves are read
   }
 }
 
