@@ -11,6 +11,11 @@ and summed, each layer is
 
 and the last norm's product gives fp32 latents for ``Vocoder.decode`` or ``VocoderStream.decode``.
 
+With ``rotary`` the queries and keys of each head are normalised and turned by their position in place of
+the sinusoids at the input; with ``voices`` every sequence has a low-rank adapter beside the products into q |
+k | v and out of the attention; with ``head`` a second last product gives the logits of the next frame's
+codes, which ``score`` takes for the log probabilities of given codes and the likeliest others.
+
     python -m dac_vocoder_decode_gb300.front        # a prompt, then streamed frames to audio
 """
 from __future__ import annotations
@@ -34,6 +39,10 @@ class FrontArch:
     window: int = 250  # keys that a query sees at most (0: all)
     books: int = 16
     entries: int = 2048
+    rotary: bool = False  # norms and rotation of queries and keys; else sinusoids at the input
+    voices: int = 0  # adapters that the sequences can have
+    rank: int = 16  # of each of them (a multiple of 8)
+    head: bool = False  # logits of the next frame's codes
 
 
 class Front:
@@ -69,6 +78,30 @@ class Front:
         self.frames = 0  # of every sequence, on the host
         half = torch.arange(a.dim // 2, device="cuda") / (a.dim // 2)
         self.rates = torch.exp(-math.log(1e4) * half)
+        # what the options add is drawn last: without them the weights are those of the plain stack
+        self.turns = None
+        if a.rotary:
+            pairs = a.head_dim // 2
+            at = torch.arange(pairs, device="cuda").double() / pairs
+            self.turns = V.rotation_turns(torch.exp(-math.log(1e4) * at))
+            for p in self.layers:
+                p["q_norm"], p["k_norm"] = norm(a.head_dim), norm(a.head_dim)
+
+        def adapter(n, k):
+            """A pool of low-rank adapters of a product [n, k]: down and up (bf16), their scales."""
+            wide = (k + 7) // 8 * 8
+            down = torch.randn((a.voices, a.rank, wide), generator=g, device="cuda") / math.sqrt(k)
+            up = torch.randn((a.voices, n, a.rank), generator=g, device="cuda") / math.sqrt(a.rank)
+            return (down.bfloat16()[:, :, :k], up.bfloat16(),
+                    0.2 + 0.2 * torch.rand(a.voices, generator=g, device="cuda"))
+
+        if a.voices:
+            for p in self.layers:
+                p["qkv_voice"] = adapter((a.heads + 2 * a.kv_heads) * a.head_dim, a.dim)
+                p["out_voice"] = adapter(a.dim, a.heads * a.head_dim)
+        if a.head:
+            self.codes_head = weight(a.books * a.entries, a.dim)
+        self.voice = torch.full((B,), -1, dtype=torch.int32, device="cuda")  # of each sequence, -1: none
         self._graph = None
 
     def reset(self):
@@ -76,32 +109,52 @@ class Front:
         self.lens.zero_()
         self.frames = 0
 
-    def _run(self, codes, new: int, max_kv: int):
-        """codes [B, new, books] -> latents [B, latent, new] fp32; the lengths on the device count
-        the new frames already."""
+    def _product(self, p, name, h, hs, voice):
+        """A product with each token's own adapter beside it."""
+        y = V.linear_fp8(h, hs, *p[name])
+        if voice is not None:
+            V.adapters_fp8(y, h, hs, *p[name + "_voice"], voice, out=y)
+        return y
+
+    def _hidden(self, codes, new: int, max_kv: int):
+        """codes [B, new, books] -> the last norm's rows in e4m3 and their scales; the lengths on the
+        device count the new frames already."""
         import torch
         a = self.arch
         at = self.lens[:, None] - new + torch.arange(new, device="cuda")  # positions
-        turn = at[:, :, None] * self.rates
         x = self.embed[torch.arange(a.books, device="cuda"), codes].sum(2)
-        x = (x + torch.cat([turn.sin(), turn.cos()], 2)).view(-1, a.dim).bfloat16()
+        if a.rotary:
+            x, at = x.view(-1, a.dim).bfloat16(), at.to(torch.int32).view(-1)
+        else:
+            turn = at[:, :, None] * self.rates
+            x = (x + torch.cat([turn.sin(), turn.cos()], 2)).view(-1, a.dim).bfloat16()
+        voice = self.voice[:, None].expand(-1, new).reshape(-1) if a.voices else None
         delta = None
         for p, cache in zip(self.layers, self.cache):
             h, hs, total = V.rows_fp8(x, V.VOC_LM_RMS, weight=p["norm1"], residual=delta)
             x = x if total is None else total
-            qkv = V.linear_fp8(h, hs, *p["qkv"]).view(-1, a.heads + 2 * a.kv_heads, a.head_dim)
+            qkv = self._product(p, "qkv", h, hs, voice).view(-1, a.heads + 2 * a.kv_heads, a.head_dim)
             q, k, v = qkv.split([a.heads, a.kv_heads, a.kv_heads], 1)
+            if a.rotary:
+                V.rotate_heads(q, k, at, self.turns, q_weight=p["q_norm"], k_weight=p["k_norm"], q_out=q,
+                               k_out=k)
             V.kv_append_fp8(cache, k, v, self.page_table, self.lens, max_q=new)
             o = V.attention_fp8(q, cache, self.page_table, self.lens, max_q=new, max_kv=max_kv,
                                 window=a.window)
             h, hs, _ = V.rows_fp8(o.view(-1, a.heads * a.head_dim), V.VOC_LM_NONE)
-            delta = V.linear_fp8(h, hs, *p["out"])
+            delta = self._product(p, "out", h, hs, voice)
             h, hs, x = V.rows_fp8(x, V.VOC_LM_RMS, weight=p["norm2"], residual=delta)
             h, hs, _ = V.rows_fp8(V.linear_fp8(h, hs, *p["up"]), V.VOC_LM_GATED)
             delta = V.linear_fp8(h, hs, *p["down"])
         h, hs, _ = V.rows_fp8(x, V.VOC_LM_RMS, weight=self.last_norm, residual=delta)
+        return h, hs
+
+    def _run(self, codes, new: int, max_kv: int):
+        """codes [B, new, books] -> latents [B, latent, new] fp32 (as _hidden)."""
+        import torch
+        h, hs = self._hidden(codes, new, max_kv)
         y = V.linear_fp8(h, hs, *self.last, out_dtype=torch.float32)
-        return y.view(self.B, new, a.latent).transpose(1, 2).contiguous()
+        return y.view(self.B, new, self.arch.latent).transpose(1, 2).contiguous()
 
     def _room(self, new: int):
         if self.frames + new > self.max_frames:
@@ -114,6 +167,30 @@ class Front:
         self._room(codes.shape[1])
         self.lens += codes.shape[1]
         return self._run(codes, codes.shape[1], self.frames)
+
+    def score(self, codes, top: int = 0, temperature: float = 1.0):
+        """The next codes [B, new, books] of every sequence at once, as prompt takes them -> (logprob,
+        entropy, top_logprobs, top_codes): of each frame's codes behind the first (what the frames before
+        it say of it) fp32 [B, new - 1, books], and the `top` likeliest codes of each frame's successor, fp32
+        and int64 [B, new, books, top] (None with top=0).  entropy is fp32 [B, new, books], of the
+        successors."""
+        import torch
+        a, (B, new, books) = self.arch, codes.shape
+        if not a.head:
+            raise V.VocoderError(V.VOC_INVALID_ARG, "score needs head=True")
+        self._room(new)
+        self.lens += new
+        h, hs = self._hidden(codes, new, self.frames)
+        logits = V.linear_fp8(h, hs, *self.codes_head, out_dtype=torch.float32).view(-1, a.entries)
+        # the codes that each frame's logits speak of: the next frame's, none behind the last
+        given = torch.full_like(codes, -1)
+        given[:, :-1] = codes[:, 1:]
+        logprob, entropy, best, best_codes = V.logprobs(logits, given.view(-1), top=top,
+                                                        temperature=temperature)
+        shape = (B, new, books)
+        return (logprob.view(shape)[:, :-1], entropy.view(shape),
+                None if best is None else best.view(*shape, top),
+                None if best_codes is None else best_codes.view(*shape, top))
 
     def step(self, codes):
         """One frame of codes [B, books] of every sequence -> latents [B, latent, 1].  The launches
