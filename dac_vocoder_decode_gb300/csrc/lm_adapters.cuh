@@ -43,7 +43,7 @@ struct AdapterSmem {
 
 __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
                                       __half) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -51,7 +51,7 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
 }
 __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
                                       __nv_bfloat16) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -180,6 +180,11 @@ struct Eight {
 // memory by all of them, in a fixed order.  Second product: each CTA a part of the output channels, added to
 // y on the way.  So a few tokens keep 8 CTAs busy, and many tokens read every adapter once a tile, from
 // cache.
+// Measured: 8 tokens with a voice each, 1024 -> 1536, rank 16: 5.2 us, two barriers of the cluster in a chain of
+// five reads; 33 x 4096 -> 12288, rank 16: 11.0 us; 15423 tokens x 1001 -> 1540, rank 32: 53 us, 2.1 TB/s (rows
+// of y start on 8 bytes); 15504 x 4096 -> 4096, rank 64: 124 us, 2.6 TB/s.  Bound by latencies: 16 warps an SM,
+// what 128 registers leave (3 CTAs of 80: prompts 76 us), issue in 44 % of the cycles, the matrix pipe a third.
+// Skipping the eights of ranks that an adapter lacks cost the full ones more (136 us) than it spares.
 template <typename W, typename Y, int R>
 __global__ void __launch_bounds__(kAdThreads, R <= 64 ? 2 : 1) adapters_kernel(const LmAdaptersArgs p) {
   using Smem = AdapterSmem<R>;
@@ -263,7 +268,6 @@ __global__ void __launch_bounds__(kAdThreads, R <= 64 ? 2 : 1) adapters_kernel(c
     const int s1 = static_cast<int>(static_cast<long long>(segs) * (part + 1) / split);
     const int chunks = (s1 - s0 + 7) / 8;
     const int k_end = min(p.K, s1 * kAdSeg);
-    const int tiles8 = (rank + 7) / 8;  // eights of ranks
     const uint32_t base = smem_u32(ring);
     auto load = [&](int c) {
       const uint32_t xs = base + (c % Smem::kStages) * Smem::kStage, as = xs + Smem::kX;
@@ -278,7 +282,7 @@ __global__ void __launch_bounds__(kAdThreads, R <= 64 ? 2 : 1) adapters_kernel(c
       {
         const int chunk = lane, k = k0 + 8 * chunk;
         const int bytes = max(0, min(16, 2 * (k_end - k)));
-        for (int r = warp; r < tiles8 * 8; r += kAdThreads / 32) {
+        for (int r = warp; r < R; r += kAdThreads / 32) {  // zeros behind the rank
           const int some = r < rank ? bytes : 0;
           copy16(as + r * (2 * kAdK) + ((chunk ^ (r & 1) << 2) << 4),
                  some ? static_cast<const void *>(a + r * p.lda + k) : p.a, some);
@@ -317,7 +321,6 @@ __global__ void __launch_bounds__(kAdThreads, R <= 64 ? 2 : 1) adapters_kernel(c
         }
 #pragma unroll
         for (int j = 0; j < R / 8; ++j) {
-          if (j >= tiles8) break;
           const uint4 w = *reinterpret_cast<const uint4 *>(as + 8 * j * (2 * kAdK) + a_at);
           mma16(acc[j], xa[0], w.x, w.y, W());
           mma16(acc[j], xa[1], w.z, w.w, W());
