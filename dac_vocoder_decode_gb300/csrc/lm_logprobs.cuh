@@ -268,11 +268,12 @@ __device__ __forceinline__ void lp_bound(LpShared<TPR> &sh, int k, int lane) {
 // and they are gathered again.
 // Bound by instructions beside DRAM: 4001 rows of 50001 f16 values, 5 alternatives: 82 us, 4.9 TB/s (six
 // instructions a value in the stream, as many again for a row's way in and out; 5 CTAs on an SM, with 4 87 us,
-// with 6 or 3 101; rows of 128 threads 83); 15504 x 2048 bf16, none: 15.0 us, 4.2 TB/s (a warp a row, 36 on an
+// with 6 or 3 101; rows of 128 threads 83); 15504 x 2048 bf16, none: 15.1 us, 4.2 TB/s (a warp a row, 36 on an
 // SM; with 48 19.9, with 32 15.9).  Few rows by latency: 128 x 2048, 20 alternatives 4.7 us, 8 x 131072 f32, 20
 // alternatives 9.8 (8 CTAs a row; rows of 128 threads 12.2).
 template <typename T, int TPR, bool TOP>
-__global__ void __launch_bounds__(TPR == 32 ? 32 * kLpWarps : kLpWide, TPR > 32 && sizeof(T) == 2 ? 5 : 1)
+__global__ void __launch_bounds__(TPR == 32 ? 32 * kLpWarps : kLpWide,
+                                  TPR == 32 ? (sizeof(T) == 2 ? 9 : 5) : (sizeof(T) == 2 ? 5 : 3))
     logprobs_kernel(const LmLogprobsArgs p) {
   using Row = LpRow<T>;
   constexpr int B = Row::kBatch, N = Row::N;

@@ -601,8 +601,8 @@ voc_status vocoder_lm_attention(const void *q, long long ldq, long long hsq, int
  * rounded once.  Pair p < pairs is channels (p, p + pairs) with neighbours = 0, (2p, 2p + 1) with 1; the
  * channels behind the first 2 * pairs are not turned.  The angle is positions[axis[p]][token] * turns[p] in
  * units of 2^-64 of a turn, whole turns dropped: turns[p] = rate / (2 pi) * 2^64 modulo 2^64 for a rate in
- * radians, so that no position is too far for an exact angle.  positions int32 [axes][n_tokens] (row
- * stride ldp), axis int32 [pairs] or NULL (all pairs on axis 0); a pair with an axis outside 0..axes-1 is
+ * radians, so that no position is too far for an exact angle.  positions int32 [axes][n_tokens] (1 to 16
+ * axes, row stride ldp), axis int32 [pairs] or NULL (all pairs on axis 0); a pair with an axis outside 0..axes-1 is
  * not turned.  q or k may be absent (heads or kv_heads 0, NULL).  q_out and k_out may be the buffers of q
  * and k with their strides; otherwise they do not overlap with them.  head_dim a multiple of 16 up to 256,
  * pairs one of 8; heads, outputs, weights (of the same type) and turns 16-byte aligned, axis 8-byte, strides
@@ -623,8 +623,8 @@ voc_status vocoder_lm_rotate(const void *q, long long ldq, long long hsq, int he
  * b [pool][N][rank] (ldb, sb) bf16 or f16 (dtype), 16-byte aligned, strides multiples of 8; y and out [M][N]
  * in the adapters' type or f32, out may be y (same stride) and otherwise does not overlap with it; scale
  * fp32 [pool]; ids int32 [M] in any order.  rank: a multiple of 8 up to 128; ranks int32 [pool] or NULL: the
- * rank of each adapter (0 to rank), what lies behind it in a and b is not used.  Sums are 32-bit; the
- * low-rank values keep 16 (bf16) or 22 (f16) bits between the products. */
+ * rank of each adapter (0 to rank), what lies behind it in a and b is not used.  Row strides stay below
+ * 2^31.  Sums are 32-bit; the low-rank values keep 16 (bf16) or 22 (f16) bits between the products. */
 voc_status vocoder_lm_adapters(const void *x8, long long ldx, const float *x_scale, const void *y,
                                long long ldy, int y_dtype, const void *a, long long lda, long long sa,
                                const void *b, long long ldb, long long sb, int dtype,
@@ -633,7 +633,7 @@ voc_status vocoder_lm_adapters(const void *x8, long long ldx, const float *x_sca
                                voc_stream_t stream, unsigned flags);
 
 /* Rows of logits [rows][vocab] (bf16, f16 or f32, row stride ldl >= vocab, any alignment of the type).  With
- * z = logits / temperature and lse = log sum exp z:
+ * z = logits / temperature (2^-20 to 2^20) and lse = log sum exp z:
  *   logprob[row] = z[tokens[row]] - lse      (tokens int64 [rows]; both NULL: not wanted)
  *   entropy[row] = lse - sum_i exp(z_i - lse) z_i   (NULL: not wanted)
  *   top_tokens[row][0..top-1], top_logprobs: the top (0 to 32) largest logits in falling order, equal ones by
