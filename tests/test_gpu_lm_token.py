@@ -297,11 +297,13 @@ def test_adapters_orders_of_tokens(M, how):
     c.check(got)
     if how == "none":
         assert torch.equal(got, c.y)
-    # a token's result does not depend on its neighbours
+    # in another order: the same up to the order of 32-bit sums, which goes by the number of tokens that share an
+    # adapter in a tile; the same bits where they are alone
     order = torch.randperm(M, generator=_gen(1), device="cuda")
     c.x, c.x_scale, c.y, c.ids = (c.x8[order].view(torch.float8_e4m3fn)[:, :c.K], c.x_scale[order], c.y[order],
                                   c.ids[order])
-    assert torch.equal(c.run(), got[order]) or how == "runs"
+    if how in ("each", "none"):
+        assert torch.equal(c.run(), got[order])
     c.check(c.run())
 
 
