@@ -162,8 +162,8 @@ VOC_API voc_status vocoder_lm_adapters(const void *x8, long long ldx, const floa
   if (dtype != VOC_LM_BF16 && dtype != VOC_LM_F16) return fail(VOC_INVALID_ARG, "adapters: dtype");
   if (y_dtype != dtype && y_dtype != VOC_LM_F32)
     return fail(VOC_INVALID_ARG, "adapters: y_dtype must be the adapters' type or f32");
-  if (M < 0 || N < 0 || K < 1 || M > (1 << 28) || N > (1 << 28) || K > (1 << 28))
-    return fail(VOC_INVALID_ARG, "adapters: sizes");
+  if (M < 0 || N < 0 || K < 1 || M > (1 << 28) || N > (1 << 24) || K > (1 << 28))
+    return fail(VOC_INVALID_ARG, "adapters: sizes");  // 32-bit counters of a tile's values
   if (rank < 8 || rank > 128 || rank % 8)
     return fail(VOC_UNSUPPORTED, "adapters: rank must be a multiple of 8 up to 128");
   if (pool < 1) return fail(VOC_INVALID_ARG, "adapters: pool");

@@ -56,7 +56,8 @@ ADAPTERS = dict(x8=PTR, ldx=64, x_scale=PTR, y=PTR, ldy=40, y_dtype=V.VOC_LM_BF1
 @pytest.mark.parametrize("change,text,status", [
     (dict(dtype=V.VOC_LM_F32, y_dtype=V.VOC_LM_F32), "dtype", BAD), (dict(y_dtype=V.VOC_LM_F16), "y_dtype", BAD),
     (dict(y_dtype=7), "y_dtype", BAD), (dict(M=-1), "sizes", BAD), (dict(K=0), "sizes", BAD),
-    (dict(N=1 << 29), "sizes", BAD), (dict(rank=0), "rank", NOT), (dict(rank=12), "rank", NOT),
+    (dict(N=1 << 29), "sizes", BAD), (dict(N=(1 << 24) + 1, ldy=1 << 25, ldo=1 << 25), "sizes", BAD),
+    (dict(rank=0), "rank", NOT), (dict(rank=12), "rank", NOT),
     (dict(rank=136), "rank", NOT), (dict(pool=0), "pool", BAD), (dict(flags=4), "flags", BAD),
     (dict(ldx=48), "stride", BAD), (dict(ldy=39), "stride", BAD), (dict(ldo=39), "stride", BAD),
     (dict(lda=56), "stride", BAD), (dict(ldb=8), "stride", BAD), (dict(ldx=72), "multiple of 16", BAD),
