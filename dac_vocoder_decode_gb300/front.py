@@ -182,8 +182,9 @@ class Front:
         self.lens += new
         h, hs = self._hidden(codes, new, self.frames)
         logits = V.linear_fp8(h, hs, *self.codes_head, out_dtype=torch.float32).view(-1, a.entries)
-        # the codes that each frame's logits speak of: the next frame's, none behind the last
-        given = torch.full_like(codes, -1)
+        # the codes that each frame's logits speak of: the next frame's, none behind the last; in rows whatever
+        # the codes' strides, type and device are
+        given = torch.full(codes.shape, -1, dtype=torch.int64, device=logits.device)
         given[:, :-1] = codes[:, 1:]
         logprob, entropy, best, best_codes = V.logprobs(logits, given.view(-1), top=top,
                                                         temperature=temperature)
