@@ -173,11 +173,16 @@ class Front:
         entropy, top_logprobs, top_codes): of each frame's codes behind the first (what the frames before
         it say of it) fp32 [B, new - 1, books], and the `top` likeliest codes of each frame's successor, fp32
         and int64 [B, new, books, top] (None with top=0).  entropy is fp32 [B, new, books], of the
-        successors."""
+        successors.  A call that is refused takes no frames."""
         import torch
-        a, (B, new, books) = self.arch, codes.shape
+        a, shape = self.arch, tuple(codes.shape)
         if not a.head:
             raise V.VocoderError(V.VOC_INVALID_ARG, "score needs head=True")
+        # everything is refused before the frames are taken: the cache cannot give them back unchanged
+        if len(shape) != 3 or shape[0] != self.B or shape[2] != a.books or codes.is_floating_point():
+            raise V.VocoderError(V.VOC_INVALID_ARG, f"codes must be whole numbers [{self.B}, new, {a.books}]")
+        V.logprobs(self.embed.new_empty((0, a.entries)), top=top, temperature=temperature, entropy=False)
+        new = shape[1]
         self._room(new)
         self.lens += new
         h, hs = self._hidden(codes, new, self.frames)
@@ -188,7 +193,6 @@ class Front:
         given[:, :-1] = codes[:, 1:]
         logprob, entropy, best, best_codes = V.logprobs(logits, given.view(-1), top=top,
                                                         temperature=temperature)
-        shape = (B, new, books)
         return (logprob.view(shape)[:, :-1], entropy.view(shape),
                 None if best is None else best.view(*shape, top),
                 None if best_codes is None else best_codes.view(*shape, top))

@@ -10,6 +10,7 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():  # collected on CPU-only machines, never run there
     pytest.skip("no CUDA device", allow_module_level=True)
 
+from dac_vocoder_decode_gb300 import binding as V  # noqa: E402
 from dac_vocoder_decode_gb300.front import Front  # noqa: E402
 from tests.test_gpu_front_token import TOKEN, _codes, _voices  # noqa: E402
 
@@ -35,3 +36,24 @@ def test_score_takes_the_codes_that_a_prompt_takes(how):
     assert torch.equal(front.prompt(given), latent)
     front.reset()
     assert _same(front.score(given, top=4), want)
+
+
+@pytest.mark.parametrize("change", [dict(top=33), dict(top=65), dict(top=-1), dict(temperature=0.0),
+                                    dict(temperature=float("nan")), dict(books=3), dict(sequences=1),
+                                    dict(frames=99), dict(floats=True)])
+def test_a_refused_score_takes_no_frames(change):
+    """The sequence goes on where it was: the score after the refusal is that of a stack that never saw it."""
+    codes = _codes(2, 70, seed=8)
+    front, other = Front(TOKEN, 2, 70), Front(TOKEN, 2, 70)
+    for f in (front, other):
+        _voices(f, -1, 2)
+        f.prompt(codes[:, :20])
+    bad = _codes(2, change.pop("frames", 50), seed=9)
+    bad = bad[:change.pop("sequences", 2), :, :change.pop("books", 4)]
+    if change.pop("floats", False):
+        bad = bad.float()
+    with pytest.raises(V.VocoderError) as e:
+        front.score(bad, **change)
+    assert e.value.status in (V.VOC_INVALID_ARG, V.VOC_UNSUPPORTED)
+    assert front.frames == 20 and front.lens.tolist() == [20, 20]
+    assert _same(front.score(codes[:, 20:], top=3), other.score(codes[:, 20:], top=3))
