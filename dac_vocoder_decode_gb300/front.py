@@ -101,8 +101,22 @@ class Front:
                 p["out_voice"] = adapter(a.dim, a.heads * a.head_dim)
         if a.head:
             self.codes_head = weight(a.books * a.entries, a.dim)
-        self.voice = torch.full((B,), -1, dtype=torch.int32, device="cuda")  # of each sequence, -1: none
+        self._voice = torch.full((B,), -1, dtype=torch.int32, device="cuda")
         self._graph = None
+
+    @property
+    def voice(self):
+        """The adapter of each sequence, int32 [B] on the device; -1: none.  What is assigned (a tensor or a
+        sequence of B) is copied into it, so captured steps take it too."""
+        return self._voice
+
+    @voice.setter
+    def voice(self, voice):
+        import torch
+        voice = torch.as_tensor(voice)
+        if tuple(voice.shape) != (self.B,) or voice.is_floating_point():
+            raise V.VocoderError(V.VOC_INVALID_ARG, f"voice must be {self.B} whole numbers")
+        self._voice.copy_(voice)
 
     def reset(self):
         """Forget all frames."""
@@ -128,7 +142,7 @@ class Front:
         else:
             turn = at[:, :, None] * self.rates
             x = (x + torch.cat([turn.sin(), turn.cos()], 2)).view(-1, a.dim).bfloat16()
-        voice = self.voice[:, None].expand(-1, new).reshape(-1) if a.voices else None
+        voice = self._voice[:, None].expand(-1, new).reshape(-1) if a.voices else None
         delta = None
         for p, cache in zip(self.layers, self.cache):
             h, hs, total = V.rows_fp8(x, V.VOC_LM_RMS, weight=p["norm1"], residual=delta)

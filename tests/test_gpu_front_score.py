@@ -57,3 +57,23 @@ def test_a_refused_score_takes_no_frames(change):
     assert e.value.status in (V.VOC_INVALID_ARG, V.VOC_UNSUPPORTED)
     assert front.frames == 20 and front.lens.tolist() == [20, 20]
     assert _same(front.score(codes[:, 20:], top=3), other.score(codes[:, 20:], top=3))
+
+
+@pytest.mark.parametrize("how", ["list", "int32", "int64", "host"])
+def test_assigned_voices_reach_captured_steps(how):
+    """The graph of a step reads the voices that were assigned behind its capture."""
+    codes = _codes(2, 6, seed=10)
+    front, other = Front(TOKEN, 2, 6), Front(TOKEN, 2, 6)
+    _voices(other, 2, -1)
+    want = [other.step(codes[:, i]).clone() for i in range(6)]
+    front.step(codes[:, 0])
+    front.reset()
+    given = torch.tensor([2, -1], dtype=torch.int32 if how == "int32" else torch.int64,
+                         device="cpu" if how == "host" else "cuda")
+    front.voice = given.tolist() if how == "list" else given
+    assert front.voice.tolist() == [2, -1] and front.voice.dtype == torch.int32
+    assert _same([front.step(codes[:, i]).clone() for i in range(6)], want)
+    for bad in ([0], [[0, 1]], [0.5, 1.0], 1):
+        with pytest.raises(V.VocoderError):
+            front.voice = bad
+    assert front.voice.tolist() == [2, -1]
