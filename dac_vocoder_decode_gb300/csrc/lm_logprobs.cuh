@@ -5,9 +5,11 @@
 //   top: the k largest x, the lowest index first among equal ones, and their log probabilities
 //
 // One pass over the row with a running maximum m and the sums s = sum e^((x - m) c), t = sum (x - m) c
-// e^((x - m) c), c = log2(e) / temperature and powers of two: logprob = ln2 ((x - m) c - log2 s), entropy =
-// ln2 (log2 s - t / s).  x - m is taken before the factor, so values at the end of the type's range do not
-// overflow; its lowest value as a mask in every place gives equal weights, as the formula does.
+// e^((x - m) c), c = log2(e) / temperature and powers of two: logprob = (x - m) / temperature - ln2 log2 s,
+// entropy = ln2 (log2 s - t / s).  In the sums x - m is taken before the factor and may leave 32 bits: the weight is
+// 0 all the same, and the type's lowest value as a mask in every place gives equal weights, as the formula
+// does.  In the results it is taken by halves and without log2(e), so that one that 32 bits hold does not
+// overflow on the way (a token of the type's lowest value beside ordinary ones).
 #pragma once
 #include "lm_common.cuh"
 
@@ -20,7 +22,7 @@ struct LmLogprobsArgs {
   long long *top_tokens;
   long long rows, ldx;
   int vocab, k;
-  float c;
+  float c, twice;  // log2(e) / temperature, 2 / temperature
 };
 
 constexpr int kLpMaxTop = 32;
@@ -447,18 +449,21 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kLpWarps : kLpWide,
     constexpr float kLn2 = 0.693147181f;
     const float log2s = log2f(mine.s);
     const bool none = mine.s == 0.f;  // nothing but -infinity: no token has any weight
+    auto logprob = [&](float x) {
+      return none ? -INFINITY : fmaf(0.5f * x - 0.5f * mine.m, p.twice, -kLn2 * log2s);
+    };
     if (tid == 0) {
       if (p.entropy) p.entropy[at] = none ? 0.f : (log2s - mine.t / mine.s) * kLn2;
       if (p.tokens) {
         const long long i = p.tokens[at];
         const float x = i >= 0 && i < p.vocab ? to_f32(row.row[i]) : -INFINITY;
-        p.logprob[at] = none ? -INFINITY : ((x - mine.m) * c - log2s) * kLn2;
+        p.logprob[at] = logprob(x);
       }
     }
     if constexpr (TOP) {
       if (lane < p.k) {
         const unsigned long long key = sh.top[lane];
-        p.top[at * p.k + lane] = none ? -INFINITY : ((key_value(key) - mine.m) * c - log2s) * kLn2;
+        p.top[at * p.k + lane] = logprob(key_value(key));
         p.top_tokens[at * p.k + lane] = key_index(key);
       }
     }

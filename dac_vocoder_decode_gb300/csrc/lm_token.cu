@@ -251,7 +251,7 @@ VOC_API voc_status vocoder_lm_logprobs(const void *logits, long long ldl, int dt
   if (voc_status st = device(&dev); st != VOC_OK) return st;
   if (rows == 0 || (!logprob && !entropy && !top)) return finish(*dev, stream, flags);
   voc::LmLogprobsArgs a{logits, tokens, logprob, entropy, top_logprobs, top_tokens, rows, ldl, vocab, top,
-                        static_cast<float>(1.4426950408889634 / temperature)};
+                        static_cast<float>(1.4426950408889634 / temperature), 2.f / temperature};
   cudaError_t e;
   if (dtype == VOC_LM_F32)
     e = launch_logprobs<float>(dev->sms, a, stream);

@@ -1,0 +1,48 @@
+"""GPU: low-rank adapters and log probabilities at the launch shapes and ends of ranges that small calls do not
+reach, against 64-bit forms.  Tolerances as in test_gpu_lm_token.py unless a test derives its own."""
+from __future__ import annotations
+
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # collected on CPU-only machines, never run there
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+from dac_vocoder_decode_gb300 import binding as V  # noqa: E402
+from tests import test_gpu_lm_token as T  # noqa: E402
+
+SYNC = V.VOC_FLAG_SYNC
+SMS = torch.cuda.get_device_properties(0).multi_processor_count
+
+
+# ------------------------------------------------------------------ log probabilities
+@pytest.mark.parametrize("temperature", [0.7, 1.0, 1.3, 4.0])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,vocab", [(5, 50), (5, 3000), (4 * SMS + 3, 2048), (3, 9001), (3, 70001)])
+def test_logprobs_of_the_lowest_value_beside_ordinary_ones(rows, vocab, dtype, temperature):
+    """A mask of the type's lowest value: its tokens' log probabilities as far as 32 bits hold them, -infinity beyond.
+
+    1 / temperature, the difference and their product round by 2^-24 each, the sum by one more: below 2^-21 of
+    the result, beside the sums' error of an ordinary row, far below 1e-4."""
+    t, g = T.TYPES[dtype], T._gen(vocab)
+    x = T._randn(g, rows, vocab) * 3
+    x = x.to(t)
+    x[:, 20:] = torch.finfo(t).min
+    x[1, 7] = torch.finfo(t).max  # a difference of twice the range
+    tokens = torch.randint(0, 40, (rows,), generator=g, device="cuda")
+    tokens[0], tokens[1], tokens[2] = vocab - 1, 30, 3
+    lp, ent, top, top_tokens = V.logprobs(x, tokens, top=32, temperature=temperature, flags=SYNC)
+    want = T._exact_logprobs(x, tokens, 32, temperature)
+    assert torch.equal(top_tokens, want[3])
+    for got, ref in ((lp, want[0]), (ent, want[1]), (top, want[2])):
+        gone = ref.float() == -math.inf
+        assert torch.equal(got == -math.inf, gone)
+        off = (got.double() - ref).masked_fill(gone, 0).abs()
+        assert bool((off <= ref.abs().masked_fill(gone, 0) * 2.0 ** -21 + 1e-4).all())
+    if dtype != "f16" and temperature == 1:
+        assert bool((lp[0] < -3e38) & (lp[0] > -math.inf)) and lp[1] == -math.inf
