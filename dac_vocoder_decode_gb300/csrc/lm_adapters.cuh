@@ -77,10 +77,10 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// 2^-e with the largest of magnitude `amax` brought to [1, 2); 1 for zeros, infinities and NaN.
+// The exponent e, from -126 to 126, for which 2^-e brings the finite value of magnitude bits `amax` to [1, 2)
+// (0 for zeros; beyond those exponents as near as they go).
 __device__ __forceinline__ int binade(uint32_t amax) {
-  const int e = static_cast<int>(amax >> 23) - 127;
-  return amax == 0 || amax >= kInfBits ? 0 : max(-126, min(126, e));
+  return amax == 0 ? 0 : max(-126, min(126, static_cast<int>(amax >> 23) - 127));
 }
 
 // The words of 8 (4) values of which the first `left` (any number) count, zeros for the others.
@@ -369,7 +369,9 @@ __global__ void __launch_bounds__(kAdThreads, R <= 64 ? 2 : 1) adapters_kernel(c
       float v[4] = {all[0].x, all[0].y, all[0].z, all[0].w};
 #pragma unroll
       for (int q = 1; q < 8; ++q) v[0] += all[q].x, v[1] += all[q].y, v[2] += all[q].z, v[3] += all[q].w;
-      uint32_t top = max(max(abs_bits(v[0]), abs_bits(v[1])), max(abs_bits(v[2]), abs_bits(v[3])));
+      uint32_t top = 0;  // of the finite ones, which stay finite in 16 bits beside an infinity
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = max(top, abs_bits(v[i]) < kInfBits ? abs_bits(v[i]) : 0u);
 #pragma unroll
       for (int o = 1; o < kQuads; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       const int e = binade(top);
@@ -379,7 +381,8 @@ __global__ void __launch_bounds__(kAdThreads, R <= 64 ? 2 : 1) adapters_kernel(c
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[i] *= down;
-        lo[i] = v[i] - to_f32(from_f32<W>(v[i]));
+        // an infinity is whole in the first half (infinity less itself would be NaN)
+        lo[i] = abs_bits(v[i]) == kInfBits ? 0.f : v[i] - to_f32(from_f32<W>(v[i]));
       }
       hw = make_uint2(pack2<W>(v[0], v[1]), pack2<W>(v[2], v[3]));
       lw = make_uint2(pack2<W>(lo[0], lo[1]), pack2<W>(lo[2], lo[3]));

@@ -20,6 +20,34 @@ SYNC = V.VOC_FLAG_SYNC
 SMS = torch.cuda.get_device_properties(0).multi_processor_count
 
 
+# ------------------------------------------------------------------ low-rank adapters
+@pytest.mark.parametrize("dtype,y_dtype", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "f32"), ("f16", "f32")])
+@pytest.mark.parametrize("M,N,K,rank", [(6, 70, 64, 8), (40, 33, 96, 16), (150, 64, 300, 32), (70, 40, 64, 128)])
+def test_adapters_infinite_low_rank_values_stay_infinite(M, N, K, rank, dtype, y_dtype):
+    """An infinity in A: the formula's infinities, their signs and its NaN (0 times an infinity, two of unlike sign);
+    finite low-rank values beside them, beyond 16 bits too, take nothing away.  Tokens of others are ordinary."""
+    c = T.Adapters(M, N, K, rank, 3, dtype, y_dtype, ids=torch.arange(M, device="cuda") % 4 - 1)
+    c.a[1] *= 1000
+    c.a[1, 2, 5] = math.inf
+    c.a[2, 0, 1], c.a[2, 3, 9] = math.inf, -math.inf
+    c.x8[3::8, 5] = 0
+    got = c.run()
+    ref = c.y.double()
+    for i in range(3):
+        rows = torch.nonzero(c.ids == i)[:, 0]
+        x = c.x[rows].double() * c.x_scale[rows].double()[:, None]
+        ref[rows] += float(c.scale[i]) * (x @ c.a[i].double().T) @ c.b[i].double().T
+    far = (c.ids == 1) | (c.ids == 2)
+    assert bool(torch.isinf(ref[far]).any()) and bool(torch.isnan(ref[far]).any())
+    assert not bool(torch.isfinite(ref[far]).any())
+    assert torch.equal(torch.isnan(got), torch.isnan(ref))
+    assert torch.equal(got[far].double().nan_to_num(0, 1, -1), ref[far].nan_to_num(0, 1, -1))
+    c.a[1:] = 0
+    again = c.run()
+    assert torch.equal(again[~far], got[~far])
+    c.check(again)
+
+
 # ------------------------------------------------------------------ log probabilities
 @pytest.mark.parametrize("temperature", [0.7, 1.0, 1.3, 4.0])
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
