@@ -3,9 +3,12 @@
 //   out[m] = y[m] + scale[a] * xs[m] * B_a (A_a x[m]),   a = ids[m]   (no adapter: out[m] = y[m])
 //
 // x in e4m3 with a scale per row, as the projection takes it; A_a [rank][K] and B_a [N][rank] in 16 bits;
-// sums in 32 bits.  The low-rank values between the two products go on as two 16-bit halves, of 16 (bf16) or
-// 22 (f16) bits together, so that only the output is rounded.
+// sums in 32 bits.  The low-rank values between the two products go on as two 16-bit parts, of 16 (bf16) or
+// 22 (f16, of the token's largest) bits together: they lose 2^-8 of half a step of a 16-bit output, or less.
+// Beside 32-bit outputs bf16 takes three, 24 bits together.
 #pragma once
+#include <type_traits>
+
 #include "lm_common.cuh"
 #include "lm_rows.cuh"
 
@@ -27,17 +30,21 @@ constexpr int kAdTokens = 64;  // tokens of a tile
 constexpr int kAdK = 256;      // channels of x of a stage, 8 segments of 32
 constexpr int kAdSeg = 32;
 
-template <int R>
+// 16-bit parts of a low-rank value.
+template <typename W, typename Y>
+constexpr int kAdParts = sizeof(Y) == 4 && std::is_same<W, __nv_bfloat16>::value ? 3 : 2;
+
+template <int R, int PARTS>
 struct AdapterSmem {
   static constexpr int kX = kAdTokens * kAdK, kA = R * kAdK * 2;
   static constexpr int kStage = kX + kA;
   static constexpr int kStages = R <= 32 ? 3 : 2;
-  // after the first product, in the ring's place: sums of the warps, of the CTA, and the two halves
+  // after the first product, in the ring's place: sums of the warps, of the CTA, and the parts
   static constexpr int kWarpSums = 8 * 16 * R * 4;
   static constexpr int kSums = kAdTokens * R * 4;
-  static constexpr int kRow = R * 2 + (R >= 64 ? 64 : 0);  // bytes of a row of a half, rows on other banks
-  static constexpr int kHalf = kAdTokens * kRow;
-  static constexpr int kAfter = kWarpSums + kSums + 2 * kHalf;
+  static constexpr int kRow = R * 2 + (R >= 64 ? 64 : 0);  // bytes of a row of a part, rows on other banks
+  static constexpr int kPart = kAdTokens * kRow;
+  static constexpr int kAfter = kWarpSums + kSums + PARTS * kPart;
   static constexpr int kBytes = kStages * kStage > kAfter ? kStages * kStage : kAfter;
 };
 
@@ -187,7 +194,8 @@ struct Eight {
 // Skipping the eights of ranks that an adapter lacks cost the full ones more (136 us) than it spares.
 template <typename W, typename Y, int R>
 __global__ void __launch_bounds__(kAdThreads, R <= 64 ? 2 : 1) adapters_kernel(const LmAdaptersArgs p) {
-  using Smem = AdapterSmem<R>;
+  constexpr int kParts = kAdParts<W, Y>;
+  using Smem = AdapterSmem<R, kParts>;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ int rows[kAdTokens];
   __shared__ float factor[kAdTokens];
@@ -331,7 +339,7 @@ __global__ void __launch_bounds__(kAdThreads, R <= 64 ? 2 : 1) adapters_kernel(c
     __syncthreads();  // the ring has been read
     float *warp_sums = reinterpret_cast<float *>(ring);
     float *sums = reinterpret_cast<float *>(ring + Smem::kWarpSums);
-    uint8_t *half = ring + Smem::kWarpSums + Smem::kSums;
+    uint8_t *parts = ring + Smem::kWarpSums + Smem::kSums;
 #pragma unroll
     for (int j = 0; j < R / 8; ++j)
 #pragma unroll
@@ -355,7 +363,7 @@ __global__ void __launch_bounds__(kAdThreads, R <= 64 ? 2 : 1) adapters_kernel(c
     else
       __syncthreads();
 
-    // ------------------------------------------- all of K, relative to the token's largest, in two halves
+    // ------------------------------------------- all of K, relative to the token's largest, in parts
     const uint32_t sums_at = smem_u32(sums + col);
     const float scale = p.scale[which];
     for (int r0 = 0; r0 < count; r0 += kAdThreads / kQuads) {  // whole warps: they exchange maxima
@@ -376,19 +384,20 @@ __global__ void __launch_bounds__(kAdThreads, R <= 64 ? 2 : 1) adapters_kernel(c
       for (int o = 1; o < kQuads; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       const int e = binade(top);
       const float down = pow2(-e);
-      float lo[4];
-      uint2 hw, lw;
+      uint2 words[kParts];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] *= down;
-        // an infinity is whole in the first half (infinity less itself would be NaN)
-        lo[i] = abs_bits(v[i]) == kInfBits ? 0.f : v[i] - to_f32(from_f32<W>(v[i]));
+      for (int i = 0; i < 4; ++i) v[i] *= down;
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) {
+        words[i] = make_uint2(pack2<W>(v[0], v[1]), pack2<W>(v[2], v[3]));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)  // an infinity is whole in the first part (infinity less itself would be NaN)
+          v[j] = abs_bits(v[j]) == kInfBits ? 0.f : v[j] - to_f32(from_f32<W>(v[j]));
       }
-      hw = make_uint2(pack2<W>(v[0], v[1]), pack2<W>(v[2], v[3]));
-      lw = make_uint2(pack2<W>(lo[0], lo[1]), pack2<W>(lo[2], lo[3]));
       if (r < count) {
-        *reinterpret_cast<uint2 *>(half + r * Smem::kRow + col * 2) = hw;
-        *reinterpret_cast<uint2 *>(half + Smem::kHalf + r * Smem::kRow + col * 2) = lw;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+          *reinterpret_cast<uint2 *>(parts + i * Smem::kPart + r * Smem::kRow + col * 2) = words[i];
         if (col == 0) factor[r] = p.xs[m0 + rows[r]] * pow2(e) * scale;
       }
     }
@@ -450,8 +459,8 @@ __global__ void __launch_bounds__(kAdThreads, R <= 64 ? 2 : 1) adapters_kernel(c
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
 #pragma unroll
-          for (int part_of = 0; part_of < 2; ++part_of) {
-            const uint8_t *from = half + part_of * Smem::kHalf + ((first16 + m) * 16 + g) * Smem::kRow +
+          for (int part_of = 0; part_of < kParts; ++part_of) {
+            const uint8_t *from = parts + part_of * Smem::kPart + ((first16 + m) * 16 + g) * Smem::kRow +
                                   4 * kWords * t;
 #pragma unroll
             for (int i = 0; i < kBlocks; ++i) {
@@ -493,7 +502,7 @@ __global__ void __launch_bounds__(kAdThreads, R <= 64 ? 2 : 1) adapters_kernel(c
       }
     }
     if (split > 1) cluster_wait();  // nobody leaves or writes its sums' place while they are being read
-    __syncthreads();                // rows, factors and halves are read
+    __syncthreads();                // rows, factors and parts are read
   }
 }
 

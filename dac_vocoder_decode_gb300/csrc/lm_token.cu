@@ -111,10 +111,10 @@ AdapterSetup g_adapters[kMaxDevices];
 template <typename W, typename Y>
 void allow_adapters(cudaError_t &e) {
   using namespace voc;
-  allow_smem(e, adapters_kernel<W, Y, 16>, AdapterSmem<16>::kBytes);
-  allow_smem(e, adapters_kernel<W, Y, 32>, AdapterSmem<32>::kBytes);
-  allow_smem(e, adapters_kernel<W, Y, 64>, AdapterSmem<64>::kBytes);
-  allow_smem(e, adapters_kernel<W, Y, 128>, AdapterSmem<128>::kBytes);
+  allow_smem(e, adapters_kernel<W, Y, 16>, AdapterSmem<16, kAdParts<W, Y>>::kBytes);
+  allow_smem(e, adapters_kernel<W, Y, 32>, AdapterSmem<32, kAdParts<W, Y>>::kBytes);
+  allow_smem(e, adapters_kernel<W, Y, 64>, AdapterSmem<64, kAdParts<W, Y>>::kBytes);
+  allow_smem(e, adapters_kernel<W, Y, 128>, AdapterSmem<128, kAdParts<W, Y>>::kBytes);
 }
 cudaError_t set_up_adapters() {
   int d = 0;
@@ -140,7 +140,7 @@ cudaError_t launch_adapters(int sms, const voc::LmAdaptersArgs &a, voc_stream_t 
   int split = 8;
   while (split > 1 && static_cast<long long>(tiles) * split > 2 * sms) split /= 2;
   return launch(voc::adapters_kernel<W, Y, R>, dim3(tiles, turns, split), dim3(voc::kAdThreads),
-                voc::AdapterSmem<R>::kBytes, split, stream, a);
+                voc::AdapterSmem<R, voc::kAdParts<W, Y>>::kBytes, split, stream, a);
 }
 template <typename W, typename Y>
 cudaError_t launch_adapters(int sms, const voc::LmAdaptersArgs &a, voc_stream_t stream) {

@@ -624,8 +624,9 @@ voc_status vocoder_lm_rotate(const void *q, long long ldq, long long hsq, int he
  * in the adapters' type or f32, out may be y (same stride) and otherwise does not overlap with it; scale
  * fp32 [pool]; ids int32 [M] in any order.  rank: a multiple of 8 up to 128; ranks int32 [pool] or NULL: the
  * rank of each adapter (0 to rank), what lies behind it in a and b is not used.  Row strides stay below
- * 2^31.  Sums are 32-bit; the low-rank values keep 16 (bf16) or 22 (f16) bits between the products, infinite
- * ones stay infinite.  A token with a NaN does not touch others; an infinity in b gives infinities or NaN. */
+ * 2^31.  Sums are 32-bit; between the products the low-rank values keep 16 bits (bf16), 24 (bf16 beside f32 outputs)
+ * or 22 of the token's largest (f16), infinite ones stay infinite.  A token with a NaN does not touch others; an
+ * infinity in b gives infinities or NaN. */
 voc_status vocoder_lm_adapters(const void *x8, long long ldx, const float *x_scale, const void *y,
                                long long ldy, int y_dtype, const void *a, long long lda, long long sa,
                                const void *b, long long ldb, long long sb, int dtype,

@@ -48,6 +48,23 @@ def test_adapters_infinite_low_rank_values_stay_infinite(M, N, K, rank, dtype, y
     c.check(again)
 
 
+@pytest.mark.parametrize("rank,M", [(8, 3), (32, 70), (64, 1), (128, 20)])
+def test_adapters_32_bit_outputs_of_bf16_keep_the_low_rank_bits(rank, M):
+    """A low-rank value of 21 bits, exact in every sum: what is lost is what the parts between the products drop.  Two
+    parts of 8 bits would drop the last, 2^-20; an accumulation may drop 2^-22 of the value."""
+    c = T.Adapters(M, 40, 48, rank, 1, "bf16", "f32", ids=torch.zeros(M, device="cuda"))
+    c.x8[:] = torch.ones(1, device="cuda").to(torch.float8_e4m3fn).view(torch.uint8)
+    c.x_scale.fill_(1)
+    c.y.zero_()
+    c.a.zero_()
+    c.b.zero_()
+    c.scale.fill_(1)
+    c.a[0, 5, 0], c.a[0, 5, 1], c.a[0, 5, 2] = 1, 2.0 ** -10, 2.0 ** -20
+    c.b[0, :, 5] = 1
+    got = c.run().double()
+    assert float((got - (1 + 2.0 ** -10 + 2.0 ** -20)).abs().max()) <= 2.0 ** -22
+
+
 # ------------------------------------------------------------------ log probabilities
 @pytest.mark.parametrize("temperature", [0.7, 1.0, 1.3, 4.0])
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
