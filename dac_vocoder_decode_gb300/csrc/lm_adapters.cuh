@@ -192,6 +192,10 @@ struct Eight {
 // of y start on 8 bytes); 15504 x 4096 -> 4096, rank 64: 124 us, 2.6 TB/s.  Bound by latencies: 16 warps an SM,
 // what 128 registers leave (3 CTAs of 80: prompts 76 us), issue in 44 % of the cycles, the matrix pipe a third.
 // Skipping the eights of ranks that an adapter lacks cost the full ones more (136 us) than it spares.
+// Other ranks and outputs, 15504 x 4096 -> 4096, bf16 / f16 pools: rank 16 81 / 77 us, with f32 y 114 / 109; rank 64
+// 124 / 121, with f32 y 159 / 146 (bf16 with two parts 148); rank 128 (one CTA an SM, 242 registers) 257 / 255, with f32
+// y 315 / 278 (280).  Ids in no order cost a turn of a tile for each adapter in it, 1024 -> 1536, rank 16: 15504
+// tokens of 8 adapters 93 us, 4000 of 64 214 us, 2000 of an adapter each 316 us.
 template <typename W, typename Y, int R>
 __global__ void __launch_bounds__(kAdThreads, R <= 64 ? 2 : 1) adapters_kernel(const LmAdaptersArgs p) {
   constexpr int kParts = kAdParts<W, Y>;

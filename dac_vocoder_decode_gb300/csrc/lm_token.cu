@@ -134,6 +134,10 @@ template <typename W, typename Y, int R>
 cudaError_t launch_adapters(int sms, const voc::LmAdaptersArgs &a, voc_stream_t stream) {
   const int tiles = (a.M + voc::kAdTokens - 1) / voc::kAdTokens;
   const int most = std::min({a.M, a.pool + 1, voc::kAdTokens});  // adapters of a tile
+  // Clusters of a tile, which share its adapters: some 512 of all tiles.  Measured, for 64 / 128 / 256 / 512 / 1024 /
+  // 2048 of them, 1024 -> 1536, rank 16: 4000 tokens of 64 adapters in no order 260 / 243 / 232 / 214 / 218 / 233
+  // us, 768 tokens 79 / 78 / 81 / 90 / 98 / 98, 15504 of 8 adapters 93 / 93 / 93 / 93 / 91 / 84; 15504 x 4096 ->
+  // 4096, rank 64, runs of 4: 159 / 159 / 158 / 124 / 124 / 124.
   const int turns = std::max(1, std::min(most, 512 / tiles));
   // CTAs of a cluster, as long as the tiles' clusters fill two CTAs an SM: measured, 1 / 2 / 4 CTAs, 15504 x 4096 x
   // 4096 of rank 64 136 / 143 / 150 us, 15423 x 1001 x 1540 of rank 32 54 / 62 / 72.
@@ -208,8 +212,14 @@ namespace {
 
 template <typename T, bool TOP>
 cudaError_t launch_logprobs(int sms, const voc::LmLogprobsArgs &a, voc_stream_t stream) {
-  // A warp has a row of up to 4096 values where there are rows enough (128 x 2048, 20 alternatives, with a warp a row
-  // 14.0 us, a CTA 4.7), a CTA another, several CTAs while there are SMs for them and a CTA keeps 4096 values.
+  // A warp has a row of up to 4096 values where there are more than four rows an SM, a CTA another, several CTAs while
+  // there are SMs for them and a CTA keeps 4096 values.  Measured, a warp / a CTA a row of 2048 bf16 values: without
+  // alternatives 300 rows 2.5 / 2.6 us, 640 2.8 / 3.3, 4800 6.4 / 16.4; with 5 5.0 / 4.4, 5.3 / 5.4, 10.6 / 29.1;
+  // with 20 8.4 / 4.9, 8.7 / 6.2, 1200 rows 9.6 / 10.5, 4800 17.2 / 33.8.  (So with 20 of 16-bit rows the border comes
+  // early: the CTA is ahead up to some seven rows an SM, at 640 x 4096 with 7.2 of 12.8 us.  f32 rows, 640 x 2048:
+  // 3.6 / 6.2, 7.1 / 9.6, 11.2 / 10.4.)  A CTA's loop has whole batches from 6144 values of 16 bits on and one vector
+  // at a time below: 4800 rows of 4097 / 5000 / 6200 / 8192 bf16 values 24 / 25 / 31 / 23 us (of 4096, a warp
+  // each, 9.2).
   if (a.vocab <= 4096 && a.rows > 4 * sms)
     return launch(voc::logprobs_kernel<T, 32, TOP>,
                   dim3(static_cast<unsigned>((a.rows + voc::kLpWarps - 1) / voc::kLpWarps)),

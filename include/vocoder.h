@@ -598,14 +598,15 @@ voc_status vocoder_lm_attention(const void *q, long long ldq, long long hsq, int
  * the product that makes them and the cache.  For each head
  *   n = x / sqrt(mean(x^2) + eps) * weight[i]   over its head_dim channels (weight NULL: n = x), then
  *   (n_a, n_b) -> (n_a cos - n_b sin, n_a sin + n_b cos)   for the channels a, b of pair p,
- * rounded once.  Pair p < pairs is channels (p, p + pairs) with neighbours = 0, (2p, 2p + 1) with 1; the
- * channels behind the first 2 * pairs are not turned.  The angle is positions[axis[p]][token] * turns[p] in
+ * in 32 bits with approximate sines, off by at most 2^-18 (|n_a| + |n_b|), and rounded to the type.  Pair
+ * p < pairs is channels (p, p + pairs) with neighbours = 0, (2p, 2p + 1) with 1; the channels behind the first
+ * 2 * pairs are not turned.  The angle is positions[axis[p]][token] * turns[p] in
  * units of 2^-64 of a turn, whole turns dropped: turns[p] = rate / (2 pi) * 2^64 modulo 2^64 for a rate in
  * radians, so that no position is too far for an exact angle.  positions int32 [axes][n_tokens] (1 to 16
- * axes, row stride ldp), axis int32 [pairs] or NULL (all pairs on axis 0); a pair with an axis outside 0..axes-1 is
- * not turned.  q or k may be absent (heads or kv_heads 0, NULL).  q_out and k_out may be the buffers of q
- * and k with their strides; otherwise they do not overlap with them.  head_dim a multiple of 16 up to 256,
- * pairs one of 8; heads, outputs, weights (of the same type) and turns 16-byte aligned, axis 8-byte, strides
+ * axes, row stride ldp), axis int32 [pairs] or NULL (all pairs on axis 0); a pair with an axis outside
+ * 0..axes-1 is at position 0, not turned.  q or k may be absent (heads or kv_heads 0, NULL).  q_out and k_out
+ * may be the buffers of q and k with their strides; otherwise they do not overlap with them.  head_dim a
+ * multiple of 16 up to 256, pairs one of 8; heads, outputs, weights (of the same type) and turns 16-byte aligned, axis 8-byte, strides
  * multiples of 8.
  * A head with a NaN or an infinity does not touch others. */
 voc_status vocoder_lm_rotate(const void *q, long long ldq, long long hsq, int heads, const void *k,
@@ -624,9 +625,9 @@ voc_status vocoder_lm_rotate(const void *q, long long ldq, long long hsq, int he
  * in the adapters' type or f32, out may be y (same stride) and otherwise does not overlap with it; scale
  * fp32 [pool]; ids int32 [M] in any order.  rank: a multiple of 8 up to 128; ranks int32 [pool] or NULL: the
  * rank of each adapter (0 to rank), what lies behind it in a and b is not used.  Row strides stay below
- * 2^31.  Sums are 32-bit; between the products the low-rank values keep 16 bits (bf16), 24 (bf16 beside f32 outputs)
- * or 22 of the token's largest (f16), infinite ones stay infinite.  A token with a NaN does not touch others; an
- * infinity in b gives infinities or NaN. */
+ * 2^31.  Sums are 32-bit; between the products the low-rank values keep 16 bits (bf16), 24 (bf16 beside f32
+ * outputs) or 22 of the token's largest (f16), infinite ones stay infinite.  A token with a NaN does not touch
+ * others; an infinity in b gives infinities or NaN. */
 voc_status vocoder_lm_adapters(const void *x8, long long ldx, const float *x_scale, const void *y,
                                long long ldy, int y_dtype, const void *a, long long lda, long long sa,
                                const void *b, long long ldb, long long sb, int dtype,
@@ -640,9 +641,10 @@ voc_status vocoder_lm_adapters(const void *x8, long long ldx, const float *x_sca
  *   entropy[row] = lse - sum_i exp(z_i - lse) z_i   (NULL: not wanted)
  *   top_tokens[row][0..top-1], top_logprobs: the top (0 to 32) largest logits in falling order, equal ones by
  *   their index (of a row with a NaN: some of its tokens).
- * -infinity closes a token; a row of nothing else has logprob and top_logprobs -infinity and entropy 0.  A
- * token outside 0..vocab-1 has -infinity.  A row with a NaN or +infinity gives NaN; other rows are not
- * touched by it. */
+ * Results that 32 bits hold do not overflow on the way, whatever finite values the row has; those beyond are
+ * -infinity.  -infinity closes a token; a row of nothing else has logprob and top_logprobs -infinity and
+ * entropy 0.  A token outside 0..vocab-1 has -infinity.  A row with a NaN or +infinity gives NaN; other rows
+ * are not touched by it. */
 voc_status vocoder_lm_logprobs(const void *logits, long long ldl, int dtype, long long rows, int vocab,
                                float temperature, const long long *tokens, float *logprob,
                                float *entropy, int top, float *top_logprobs, long long *top_tokens,
