@@ -30,10 +30,10 @@ constexpr int kRotThreads = 128;
 
 // cos and sin of position * turn.  The product modulo 2^64 is exact, so a far position loses nothing; the
 // upper half, a signed fraction of a turn good to 2^-33, goes through the hardware's approximations
-// (2^-20.5 absolute over [-pi, pi], beside 2^-21 of the 32-bit angle).  With the norm's sums a result is off by 2^-18 of
-// |a| + |b| at most before it is rounded: 2^-7 of half a step of f16 and 2^-9 of bf16's where it is of their
-// size, and more than half a step where a cos and b sin cancel or the larger one's sine is near 0 (a slow pair
-// near its start: a = 1, b = 0, angle 1e-4, 20 times half a step of f16).
+// (2^-20.5 absolute over [-pi, pi], beside 2^-21 of the 32-bit angle).  With the norm's sums a result is off by
+// 2^-18 of |a| + |b| at most before it is rounded: 2^-7 of half a step of f16 and 2^-9 of bf16's where it is of
+// their size, and more than half a step where a cos and b sin cancel or the larger one's sine is near 0 (a slow
+// pair near its start: a = 1, b = 0, angle 1e-4, 20 times half a step of f16).
 __device__ __forceinline__ void turn_cos_sin(int pos, unsigned long long turn, float &co, float &si) {
   const uint32_t lo = static_cast<uint32_t>(turn), hi = static_cast<uint32_t>(turn >> 32);
   const uint32_t upper = __umulhi(static_cast<uint32_t>(pos), lo) + static_cast<uint32_t>(pos) * hi -
@@ -48,8 +48,8 @@ __device__ __forceinline__ void turn_cos_sin(int pos, unsigned long long turn, f
 // 8 angles of a lane are the same for all heads of the token and are computed once.
 // Bound by DRAM and by its instructions: 15504 tokens x 20 heads of 128 bf16 channels (159 MB) 29.3 us, 5.4
 // TB/s; 4001 x 32 f16, three axes (66 MB) 13.9 us, 4.7 TB/s (11.4 us with the input in L2); 8 x 20 heads of 64
-// 1.9 us.  Next to 72 registers a thread (7 CTAs an SM) and the next head's loads ahead, 15504 tokens took with 80 registers and the weights unpacked
-// 31.7 us, 64 registers 30.2, without loads ahead 32.8.
+// 1.9 us.  Next to 72 registers a thread (7 CTAs an SM) and the next head's loads ahead, 15504 tokens took with 80
+// registers and the weights unpacked 31.7 us, 64 registers 30.2, without loads ahead 32.8.
 template <typename T, int L, bool NEAR>
 __global__ void __launch_bounds__(kRotThreads, 7) rotate_kernel(const LmRotateArgs p) {
   constexpr int kAtOnce = 32 / L;
